@@ -326,9 +326,8 @@ def _own(s, case, op):
     if op in ("prompt", "dense", "backward") and "t" not in s["ws"]:
         B, T = s["q"].shape[:2]
         H, d = case["H"], case["d"]
-        code, n = (api._abi.GDN_OP_LINEAR_ATTN_BACKWARD, 0) if op == "backward" else \
-            (api._abi.GDN_OP_LINEAR_ATTN, 0) if op == "dense" else (api._abi.GDN_OP_LINEAR_ATTN_VARLEN, len(s["lengths"]))
-        size = api.gdn_workspace_bytes(code, B, T, H, d, d, n)
+        size = api.gdn_linear_attn_workspace_bytes(B, T, H, case["Hk"], d, d, backward=op == "backward",
+                                                   num_seqs=len(s["lengths"]) if op == "prompt" else 0)
         s["ws"]["t"] = torch.empty(size, dtype=torch.uint8, device="cuda") if size else None
     if op == "prompt":
         return list(api.gdn_linear_attn_varlen(s["q"], s["k"], s["v"], s["log_decay"], s["cu_seqlens"], s0=s["s0"],
