@@ -8,7 +8,11 @@ from ._abi import GdnError  # noqa: F401
 
 __all__ = ["gdn_prefill", "gdn_prefill_varlen", "gdn_decode_step", "gdn_backward",
            "gdn_backward_noalloc", "gdn_backward_noalloc_max_workspace", "gdn_workspace_bytes",
-           "gdn_read_device_status", "GdnError"]
+           "gdn_read_device_status", "gdn_linear_attn", "gdn_linear_attn_varlen",
+           "gdn_linear_attn_decode_step", "gdn_linear_attn_backward",
+           "gdn_linear_attn_backward_varlen", "gdn_linear_attn_workspace_bytes", "gdn_rotary",
+           "gdn_rotary_inv_freq", "gdn_add_rmsnorm", "gdn_add_rmsnorm_fp8",
+           "gdn_add_rmsnorm_backward", "GdnError"]
 
 
 def __getattr__(name):

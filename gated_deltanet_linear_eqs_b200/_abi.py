@@ -32,6 +32,12 @@ GDN_OP_DECODE = 2
 GDN_OP_BACKWARD = 3
 GDN_OP_PREFILL_SEGMENTED = 4
 GDN_OP_QSA_SCORES = 5
+GDN_OP_ADD_RMSNORM_BACKWARD = 6
+
+GDN_ROTARY_PLAIN = 0
+GDN_ROTARY_LINEAR = 1
+GDN_ROTARY_NTK = 2
+GDN_ROTARY_YARN = 3
 
 _P = ctypes.c_void_p
 _F = ctypes.c_float
@@ -68,6 +74,20 @@ SIGNATURES = {
     "gdn_qsa_block_scores": (_I, [_P, _P, _P, _P, _I, _I, _I, _P, _P, _P, _I, _P, _S, _P]),
     "gdn_qsa_select_blocks": (_I, [_P, _I, _P, _I, _I, _I, _P, _P]),
     "gdn_qsa_indexer": (_I, [_P, _P, _P, _P, _I, _I, _I, _I, _P, _P, _P, _I, _P, _P, _S, _P]),
+    "gdn_linear_attn_workspace_bytes": (_I, [_I] * 8 + [ctypes.POINTER(_S)]),
+    "gdn_linear_attn": (_I, [_P] * 7 + [_I] * 7 + [_F, _P, _S, _P]),
+    "gdn_linear_attn_varlen": (_I, [_P] * 5 + [_I] + [_P] * 3 + [_I] * 6 + [_F, _P, _S, _P]),
+    "gdn_linear_attn_decode_step": (_I, [_P] * 6 + [_I] * 6 + [_F, _P]),
+    "gdn_linear_attn_backward": (_I, [_P] * 11 + [_I] * 7 + [_F, _P, _S, _P]),
+    "gdn_linear_attn_backward_varlen": (_I, [_P] * 5 + [_I] + [_P] * 7 + [_I] * 6 + [_F, _P, _S,
+                                                                                  _P]),
+    "gdn_rotary": (_I, [_P] * 6 + [_I] * 5 + [ctypes.c_int64] * 4 + [_I, _I, _F, _I, _P]),
+    "gdn_rotary_inv_freq": (_I, [_I, ctypes.c_double, _I, ctypes.c_double, ctypes.c_int64,
+                                 ctypes.c_double, ctypes.c_double, ctypes.POINTER(_F),
+                                 ctypes.POINTER(_F)]),
+    "gdn_add_rmsnorm": (_I, [_P] * 5 + [ctypes.c_int64, _I, _I, _F, _P]),
+    "gdn_add_rmsnorm_fp8": (_I, [_P] * 6 + [ctypes.c_int64, _I, _I, _I, _F, _P]),
+    "gdn_add_rmsnorm_backward": (_I, [_P] * 6 + [ctypes.c_int64, _I, _I, _F, _P, _S, _P]),
     "gdn_selftest_wait_timeout": (_I, [ctypes.c_uint64, _P]),
     "gdn_prefill_segmented": (_I, [_P] * 8 + [_I] * 6 + [_F, _I, _I, _P, _S, _P]),
 }

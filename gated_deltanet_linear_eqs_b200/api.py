@@ -7,6 +7,7 @@ runs in the library's kernels; a non-OK status raises ``GdnError``.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 
 import torch
@@ -578,3 +579,332 @@ def gdn_qsa_indexer(q, k, g, cu_seqlens, max_doc_len, budget=512, stream=None):
     """Both steps: returns (sel [T, budget] int32, k_hat, block_base, scores)."""
     k_hat, base, scores = gdn_qsa_block_scores(q, k, g, cu_seqlens, max_doc_len, stream)
     return gdn_qsa_select_blocks(scores, cu_seqlens, budget, stream=stream), k_hat, base, scores
+
+
+def _on(*tensors):
+    """The device that the tensors share, made current for the call (a launch goes to the current
+    device, whatever device its pointers are on)."""
+    dev = None
+    for t in tensors:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError("every tensor must be a CUDA tensor")
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise ValueError(f"tensors on {dev} and {t.device}: one device is needed")
+    return contextlib.nullcontext() if dev.index == torch.cuda.current_device() else \
+        torch.cuda.device(dev)
+
+
+def _dtype(t, name):
+    if t.dtype not in _DT:
+        raise ValueError(f"{name} must be bf16 or fp32")
+    return t.dtype
+
+
+def gdn_linear_attn_workspace_bytes(B, T, H, Hk, dk, dv, num_seqs=0, backward=False):
+    """Bytes of device scratch of gdn_linear_attn (num_seqs = 0) and gdn_linear_attn_varlen
+    (num_seqs documents, B = 1), or of their backward calls."""
+    n = ctypes.c_size_t(0)
+    _check(_lib().gdn_linear_attn_workspace_bytes(int(bool(backward)), B, T, H, Hk, dk, dv,
+                                                  num_seqs, ctypes.byref(n)),
+           "gdn_linear_attn_workspace_bytes")
+    return int(n.value)
+
+
+def _attn_workspace(q, Hk, dv, num_seqs, backward, ws):
+    B, T, H, dk = q.shape
+    n = gdn_linear_attn_workspace_bytes(B, T, H, Hk, dk, dv, num_seqs, backward)
+    if n == 0:
+        return None, 0
+    if ws is None:
+        ws = torch.empty(n, dtype=torch.uint8, device=q.device)
+    elif not ws.is_contiguous():
+        raise ValueError("ws must be contiguous")
+    return ws, ws.numel() * ws.element_size()
+
+
+def _need_attn(q, k, v, log_decay):
+    """Shapes of q [B,T,H,d], k and v [B,T,Hk,d], log_decay [H]; returns (dtype, B, T, H, Hk, d)."""
+    dt = _dtype(q, "q/k/v")
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError("q, k and v must be [B, T, heads, d] (packed: [1, T, heads, d] or "
+                         "[T, heads, d])")
+    B, T, H, d = q.shape
+    Hk = k.shape[2]
+    if Hk < 1 or H % Hk:
+        raise ValueError(f"{Hk} heads of k and v cannot be shared by {H} heads of q")
+    _need(q, "q", dt)
+    _need(k, "k", dt, (B, T, Hk, d))
+    _need(v, "v", dt, (B, T, Hk, d))
+    _need(log_decay, "log_decay", torch.float32, (H,))
+    return dt, B, T, H, Hk, d
+
+
+def gdn_linear_attn(q, k, v, log_decay, s0=None, scale=1.0, y=None, s_final=None, want_final=True,
+                    ws=None, stream=None):
+    """Decayed linear attention S_t = e^g S_{t-1} + k_t v_t^T, y_t = scale S_t^T q_t of dense
+    sequences: q [B,T,H,d], k and v [B,T,Hk,d] (bf16 or fp32; Hk divides H), log_decay [H] fp32
+    (g <= 0, a constant), s0 [B,H,d,d] fp32 or None.  Returns (y, s_final)."""
+    dt, B, T, H, Hk, d = _need_attn(q, k, v, log_decay)
+    _need(s0, "s0", torch.float32, (B, H, d, d), optional=True)
+    with _on(q, k, v, log_decay, s0, y, s_final, ws):
+        y = torch.empty_like(q) if y is None else y
+        _need(y, "y", dt, (B, T, H, d))
+        if s_final is None and want_final:
+            s_final = torch.empty((B, H, d, d), dtype=torch.float32, device=q.device)
+        _need(s_final, "s_final", torch.float32, (B, H, d, d), optional=True)
+        ws, wsb = _attn_workspace(q, Hk, d, 0, False, ws)
+        rc = _lib().gdn_linear_attn(_p(q), _p(k), _p(v), _p(log_decay), _p(s0), _p(y),
+                                    _p(s_final), B, T, H, Hk, d, d, _DT[dt], float(scale), _p(ws),
+                                    wsb, _stream(stream))
+    _check(rc, "gdn_linear_attn")
+    return y, s_final
+
+
+def gdn_linear_attn_varlen(q, k, v, log_decay, cu_seqlens, s0=None, scale=1.0, y=None,
+                           s_final=None, want_final=True, ws=None, stream=None):
+    """gdn_linear_attn of packed documents: q [1,T,H,d] or [T,H,d] (k, v likewise), cu_seqlens
+    int32 [N+1] on the device, s0 [N,H,d,d] fp32 or None.  Returns (y like q, s_final)."""
+    shape = q.shape
+    if q.dim() == 3:
+        q, k, v = (x.unsqueeze(0) for x in (q, k, v))
+    dt, B, T, H, Hk, d = _need_attn(q, k, v, log_decay)
+    if B != 1:
+        raise ValueError("packed documents are one stream: q must be [1, T, H, d] or [T, H, d]")
+    _need(cu_seqlens, "cu_seqlens", torch.int32)
+    N = cu_seqlens.numel() - 1
+    _need(s0, "s0", torch.float32, (N, H, d, d), optional=True)
+    with _on(q, k, v, log_decay, cu_seqlens, s0, y, s_final, ws):
+        y = torch.empty(shape, dtype=dt, device=q.device) if y is None else y
+        _need(y, "y", dt, shape)
+        if s_final is None and want_final:
+            s_final = torch.empty((N, H, d, d), dtype=torch.float32, device=q.device)
+        _need(s_final, "s_final", torch.float32, (N, H, d, d), optional=True)
+        ws, wsb = _attn_workspace(q, Hk, d, N, False, ws)
+        rc = _lib().gdn_linear_attn_varlen(_p(q), _p(k), _p(v), _p(log_decay), _p(cu_seqlens), N,
+                                           _p(s0), _p(y), _p(s_final), T, H, Hk, d, d, _DT[dt],
+                                           float(scale), _p(ws), wsb, _stream(stream))
+    _check(rc, "gdn_linear_attn_varlen")
+    return y, s_final
+
+
+def gdn_linear_attn_decode_step(q, k, v, log_decay, state, scale=1.0, y=None, stream=None):
+    """One token of N sequences: q [N,H,d], k and v [N,Hk,d], state [N,H,d,d] fp32 (updated in
+    place).  Returns y [N,H,d]."""
+    dt = _dtype(q, "q/k/v")
+    N, H, d = q.shape
+    Hk = k.shape[1]
+    _need(q, "q", dt)
+    _need(k, "k", dt, (N, Hk, d))
+    _need(v, "v", dt, (N, Hk, d))
+    _need(log_decay, "log_decay", torch.float32, (H,))
+    _need(state, "state", torch.float32, (N, H, d, d))
+    with _on(q, k, v, log_decay, state, y):
+        y = torch.empty_like(q) if y is None else y
+        _need(y, "y", dt, (N, H, d))
+        rc = _lib().gdn_linear_attn_decode_step(_p(q), _p(k), _p(v), _p(log_decay), _p(state),
+                                                _p(y), N, H, Hk, d, d, _DT[dt], float(scale),
+                                                _stream(stream))
+    _check(rc, "gdn_linear_attn_decode_step")
+    return y
+
+
+def gdn_linear_attn_backward(q, k, v, log_decay, dy, s0=None, ds_final=None, scale=1.0,
+                             want_ds0=True, ws=None, stream=None):
+    """Gradients of gdn_linear_attn's (y, s_final) given dy [B,T,H,d] and ds_final.  Returns dict
+    dq, dk, dv (like q, k, v) and ds0 [B,H,d,d] (None unless want_ds0)."""
+    dt, B, T, H, Hk, d = _need_attn(q, k, v, log_decay)
+    _need(dy, "dy", dt, q.shape)
+    _need(s0, "s0", torch.float32, (B, H, d, d), optional=True)
+    _need(ds_final, "ds_final", torch.float32, (B, H, d, d), optional=True)
+    with _on(q, k, v, log_decay, dy, s0, ds_final, ws):
+        out = dict(dq=torch.empty_like(q), dk=torch.empty_like(k), dv=torch.empty_like(v),
+                   ds0=torch.empty((B, H, d, d), dtype=torch.float32, device=q.device)
+                   if want_ds0 else None)
+        ws, wsb = _attn_workspace(q, Hk, d, 0, True, ws)
+        rc = _lib().gdn_linear_attn_backward(_p(q), _p(k), _p(v), _p(log_decay), _p(s0), _p(dy),
+                                             _p(ds_final), _p(out["dq"]), _p(out["dk"]),
+                                             _p(out["dv"]), _p(out["ds0"]), B, T, H, Hk, d, d,
+                                             _DT[dt], float(scale), _p(ws), wsb, _stream(stream))
+    _check(rc, "gdn_linear_attn_backward")
+    return out
+
+
+def gdn_linear_attn_backward_varlen(q, k, v, log_decay, cu_seqlens, dy, s0=None, ds_final=None,
+                                    scale=1.0, want_ds0=True, ws=None, stream=None):
+    """Gradients of gdn_linear_attn_varlen given dy (like q) and ds_final [N,H,d,d].  Returns
+    dict dq, dk, dv (like q, k, v) and ds0 [N,H,d,d] (None unless want_ds0)."""
+    if dy.shape != q.shape:
+        raise ValueError(f"dy must have shape {tuple(q.shape)}, got {tuple(dy.shape)}")
+    shapes = [x.shape for x in (q, k, v)]
+    if q.dim() == 3:
+        q, k, v, dy = (x.unsqueeze(0) for x in (q, k, v, dy))
+    dt, B, T, H, Hk, d = _need_attn(q, k, v, log_decay)
+    if B != 1:
+        raise ValueError("packed documents are one stream: q must be [1, T, H, d] or [T, H, d]")
+    _need(dy, "dy", dt, q.shape)
+    _need(cu_seqlens, "cu_seqlens", torch.int32)
+    N = cu_seqlens.numel() - 1
+    _need(s0, "s0", torch.float32, (N, H, d, d), optional=True)
+    _need(ds_final, "ds_final", torch.float32, (N, H, d, d), optional=True)
+    with _on(q, k, v, log_decay, cu_seqlens, dy, s0, ds_final, ws):
+        out = {n: torch.empty(s, dtype=dt, device=q.device)
+               for n, s in zip(("dq", "dk", "dv"), shapes)}
+        out["ds0"] = torch.empty((N, H, d, d), dtype=torch.float32, device=q.device) \
+            if want_ds0 else None
+        ws, wsb = _attn_workspace(q, Hk, d, N, True, ws)
+        rc = _lib().gdn_linear_attn_backward_varlen(
+            _p(q), _p(k), _p(v), _p(log_decay), _p(cu_seqlens), N, _p(s0), _p(dy), _p(ds_final),
+            _p(out["dq"]), _p(out["dk"]), _p(out["dv"]), _p(out["ds0"]), T, H, Hk, d, d, _DT[dt],
+            float(scale), _p(ws), wsb, _stream(stream))
+    _check(rc, "gdn_linear_attn_backward_varlen")
+    return out
+
+
+def _need_heads(t, name, dtype, T=None, d=None):
+    """A [T, heads, d] or [B, T, heads, d] tensor whose heads are contiguous and whose tokens are a
+    fixed distance apart; returns (tokens, heads, d, distance)."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() not in (3, 4):
+        raise ValueError(f"{name} must be [T, heads, d] or [B, T, heads, d]")
+    h, hd = t.shape[-2:]
+    n = t.numel() // max(1, h * hd)
+    ld = t.stride(-3) if t.shape[-3] > 1 else t.stride(0) if t.dim() == 4 and t.shape[0] > 1 \
+        else h * hd
+    inner = (hd <= 1 or t.stride(-1) == 1) and (h <= 1 or t.stride(-2) == hd)
+    outer = t.dim() == 3 or t.shape[0] <= 1 or t.stride(0) == t.shape[1] * ld
+    if n and not (inner and outer):
+        raise ValueError(f"{name}: a token's heads must be contiguous and its tokens evenly spaced")
+    if (T is not None and n != T) or (d is not None and hd != d):
+        raise ValueError(f"{name} must have {T} tokens of heads of {d}")
+    return n, h, hd, max(ld, h * hd)
+
+
+def gdn_rotary(q, k, positions, inv_freq, interleaved=False, inverse=False, scale=1.0, q_out=None,
+               k_out=None, stream=None):
+    """Rotary positions of q [T,Hq,d] and k [T,Hk,d] (or [B,T,..]; k may be None): the first
+    2 * len(inv_freq) values of each head, in pairs (i, i + r/2) or, interleaved, (2i, 2i+1), turn
+    by positions[t] * inv_freq[i] and are scaled; inverse turns back (the gradient).  q and k may be
+    views into one projection (contiguous heads, evenly spaced tokens).  positions int32 (one
+    per token), inv_freq fp32 on the device.  q_out / k_out may be q / k.  Returns (q_out, k_out)."""
+    dt = _dtype(q, "q/k")
+    T, Hq, d, ldq = _need_heads(q, "q", dt)
+    _need(positions, "positions", torch.int32)
+    if positions.numel() != T:
+        raise ValueError(f"positions must have {T} entries, got {positions.numel()}")
+    _need(inv_freq, "inv_freq", torch.float32)
+    if k is None:
+        Hk, ldk, k_out = 0, 0, None
+    else:
+        _, Hk, _, ldk = _need_heads(k, "k", dt, T, d)
+    with _on(q, k, positions, inv_freq, q_out, k_out):
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=dt, device=q.device)
+        if k is not None and k_out is None:
+            k_out = torch.empty(k.shape, dtype=dt, device=k.device)
+        _, ho, _, ldqo = _need_heads(q_out, "q_out", dt, T, d)
+        hko, ldko = (0, 0) if k is None else _need_heads(k_out, "k_out", dt, T, d)[1::2]
+        if ho != Hq or hko != Hk:
+            raise ValueError("q_out and k_out must have the heads of q and k")
+        rc = _lib().gdn_rotary(_p(q), _p(k), _p(q_out), _p(k_out), _p(positions), _p(inv_freq), T,
+                               Hq, Hk, d, 2 * inv_freq.numel(), ldq, ldk, ldqo, ldko,
+                               int(bool(interleaved)), int(bool(inverse)), float(scale), _DT[dt],
+                               _stream(stream))
+    _check(rc, "gdn_rotary")
+    return q_out, k_out
+
+
+_ROTARY = {"plain": _abi.GDN_ROTARY_PLAIN, "linear": _abi.GDN_ROTARY_LINEAR,
+           "ntk": _abi.GDN_ROTARY_NTK, "yarn": _abi.GDN_ROTARY_YARN}
+
+
+def gdn_rotary_inv_freq(rotary_dim, base=10000.0, scaling="plain", factor=1.0, original_context=0,
+                        beta_fast=32.0, beta_slow=1.0):
+    """The frequencies of gdn_rotary, [rotary_dim / 2] fp32 on the host, and its scale; scaling is
+    "plain", "linear", "ntk" or "yarn" (see include/gdn.h)."""
+    f = torch.empty(max(0, rotary_dim // 2), dtype=torch.float32)
+    s = ctypes.c_float(0)
+    if scaling not in _ROTARY:
+        raise ValueError(f"scaling must be one of {sorted(_ROTARY)}")
+    _check(_lib().gdn_rotary_inv_freq(int(rotary_dim), float(base), _ROTARY[scaling], float(factor),
+                                      int(original_context), float(beta_fast), float(beta_slow),
+                                      ctypes.cast(f.data_ptr(), ctypes.POINTER(ctypes.c_float)),
+                                      ctypes.byref(s)), "gdn_rotary_inv_freq")
+    return f, float(s.value)
+
+
+def _need_rows(x, w, name):
+    dt = _dtype(x, name)
+    C = x.shape[-1]
+    _need(x, name, dt)
+    _need(w, "w", torch.float32, (C,))
+    return dt, C, x.numel() // C if C else 0
+
+
+def gdn_add_rmsnorm(x, residual, w, eps=1e-6, o=None, h=None, stream=None):
+    """h = x + residual, o = (1 + w) h / sqrt(mean(h^2) + eps) over the last axis: x, residual
+    [..., C] (bf16 or fp32; residual None: h = x and is not written), w [C] fp32.  h may be x or
+    residual.  Returns (o, h)."""
+    dt, C, rows = _need_rows(x, w, "x")
+    _need(residual, "residual", dt, x.shape, optional=True)
+    with _on(x, residual, w, o, h):
+        o = torch.empty_like(x) if o is None else o
+        _need(o, "o", dt, x.shape)
+        if h is None and residual is not None:
+            h = torch.empty_like(x)
+        _need(h, "h", dt, x.shape, optional=True)
+        rc = _lib().gdn_add_rmsnorm(_p(x), _p(residual), _p(w), _p(o), _p(h), rows, C, _DT[dt],
+                                    float(eps), _stream(stream))
+    _check(rc, "gdn_add_rmsnorm")
+    return o, x if h is None else h
+
+
+def gdn_add_rmsnorm_fp8(x, residual, w, eps=1e-6, group=0, o=None, scales=None, h=None,
+                        stream=None):
+    """gdn_add_rmsnorm with an 8-bit o (float8_e4m3fn) and fp32 scales [..., C / group]: scale =
+    max|o| / 448 over each group of columns, group 0 (a whole row) or 128.  Returns (o, scales, h)."""
+    dt, C, rows = _need_rows(x, w, "x")
+    _need(residual, "residual", dt, x.shape, optional=True)
+    group = C if group == 0 else int(group)
+    if group < 1 or C % group:
+        raise ValueError(f"group {group} does not divide {C} columns")
+    with _on(x, residual, w, o, scales, h):
+        if o is None:
+            o = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device)
+        _need(o, "o", torch.float8_e4m3fn, x.shape)
+        sshape = (*x.shape[:-1], C // group)
+        if scales is None:
+            scales = torch.empty(sshape, dtype=torch.float32, device=x.device)
+        _need(scales, "scales", torch.float32, sshape)
+        if h is None and residual is not None:
+            h = torch.empty_like(x)
+        _need(h, "h", dt, x.shape, optional=True)
+        rc = _lib().gdn_add_rmsnorm_fp8(_p(x), _p(residual), _p(w), _p(o), _p(scales), _p(h), rows,
+                                        C, group, _DT[dt], float(eps), _stream(stream))
+    _check(rc, "gdn_add_rmsnorm_fp8")
+    return o, scales, x if h is None else h
+
+
+def gdn_add_rmsnorm_backward(h, w, d_o, d_h=None, eps=1e-6, ws=None, stream=None):
+    """Gradients of gdn_add_rmsnorm from the stored h, given d_o and d_h (the gradient of h itself;
+    None = 0).  Returns dict dx (like h: the gradient of x and of residual) and dw [C]."""
+    dt, C, rows = _need_rows(h, w, "h")
+    _need(d_o, "d_o", dt, h.shape)
+    _need(d_h, "d_h", dt, h.shape, optional=True)
+    with _on(h, w, d_o, d_h, ws):
+        out = dict(dx=torch.empty_like(h), dw=torch.empty_like(w))
+        wsb = 0
+        if rows:
+            ws, wsb = _workspace(_abi.GDN_OP_ADD_RMSNORM_BACKWARD, h.device, 1, rows, 1, C, C,
+                                 ws=ws)
+        rc = _lib().gdn_add_rmsnorm_backward(_p(h), _p(w), _p(d_o), _p(d_h), _p(out["dx"]),
+                                             _p(out["dw"]), rows, C, _DT[dt], float(eps), _p(ws),
+                                             wsb, _stream(stream))
+    _check(rc, "gdn_add_rmsnorm_backward")
+    return out

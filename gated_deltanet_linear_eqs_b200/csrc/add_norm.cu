@@ -1,0 +1,338 @@
+// add_norm.cu -- the root-mean-square norm with the residual's addition, and its reverse mode.
+//
+//     h = x + residual,   n = h / sqrt(mean(h^2) + eps),   o = (1 + w) n          per row of C values
+//
+// (the zero-centred gain of the gated RMSNorm).  The norm is taken of the 32-bit sum; h is its
+// rounding.  8-bit outputs: for every `group` columns scale = max|o| / 448 and o8 = e4m3(o / scale),
+// quantised from the 32-bit o.  Reverse mode, from the stored h:
+//     dn = d_o (1 + w),   dx = (dn - n mean(dn n)) / sqrt(mean(h^2) + eps) + d_h,   dw = sum_rows d_o n.
+//
+// Streaming passes bound by HBM.  A row is held in registers by one block (8 consecutive values a
+// thread and vector, at most kVec vectors a thread), so everything is read once; several rows' blocks
+// share an SM, and their loads hide each other's row sums.
+#include <cuda_fp8.h>
+#include <float.h>
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace gdn {
+
+namespace {
+
+constexpr int kVec = 4;             // vectors of 8 values a thread, at most
+constexpr int kNormBwdBlocks = 592; // blocks of the reverse mode (four an SM): rows of the dw partials
+
+__device__ __forceinline__ void ld8(const __nv_bfloat16* p, float* x) {
+    const uint4 u = __ldcs(reinterpret_cast<const uint4*>(p));
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        x[2 * j] = __uint_as_float(w[j] << 16);
+        x[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+    }
+}
+__device__ __forceinline__ void ld8(const float* p, float* x) {
+    const float4 a = __ldcs(reinterpret_cast<const float4*>(p)), b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
+    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+}
+__device__ __forceinline__ void st8(__nv_bfloat16* p, const float* x) {
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * j], x[2 * j + 1]);
+        w[j] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    __stcs(reinterpret_cast<uint4*>(p), make_uint4(w[0], w[1], w[2], w[3]));
+}
+__device__ __forceinline__ void st8(float* p, const float* x) {
+    __stcs(reinterpret_cast<float4*>(p), make_float4(x[0], x[1], x[2], x[3]));
+    __stcs(reinterpret_cast<float4*>(p) + 1, make_float4(x[4], x[5], x[6], x[7]));
+}
+// the gain's 8 values (read by every row: cached)
+__device__ __forceinline__ void ld_gain(const float* p, float* x) {
+    const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+    x[0] = 1.f + a.x; x[1] = 1.f + a.y; x[2] = 1.f + a.z; x[3] = 1.f + a.w;
+    x[4] = 1.f + b.x; x[5] = 1.f + b.y; x[6] = 1.f + b.z; x[7] = 1.f + b.w;
+}
+// the larger, NaN if either is
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+    return y;
+}
+__device__ __forceinline__ float warp_max_nan(float x) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x = max_nan(x, __shfl_xor_sync(0xffffffffu, x, o));
+    return x;
+}
+
+// Sums over the block's threads (in warp order, so the same on every run); `s` is used once a call.
+template <int N>
+__device__ __forceinline__ void block_sum(float (&x)[N], float (*s)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = warp_sum(x[i]);
+    const int nw = blockDim.x >> 5;
+    if (nw == 1) return;
+    if ((threadIdx.x & 31) == 0)
+#pragma unroll
+        for (int i = 0; i < N; ++i) s[threadIdx.x >> 5][i] = x[i];
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = 0.f;
+    for (int w = 0; w < nw; ++w)
+#pragma unroll
+        for (int i = 0; i < N; ++i) x[i] += s[w][i];
+}
+
+// OUT: 0 = o in T, 1 = e4m3 with a scale a row, 2 = e4m3 with a scale for every 128 columns
+template <typename T, int NV, int OUT>
+__global__ void __launch_bounds__(512)
+add_norm_kernel(const T* x, const T* res, const float* __restrict__ w, void* o,
+                T* h, float* scales, int C, float eps) {  // h and o may be x or res
+    __shared__ float s_sum[16][1], s_max[16];
+    const long long row = blockIdx.x;
+    const int nvec = C / 8, tid = threadIdx.x;
+    const T* xr = x + row * C;
+    float v[NV][8], ss[1] = {0.f};
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = tid + i * blockDim.x;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
+        if (c < nvec) ld8(xr + c * 8, v[i]);
+    }
+    if (res) {
+        const T* rr = res + row * C;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = tid + i * blockDim.x;
+            if (c < nvec) {
+                float r[8];
+                ld8(rr + c * 8, r);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[i][j] += r[j];
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = tid + i * blockDim.x;
+        if (h && c < nvec) st8(h + row * C + c * 8, v[i]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) ss[0] = fmaf(v[i][j], v[i][j], ss[0]);
+    }
+    block_sum(ss, s_sum);
+    const float r = 1.f / sqrtf(ss[0] / (float)C + eps);
+    float top = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = tid + i * blockDim.x;
+        if (c >= nvec) continue;
+        float g[8];
+        ld_gain(w + c * 8, g);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[i][j] *= r * g[j];
+        if constexpr (OUT == 0) {
+            st8(static_cast<T*>(o) + row * C + c * 8, v[i]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) top = max_nan(top, fabsf(v[i][j]));
+        }
+    }
+    if constexpr (OUT != 0) {
+        if constexpr (OUT == 1) {
+            top = warp_max_nan(top);
+            if ((tid & 31) == 0) s_max[tid >> 5] = top;
+            __syncthreads();
+            for (int k = 0; k < (int)(blockDim.x >> 5); ++k) top = max_nan(top, s_max[k]);
+            if (tid == 0) scales[row] = top / 448.f;
+        }
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = tid + i * blockDim.x;
+            if constexpr (OUT == 2) {  // 16 neighbouring threads hold a group
+                top = 0.f;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) top = max_nan(top, fabsf(v[i][j]));
+#pragma unroll
+                for (int q = 8; q > 0; q >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, q));
+                if (c < nvec && (tid & 15) == 0) scales[row * (C / 128) + c / 16] = top / 448.f;
+            }
+            if (c >= nvec) continue;
+            const float scale = top / 448.f;
+            // a group of zeros keeps the scale 0 and gives zeros; one whose scale has no finite
+            // reciprocal is divided
+            const float inv = scale >= FLT_MIN ? 1.f / scale : scale == 0.f ? 0.f : scale;
+            const bool tiny = scale > 0.f && scale < FLT_MIN;
+            uint32_t u[2];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float a = tiny ? v[i][2 * j] / scale : v[i][2 * j] * inv;
+                const float b = tiny ? v[i][2 * j + 1] / scale : v[i][2 * j + 1] * inv;
+                const uint32_t q = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+                u[j / 2] = j % 2 ? u[j / 2] | (q << 16) : q;
+            }
+            __stcs(reinterpret_cast<uint2*>(static_cast<uint8_t*>(o) + row * C + c * 8), make_uint2(u[0], u[1]));
+        }
+    }
+}
+
+// Rows blockIdx.x, + gridDim.x, ..: dx, and the block's part of dw in part[blockIdx.x][C].
+template <typename T, int NV>
+__global__ void __launch_bounds__(512)
+add_norm_bwd_kernel(const T* __restrict__ h, const float* __restrict__ w, const T* d_o,
+                    const T* d_h, T* dx, float* __restrict__ part, long long rows, int C,  // dx may be d_o or d_h
+                    float eps) {
+    __shared__ float s_sum[2][16][2];
+    const int nvec = C / 8, tid = threadIdx.x;
+    float acc[NV][8];
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[i][j] = 0.f;
+    int turn = 0;
+    for (long long row = blockIdx.x; row < rows; row += gridDim.x, turn ^= 1) {
+        float v[NV][8], g[NV][8], s[2] = {0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = tid + i * blockDim.x;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[i][j] = g[i][j] = 0.f;
+            if (c < nvec) {
+                ld8(h + row * C + c * 8, v[i]);
+                ld8(d_o + row * C + c * 8, g[i]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = tid + i * blockDim.x;
+            if (c >= nvec) continue;
+            float gain[8];
+            ld_gain(w + c * 8, gain);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                s[0] = fmaf(v[i][j], v[i][j], s[0]);
+                s[1] = fmaf(v[i][j], g[i][j] * gain[j], s[1]);
+            }
+        }
+        block_sum(s, s_sum[turn]);  // two buffers: the next row's writes need not wait for this one's reads
+        const float r = 1.f / sqrtf(s[0] / (float)C + eps);
+        const float m = s[1] * r / (float)C;  // mean(dn n)
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = tid + i * blockDim.x;
+            if (c >= nvec) continue;
+            float gain[8], e[8];
+            ld_gain(w + c * 8, gain);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) e[j] = 0.f;
+            if (d_h) ld8(d_h + row * C + c * 8, e);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float n = v[i][j] * r;
+                acc[i][j] = fmaf(g[i][j], n, acc[i][j]);
+                e[j] = fmaf(r, fmaf(-n, m, g[i][j] * gain[j]), e[j]);
+            }
+            st8(dx + row * C + c * 8, e);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = tid + i * blockDim.x;
+        if (c >= nvec) continue;
+        float4* q = reinterpret_cast<float4*>(part + (size_t)blockIdx.x * C + c * 8);
+        q[0] = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+        q[1] = make_float4(acc[i][4], acc[i][5], acc[i][6], acc[i][7]);
+    }
+}
+
+// dw[c] = sum of the partials, in the same order on every run: 8 warps share the blocks of 32 columns.
+__global__ void __launch_bounds__(256)
+add_norm_dw_kernel(const float* __restrict__ part, float* __restrict__ dw, int blocks, int C) {
+    __shared__ float s[8][33];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
+    float t = 0.f;
+    if (c < C)
+        for (int b = warp; b < blocks; b += 8) t += part[(size_t)b * C + c];
+    s[warp][lane] = t;
+    __syncthreads();
+    if (warp == 0 && c < C) {
+        for (int k = 1; k < 8; ++k) t += s[k][lane];
+        dw[c] = t;
+    }
+}
+
+// threads of a block for C columns with NV vectors a thread
+int threads_for(int C, int nv) {
+    const int per = (C / 8 + nv - 1) / nv;
+    return (per + 31) / 32 * 32;
+}
+// vectors a thread: as few as keep the block within a warp, else four (a row then needs few warps,
+// and more rows share an SM)
+int vectors_for(int C) { return C <= 256 ? 1 : C <= 512 ? 2 : kVec; }
+
+template <typename T, int NV>
+cudaError_t launch_fwd(const AddNormArgs& a, cudaStream_t st) {
+    const unsigned grid = (unsigned)a.rows;
+    const int threads = threads_for(a.C, NV);
+    const T *x = static_cast<const T*>(a.x), *res = static_cast<const T*>(a.residual);
+    T* h = static_cast<T*>(a.h);
+    if (a.scales == nullptr)
+        add_norm_kernel<T, NV, 0><<<grid, threads, 0, st>>>(x, res, a.w, a.o, h, nullptr, a.C, a.eps);
+    else if (a.group == a.C && a.C != 128)
+        add_norm_kernel<T, NV, 1><<<grid, threads, 0, st>>>(x, res, a.w, a.o, h, a.scales, a.C, a.eps);
+    else
+        add_norm_kernel<T, NV, 2><<<grid, threads, 0, st>>>(x, res, a.w, a.o, h, a.scales, a.C, a.eps);
+    return cudaGetLastError();
+}
+template <typename T>
+cudaError_t launch_fwd_type(const AddNormArgs& a, cudaStream_t st) {
+    switch (vectors_for(a.C)) {
+        case 1: return launch_fwd<T, 1>(a, st);
+        case 2: return launch_fwd<T, 2>(a, st);
+        default: return launch_fwd<T, kVec>(a, st);
+    }
+}
+
+unsigned bwd_blocks(long long rows) { return (unsigned)(rows < kNormBwdBlocks ? rows : kNormBwdBlocks); }
+
+template <typename T, int NV>
+cudaError_t launch_bwd(const AddNormArgs& a, cudaStream_t st) {
+    const unsigned grid = bwd_blocks(a.rows);
+    float* part = static_cast<float*>(a.ws);
+    add_norm_bwd_kernel<T, NV><<<grid, threads_for(a.C, NV), 0, st>>>(
+        static_cast<const T*>(a.h), a.w, static_cast<const T*>(a.d_o), static_cast<const T*>(a.d_h),
+        static_cast<T*>(a.dx), part, a.rows, a.C, a.eps);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    add_norm_dw_kernel<<<(unsigned)((a.C + 31) / 32), 256, 0, st>>>(part, a.dw, (int)grid, a.C);
+    return cudaGetLastError();
+}
+template <typename T>
+cudaError_t launch_bwd_type(const AddNormArgs& a, cudaStream_t st) {
+    switch (vectors_for(a.C)) {
+        case 1: return launch_bwd<T, 1>(a, st);
+        case 2: return launch_bwd<T, 2>(a, st);
+        default: return launch_bwd<T, kVec>(a, st);
+    }
+}
+
+}  // namespace
+
+size_t add_norm_workspace_bytes(long long rows, int C) {
+    return rows < 1 ? 0 : (size_t)bwd_blocks(rows) * C * sizeof(float);
+}
+
+cudaError_t launch_add_norm(const AddNormArgs& a, cudaStream_t st) {
+    if (a.rows == 0) return cudaSuccess;
+    return a.dtype == GDN_BF16 ? launch_fwd_type<__nv_bfloat16>(a, st) : launch_fwd_type<float>(a, st);
+}
+
+cudaError_t launch_add_norm_backward(const AddNormArgs& a, cudaStream_t st) {
+    if (a.rows == 0) return cudaMemsetAsync(a.dw, 0, sizeof(float) * a.C, st);
+    return a.dtype == GDN_BF16 ? launch_bwd_type<__nv_bfloat16>(a, st) : launch_bwd_type<float>(a, st);
+}
+
+}  // namespace gdn

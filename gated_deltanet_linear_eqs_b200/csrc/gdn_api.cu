@@ -2,6 +2,8 @@
 //
 // Every entry point validates its arguments on the host first and launches nothing when
 // they are rejected; see include/gdn.h for the contract of each call.
+#include <math.h>
+
 #include <mutex>
 
 #include "common.cuh"
@@ -114,6 +116,10 @@ int gdn_workspace_bytes(int op, int B, int T, int H, int dk, int dv, int num_seq
         case GDN_OP_QSA_SCORES:
             if (num_seqs < 1) return GDN_ERR_INVALID_ARG;
             *bytes = gdn::qsa_workspace_bytes(num_seqs);
+            return GDN_OK;
+        case GDN_OP_ADD_RMSNORM_BACKWARD:  // T rows of dk columns
+            if (dk < 8 || dk > 16384 || dk % 8 != 0) return GDN_ERR_UNSUPPORTED_SHAPE;
+            *bytes = gdn::add_norm_workspace_bytes(T, dk);
             return GDN_OK;
         default:
             return GDN_ERR_INVALID_ARG;
@@ -482,6 +488,233 @@ int gdn_prefill_segmented(const void* q, const void* k, const void* v, const flo
                        dtype, scale, l2norm_qk ? 1 : 0, dev.status, ws, ws_bytes};
     return map_cuda(gdn::launch_prefill_segmented(a, num_segments,
                                                   static_cast<cudaStream_t>(stream)));
+}
+
+// ---- the decayed linear attention ------------------------------------------------------------
+static int check_attn(const float* log_decay, int H, int Hk, int dk, int dv, int dtype) {
+    if (!ok_ptr(log_decay) || H < 1 || Hk < 1 || H % Hk != 0) return GDN_ERR_INVALID_ARG;
+    return check_dims(dk, dv, dtype);
+}
+// dense sequences: their tokens and the grid's (segment, head) count stay within 31 bits
+static bool ok_tokens(int num_seqs, int T, int H, bool packed) {
+    const long long tokens = packed ? T : (long long)num_seqs * T;
+    const long long segments = tokens / 64 + num_seqs;
+    return tokens < (1ll << 31) - 64 && segments * H < (1ll << 31);
+}
+
+int gdn_linear_attn_workspace_bytes(int backward, int B, int T, int H, int Hk, int dk, int dv, int num_seqs,
+                                    size_t* bytes) {
+    if (!bytes) return GDN_ERR_INVALID_ARG;
+    *bytes = 0;
+    if (B < 1 || T < 1 || H < 1 || Hk < 1 || H % Hk != 0 || num_seqs < 0) return GDN_ERR_INVALID_ARG;
+    if (num_seqs > 0 && B != 1) return GDN_ERR_INVALID_ARG;
+    if (int rc = check_dims(dk, dv, GDN_BF16)) return rc;
+    const bool packed = num_seqs > 0;
+    if (!ok_tokens(packed ? num_seqs : B, T, H, packed)) return GDN_ERR_INVALID_ARG;
+    *bytes = gdn::la_layout(backward != 0, packed ? num_seqs : B, T, H, Hk, dk, packed).total;
+    return GDN_OK;
+}
+
+// forward of B dense sequences (cu_seqlens == nullptr) or of num_seqs packed documents
+static int attn_forward(const void* q, const void* k, const void* v, const float* log_decay, bool packed,
+                        const int32_t* cu_seqlens, int num_seqs, const float* s0, void* y, float* s_final, int T, int H,
+                        int Hk, int dk, int dv, int dtype, float scale, void* ws, size_t ws_bytes, void* stream) {
+    if (!ok_ptr(q) || !ok_ptr(k) || !ok_ptr(v) || !ok_ptr(y) || !ok_opt_ptr(s0) || !ok_opt_ptr(s_final))
+        return GDN_ERR_INVALID_ARG;
+    if (num_seqs < 1 || T < 1 || (packed && cu_seqlens == nullptr)) return GDN_ERR_INVALID_ARG;
+    if (int rc = check_attn(log_decay, H, Hk, dk, dv, dtype)) return rc;
+    if (!ok_tokens(num_seqs, T, H, packed)) return GDN_ERR_INVALID_ARG;
+    const size_t need = gdn::la_layout(false, num_seqs, T, H, Hk, dk, packed).total;
+    if (need > 0 && (ws == nullptr || ws_bytes < need || !aligned16(ws))) return GDN_ERR_WORKSPACE;
+    DeviceInfo dev;
+    if (int rc = current_device_info(&dev)) return rc;
+    gdn::LaArgs a{};
+    a.q = q; a.k = k; a.v = v; a.log_decay = log_decay; a.cu_seqlens = cu_seqlens;
+    a.num_seqs = num_seqs; a.T = T; a.H = H; a.Hk = Hk; a.d = dk; a.dtype = dtype; a.scale = scale;
+    a.s0 = s0; a.y = y; a.s_final = s_final; a.ws = ws; a.status = dev.status;
+    return map_cuda(gdn::launch_linear_attn(a, static_cast<cudaStream_t>(stream)));
+}
+
+static int attn_backward(const void* q, const void* k, const void* v, const float* log_decay, bool packed,
+                         const int32_t* cu_seqlens, int num_seqs, const float* s0, const void* dy,
+                         const float* ds_final, void* dq, void* dk_out, void* dv_out, float* ds0, int T, int H, int Hk,
+                         int dk, int dv, int dtype, float scale, void* ws, size_t ws_bytes, void* stream) {
+    if (!ok_ptr(q) || !ok_ptr(k) || !ok_ptr(v) || !ok_ptr(dy) || !ok_ptr(dq) || !ok_ptr(dk_out) || !ok_ptr(dv_out) ||
+        !ok_opt_ptr(s0) || !ok_opt_ptr(ds_final) || !ok_opt_ptr(ds0))
+        return GDN_ERR_INVALID_ARG;
+    if (num_seqs < 1 || T < 1 || (packed && cu_seqlens == nullptr)) return GDN_ERR_INVALID_ARG;
+    if (int rc = check_attn(log_decay, H, Hk, dk, dv, dtype)) return rc;
+    if (!ok_tokens(num_seqs, T, H, packed)) return GDN_ERR_INVALID_ARG;
+    const size_t need = gdn::la_layout(true, num_seqs, T, H, Hk, dk, packed).total;
+    if (need > 0 && (ws == nullptr || ws_bytes < need || !aligned16(ws))) return GDN_ERR_WORKSPACE;
+    DeviceInfo dev;
+    if (int rc = current_device_info(&dev)) return rc;
+    gdn::LaArgs a{};
+    a.q = q; a.k = k; a.v = v; a.log_decay = log_decay; a.cu_seqlens = cu_seqlens;
+    a.num_seqs = num_seqs; a.T = T; a.H = H; a.Hk = Hk; a.d = dk; a.dtype = dtype; a.scale = scale;
+    a.s0 = s0; a.dy = dy; a.ds_final = ds_final; a.dq = dq; a.dk_out = dk_out; a.dv_out = dv_out; a.ds0 = ds0;
+    a.ws = ws; a.status = dev.status;
+    return map_cuda(gdn::launch_linear_attn(a, static_cast<cudaStream_t>(stream)));
+}
+
+int gdn_linear_attn(const void* q, const void* k, const void* v, const float* log_decay, const float* s0, void* y,
+                    float* s_final, int B, int T, int H, int Hk, int dk, int dv, int dtype, float scale, void* ws,
+                    size_t ws_bytes, void* stream) {
+    return attn_forward(q, k, v, log_decay, false, nullptr, B, s0, y, s_final, T, H, Hk, dk, dv, dtype, scale, ws,
+                        ws_bytes, stream);
+}
+
+int gdn_linear_attn_varlen(const void* q, const void* k, const void* v, const float* log_decay,
+                           const int32_t* cu_seqlens, int num_seqs, const float* s0, void* y, float* s_final, int T,
+                           int H, int Hk, int dk, int dv, int dtype, float scale, void* ws, size_t ws_bytes,
+                           void* stream) {
+    return attn_forward(q, k, v, log_decay, true, cu_seqlens, num_seqs, s0, y, s_final, T, H, Hk, dk, dv, dtype, scale,
+                        ws, ws_bytes, stream);
+}
+
+int gdn_linear_attn_backward(const void* q, const void* k, const void* v, const float* log_decay, const float* s0,
+                             const void* dy, const float* ds_final, void* dq, void* dk_out, void* dv_out, float* ds0,
+                             int B, int T, int H, int Hk, int dk, int dv, int dtype, float scale, void* ws,
+                             size_t ws_bytes, void* stream) {
+    return attn_backward(q, k, v, log_decay, false, nullptr, B, s0, dy, ds_final, dq, dk_out, dv_out, ds0, T, H, Hk,
+                         dk, dv, dtype, scale, ws, ws_bytes, stream);
+}
+
+int gdn_linear_attn_backward_varlen(const void* q, const void* k, const void* v, const float* log_decay,
+                                    const int32_t* cu_seqlens, int num_seqs, const float* s0, const void* dy,
+                                    const float* ds_final, void* dq, void* dk_out, void* dv_out, float* ds0, int T,
+                                    int H, int Hk, int dk, int dv, int dtype, float scale, void* ws, size_t ws_bytes,
+                                    void* stream) {
+    return attn_backward(q, k, v, log_decay, true, cu_seqlens, num_seqs, s0, dy, ds_final, dq, dk_out, dv_out, ds0, T,
+                         H, Hk, dk, dv, dtype, scale, ws, ws_bytes, stream);
+}
+
+int gdn_linear_attn_decode_step(const void* q, const void* k, const void* v, const float* log_decay, float* state,
+                                void* y, int N, int H, int Hk, int dk, int dv, int dtype, float scale, void* stream) {
+    if (!ok_ptr(q) || !ok_ptr(k) || !ok_ptr(v) || !ok_ptr(state) || !ok_ptr(y) || N < 1) return GDN_ERR_INVALID_ARG;
+    if (int rc = check_attn(log_decay, H, Hk, dk, dv, dtype)) return rc;
+    if ((long long)N * H >= (1ll << 31)) return GDN_ERR_INVALID_ARG;
+    DeviceInfo dev;
+    if (int rc = current_device_info(&dev)) return rc;
+    gdn::LaStepArgs a{q, k, v, log_decay, state, y, N, H, Hk, dk, dtype, scale};
+    return map_cuda(gdn::launch_linear_attn_step(a, static_cast<cudaStream_t>(stream)));
+}
+
+// ---- rotary positions ------------------------------------------------------------------------
+int gdn_rotary(const void* q, const void* k, void* q_out, void* k_out, const int32_t* positions,
+               const float* inv_freq, int T, int Hq, int Hk, int d, int rotary_dim, int64_t ld_q, int64_t ld_k,
+               int64_t ld_q_out, int64_t ld_k_out, int interleaved, int inverse, float scale, int dtype,
+               void* stream) {
+    if (T < 0 || Hq < 1 || Hk < 0 || dtype < GDN_BF16 || dtype > GDN_FP32) return GDN_ERR_INVALID_ARG;
+    if (d < 8 || d > 1024 || d % 8 != 0) return GDN_ERR_UNSUPPORTED_SHAPE;
+    if (rotary_dim < 2 || rotary_dim > d || rotary_dim % 2 != 0) return GDN_ERR_UNSUPPORTED_SHAPE;
+    const auto ok = [T, d](const void* x, const void* y, int heads, int64_t ldx, int64_t ldy) {
+        if (heads == 0) return true;
+        const int64_t row = (int64_t)heads * d;
+        if (ldx < row || ldy < row || ldx % 8 != 0 || ldy % 8 != 0) return false;
+        if (x == y && ldx != ldy) return false;  // in place: the same rows
+        return T == 0 ? aligned16(x) && aligned16(y) : ok_ptr(x) && ok_ptr(y);
+    };
+    if (!ok(q, q_out, Hq, ld_q, ld_q_out) || !ok(k, k_out, Hk, ld_k, ld_k_out)) return GDN_ERR_INVALID_ARG;
+    if (!ok_ptr(inv_freq) || (T > 0 && (positions == nullptr || (reinterpret_cast<uintptr_t>(positions) & 3u))))
+        return GDN_ERR_INVALID_ARG;
+    DeviceInfo dev;
+    if (int rc = current_device_info(&dev)) return rc;
+    gdn::RotaryArgs a{};
+    a.a[0] = {q, q_out, (long long)ld_q, (long long)ld_q_out, Hq};
+    a.a[1] = {k, k_out, (long long)ld_k, (long long)ld_k_out, Hk};
+    a.positions = positions; a.inv_freq = inv_freq; a.T = T; a.d = d; a.r = rotary_dim; a.dtype = dtype;
+    a.interleaved = interleaved != 0; a.inverse = inverse != 0; a.scale = scale;
+    return map_cuda(gdn::launch_rotary(a, static_cast<cudaStream_t>(stream)));
+}
+
+int gdn_rotary_inv_freq(int rotary_dim, double base, int scaling, double factor, int64_t original_context,
+                        double beta_fast, double beta_slow, float* inv_freq, float* scale) {
+    if (!inv_freq || !scale || rotary_dim < 2 || rotary_dim % 2 != 0 || !(base > 1.0) || base > 1e30)
+        return GDN_ERR_INVALID_ARG;
+    if (scaling < GDN_ROTARY_PLAIN || scaling > GDN_ROTARY_YARN) return GDN_ERR_INVALID_ARG;
+    if (scaling != GDN_ROTARY_PLAIN && !(factor >= 1.0 && factor < 1e9)) return GDN_ERR_INVALID_ARG;
+    if (scaling == GDN_ROTARY_YARN && (original_context < 1 || !(beta_slow > 0.0) || !(beta_fast > beta_slow)))
+        return GDN_ERR_INVALID_ARG;
+    const int half = rotary_dim / 2;
+    const double pi = 3.14159265358979323846;
+    // the base whose slowest pair turns `factor` times slower
+    if (scaling == GDN_ROTARY_NTK && rotary_dim > 2) base *= pow(factor, rotary_dim / (rotary_dim - 2.0));
+    // the (fractional) pair that makes `turns` turns within the original context
+    const auto pair_of = [&](double turns) {
+        return rotary_dim * log((double)original_context / (turns * 2.0 * pi)) / (2.0 * log(base));
+    };
+    double lo = 0.0, hi = 0.0;
+    if (scaling == GDN_ROTARY_YARN) {
+        lo = floor(pair_of(beta_fast));
+        hi = ceil(pair_of(beta_slow));
+        lo = lo < 0.0 ? 0.0 : lo;
+        hi = hi > rotary_dim - 1.0 ? rotary_dim - 1.0 : hi;
+        if (hi <= lo) hi = lo + 0.001;
+    }
+    for (int i = 0; i < half; ++i) {
+        double f = pow(base, -2.0 * i / rotary_dim);
+        if (scaling == GDN_ROTARY_LINEAR) f /= factor;
+        if (scaling == GDN_ROTARY_YARN) {
+            double slow = (i - lo) / (hi - lo);
+            slow = slow < 0.0 ? 0.0 : slow > 1.0 ? 1.0 : slow;
+            f = f / factor * slow + f * (1.0 - slow);
+        }
+        inv_freq[i] = (float)f;
+    }
+    *scale = scaling == GDN_ROTARY_YARN ? (float)(0.1 * log(factor) + 1.0) : 1.f;
+    return GDN_OK;
+}
+
+// ---- the norm with the residual's addition -----------------------------------------------------
+static int check_add_norm(const float* w, int64_t rows, int C, int dtype, float eps) {
+    if (rows < 0 || rows >= (1ll << 31) || !(eps >= 0.f) || !ok_ptr(w)) return GDN_ERR_INVALID_ARG;
+    if (dtype != GDN_BF16 && dtype != GDN_FP32) return GDN_ERR_INVALID_ARG;
+    if (C < 8 || C > 16384 || C % 8 != 0) return GDN_ERR_UNSUPPORTED_SHAPE;
+    return GDN_OK;
+}
+
+int gdn_add_rmsnorm(const void* x, const void* residual, const float* w, void* o, void* h, int64_t rows, int C,
+                    int dtype, float eps, void* stream) {
+    if (int rc = check_add_norm(w, rows, C, dtype, eps)) return rc;
+    const auto ok = [rows](const void* p) { return rows == 0 ? aligned16(p) : ok_ptr(p); };
+    if (!ok(x) || !ok(o) || !ok_opt_ptr(residual) || !ok_opt_ptr(h)) return GDN_ERR_INVALID_ARG;
+    DeviceInfo dev;
+    if (int rc = current_device_info(&dev)) return rc;
+    gdn::AddNormArgs a{};
+    a.x = x; a.residual = residual; a.w = w; a.o = o; a.h = h; a.rows = rows; a.C = C; a.dtype = dtype; a.eps = eps;
+    return map_cuda(gdn::launch_add_norm(a, static_cast<cudaStream_t>(stream)));
+}
+
+int gdn_add_rmsnorm_fp8(const void* x, const void* residual, const float* w, void* o8, float* scales, void* h,
+                        int64_t rows, int C, int group, int dtype, float eps, void* stream) {
+    if (int rc = check_add_norm(w, rows, C, dtype, eps)) return rc;
+    if (group != C && group != 128) return GDN_ERR_INVALID_ARG;
+    if (C % group != 0) return GDN_ERR_UNSUPPORTED_SHAPE;
+    const auto ok = [rows](const void* p) { return rows == 0 ? aligned16(p) : ok_ptr(p); };
+    if (!ok(x) || !ok(o8) || !ok(scales) || !ok_opt_ptr(residual) || !ok_opt_ptr(h)) return GDN_ERR_INVALID_ARG;
+    if (rows == 0) return GDN_OK;
+    DeviceInfo dev;
+    if (int rc = current_device_info(&dev)) return rc;
+    gdn::AddNormArgs a{};
+    a.x = x; a.residual = residual; a.w = w; a.o = o8; a.h = h; a.scales = scales; a.group = group; a.rows = rows;
+    a.C = C; a.dtype = dtype; a.eps = eps;
+    return map_cuda(gdn::launch_add_norm(a, static_cast<cudaStream_t>(stream)));
+}
+
+int gdn_add_rmsnorm_backward(const void* h, const float* w, const void* d_o, const void* d_h, void* dx, float* dw,
+                             int64_t rows, int C, int dtype, float eps, void* ws, size_t ws_bytes, void* stream) {
+    if (int rc = check_add_norm(w, rows, C, dtype, eps)) return rc;
+    const auto ok = [rows](const void* p) { return rows == 0 ? aligned16(p) : ok_ptr(p); };
+    if (!ok(h) || !ok(d_o) || !ok(dx) || !ok_opt_ptr(d_h) || !ok_ptr(dw)) return GDN_ERR_INVALID_ARG;
+    const size_t need = gdn::add_norm_workspace_bytes(rows, C);
+    if (need > 0 && (ws == nullptr || ws_bytes < need || !aligned16(ws))) return GDN_ERR_WORKSPACE;
+    DeviceInfo dev;
+    if (int rc = current_device_info(&dev)) return rc;
+    gdn::AddNormArgs a{};
+    a.h = const_cast<void*>(h); a.w = w; a.d_o = d_o; a.d_h = d_h; a.dx = dx; a.dw = dw; a.rows = rows; a.C = C;
+    a.dtype = dtype; a.eps = eps; a.ws = ws;
+    return map_cuda(gdn::launch_add_norm_backward(a, static_cast<cudaStream_t>(stream)));
 }
 
 int gdn_read_device_status(int reset, int* device_status) {

@@ -157,6 +157,79 @@ size_t qsa_workspace_bytes(int num_seqs);
 cudaError_t launch_qsa_scores(const QsaArgs& a, cudaStream_t st);
 cudaError_t launch_qsa_select(const QsaArgs& a, cudaStream_t st);
 
+// The decayed linear attention (linear_attn.cu): S_t = e^g S_{t-1} + k_t v_t^T,
+// y_t = scale S_t^T q_t, over packed documents (cu_seqlens) or dense sequences, and its gradients
+// (dy != nullptr).  k and v may have fewer heads than q (Hk divides H).
+struct LaArgs {
+    const void *q, *k, *v;       // [.., H, d], [.., Hk, d], [.., Hk, d]
+    const float* log_decay;      // [H]
+    const int32_t* cu_seqlens;   // device, [num_seqs + 1]; nullptr for the dense layout
+    int num_seqs, T;             // T: tokens per sequence (dense) or of the packed stream
+    int H, Hk, d, dtype;
+    float scale;
+    const float* s0;             // [num_seqs, H, d, d] or nullptr
+    void* y;                     // forward
+    float* s_final;              // forward, or nullptr
+    const void* dy;              // backward
+    const float* ds_final;       // backward, or nullptr
+    void *dq, *dk_out, *dv_out;  // backward
+    float* ds0;                  // backward, or nullptr
+    void* ws;
+    int* status;
+};
+struct LaLayout {
+    size_t off_local, off_dk, off_dv, total;
+};
+LaLayout la_layout(bool backward, int num_seqs, int T, int H, int Hk, int d, bool packed);
+cudaError_t launch_linear_attn(const LaArgs& a, cudaStream_t st);
+
+struct LaStepArgs {
+    const void *q, *k, *v;
+    const float* log_decay;
+    float* state;                // [N, H, d, d], updated in place
+    void* y;
+    int N, H, Hk, d, dtype;
+    float scale;
+};
+cudaError_t launch_linear_attn_step(const LaStepArgs& a, cudaStream_t st);
+
+// Rotary positions (rotary.cu): [T, heads, d] tensors whose heads are contiguous and whose tokens
+// are ld elements apart.
+struct RotaryTensor {
+    const void* x;
+    void* y;
+    long long ldx, ldy;
+    int heads;
+};
+struct RotaryArgs {
+    RotaryTensor a[2];           // q and k (heads = 0: absent)
+    const int32_t* positions;    // [T]
+    const float* inv_freq;       // [r / 2]
+    int T, d, r, dtype;
+    bool interleaved, inverse;
+    float scale;
+};
+cudaError_t launch_rotary(const RotaryArgs& a, cudaStream_t st);
+
+// The root-mean-square norm with the residual's addition (add_norm.cu) and its reverse mode.
+struct AddNormArgs {
+    const void *x, *residual;    // [rows, C]; residual may be nullptr
+    const float* w;              // [C], gain 1 + w
+    void *o, *h;                 // h may be nullptr
+    float* scales;               // 8-bit outputs: [rows, C / group]; nullptr: o in dtype
+    int group;
+    const void *d_o, *d_h;       // backward; d_h may be nullptr
+    void* dx;
+    float* dw;
+    long long rows;
+    int C, dtype;
+    float eps;
+    void* ws;
+};
+size_t add_norm_workspace_bytes(long long rows, int C);
+cudaError_t launch_add_norm(const AddNormArgs& a, cudaStream_t st);
+cudaError_t launch_add_norm_backward(const AddNormArgs& a, cudaStream_t st);
+
 // Size of the fixed device scratch array behind gdn_backward_noalloc.
 constexpr size_t kBackwardFixedScratchBytes = size_t(32) << 20;
 // Device address of that array on the current device (looked up on first use per device).

@@ -1,0 +1,438 @@
+// linear_attn.cu -- the decayed linear attention: segment plan, the passes of the prompt and of its
+// gradients, the fp32 kernel, the sum over shared heads and the one-token step.
+// The formulas and the roles that the kernels play are in linear_attn.cuh.
+#include "linear_attn.cuh"
+#include "sm100.cuh"
+
+namespace gdn {
+
+namespace {
+
+// ============================================================================ fp32 kernel
+// One CTA per (segment, head), 256 threads, 64-token chunks on the CUDA cores.  Q^T and K^T (token
+// fastest), V and the state live in shared memory; the products are register tiles: 4 x 4 for
+// the scores, 8 tokens x D/32 columns for the outputs, D/16 x D/16 for the state.
+template <int D>
+struct LaSimt {
+    static constexpr int C = kLaChunk;
+    static constexpr int LT = C + 4;                 // row stride of the transposed tiles
+    static constexpr int QT = 0;                     // [D][LT]
+    static constexpr int KT = QT + D * LT;           // [D][LT]
+    static constexpr int V = KT + D * LT;            // [C][D]
+    static constexpr int S = V + C * D;              // [D][D]
+    static constexpr int PT = S + D * D;             // [C][LT]: row j, column i
+    static constexpr int PW = PT + C * LT;           // e^{g n}, n = 0 .. C
+    static constexpr int BYTES = (PW + C + 4) * 4;
+};
+
+template <int D, typename T>
+__global__ void __launch_bounds__(256)
+la_simt_kernel(const LaParams p) {
+    using M = LaSimt<D>;
+    constexpr int C = M::C, LT = M::LT;
+    extern __shared__ float sm[];
+    float *qt = sm + M::QT, *kt = sm + M::KT, *vs = sm + M::V, *S = sm + M::S, *pt = sm + M::PT,
+          *pw = sm + M::PW;
+    const int h = blockIdx.x % p.H, tid = threadIdx.x;
+    LaSegment sg;
+    if (!la_find_segment(p, blockIdx.x / p.H, &sg)) return;
+    if (p.state_only && sg.idx == (p.reverse ? 0 : sg.count - 1)) return;  // nobody starts behind it
+    const float g = p.log_decay[h];
+    for (int n = tid; n <= C; n += 256) pw[n] = expf(g * (float)n);
+
+    // ---- the state this segment starts from
+    const size_t DD = (size_t)D * D;
+    if (p.state_only) {
+        for (int e = tid; e < D * D; e += 256) S[e] = 0.f;
+    } else {
+        const int behind = p.reverse ? sg.count - 1 - sg.idx : sg.idx;
+        const float* s_in = p.s_in ? p.s_in + ((size_t)sg.doc * p.H + h) * DD : nullptr;
+        const float2 full = la_power2(g, p.L);
+        const float2 last = la_power2(g, sg.doc_len - (sg.count - 1) * p.L);
+        for (int e = tid; e < D * D; e += 256) {
+            const int kk = p.state_t ? e % D : e / D, vv = p.state_t ? e / D : e % D;
+            float x = s_in ? s_in[e] : 0.f;
+            for (int b = 0; b < behind; ++b) {
+                const int r = p.reverse ? sg.count - 1 - b : b;
+                const float2 w = r == sg.count - 1 ? last : full;
+                x = fmaf(x, w.x, fmaf(x, w.y, p.local[((size_t)(sg.first_id + r) * p.H + h) * DD + e]));
+            }
+            S[kk * D + vv] = x;
+        }
+    }
+    __syncthreads();
+
+    const int nch = (sg.len + C - 1) / C;
+    const T* q = static_cast<const T*>(p.q);
+    const T* k = static_cast<const T*>(p.k);
+    const T* v = static_cast<const T*>(p.v);
+    const int Hq = p.H / p.qdiv, Hk = p.H / p.kdiv, Hv = p.H / p.vdiv;
+    const int warp = tid >> 5, lane = tid & 31;
+    for (int cc = 0; cc < nch; ++cc) {
+        const int c = p.reverse ? nch - 1 - cc : cc;
+        const int n = min(C, sg.len - c * C);
+        const size_t tok = (size_t)sg.t0 + (size_t)c * C;
+        // rows past the end of the document are zero
+        for (int e = tid; e < C * (D / 4); e += 256) {
+            const int i = e / (D / 4), x = (e % (D / 4)) * 4;
+            float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a, w = a;
+            if (i < n) {
+                a = load4(k + ((tok + i) * Hk + h / p.kdiv) * D + x);
+                b = load4(v + ((tok + i) * Hv + h / p.vdiv) * D + x);
+                if (!p.state_only) w = load4(q + ((tok + i) * Hq + h / p.qdiv) * D + x);
+            }
+            kt[(x + 0) * LT + i] = a.x; kt[(x + 1) * LT + i] = a.y;
+            kt[(x + 2) * LT + i] = a.z; kt[(x + 3) * LT + i] = a.w;
+            qt[(x + 0) * LT + i] = w.x; qt[(x + 1) * LT + i] = w.y;
+            qt[(x + 2) * LT + i] = w.z; qt[(x + 3) * LT + i] = w.w;
+            store4(vs + i * D + x, b);
+        }
+        __syncthreads();
+        if (!p.state_only) {
+            // ---- scores, their decay and mask: pt[j][i]
+            {
+                const int j0 = (tid / 16) * 4, i0 = (tid % 16) * 4;
+                float acc[4][4] = {};
+                for (int x = 0; x < D; ++x) {
+                    const float4 a = load4(kt + x * LT + j0), b = load4(qt + x * LT + i0);
+                    const float av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+#pragma unroll
+                        for (int s = 0; s < 4; ++s) acc[r][s] = fmaf(av[r], bv[s], acc[r][s]);
+                }
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    float o[4];
+#pragma unroll
+                    for (int s = 0; s < 4; ++s) {
+                        const int d = p.reverse ? j0 + r - (i0 + s) : i0 + s - (j0 + r);
+                        o[s] = d >= 0 ? acc[r][s] * pw[d] * p.p_scale : 0.f;
+                    }
+                    store4(pt + (j0 + r) * LT + i0, make_float4(o[0], o[1], o[2], o[3]));
+                }
+            }
+            __syncthreads();
+            // ---- outputs: rows 8 warp .. +7, columns lane * D/32 ..
+            constexpr int CPL = D / 32;
+            float acc[8][CPL] = {};
+            const int i0 = warp * 8, c0 = lane * CPL;
+            auto product = [&](const float* a, const float* b, int len) {
+                for (int x = 0; x < len; ++x) {
+                    const float4 u = load4(a + x * LT + i0), w = load4(a + x * LT + i0 + 4);
+                    const float av[8] = {u.x, u.y, u.z, u.w, w.x, w.y, w.z, w.w};
+                    float bv[CPL];
+#pragma unroll
+                    for (int s = 0; s < CPL; ++s) bv[s] = b[x * D + c0 + s];
+#pragma unroll
+                    for (int r = 0; r < 8; ++r)
+#pragma unroll
+                        for (int s = 0; s < CPL; ++s) acc[r][s] = fmaf(av[r], bv[s], acc[r][s]);
+                }
+            };
+            product(qt, S, D);
+#pragma unroll
+            for (int r = 0; r < 8; ++r) {
+                const int i = i0 + r;
+                const float f = i < n ? pw[p.reverse ? n - 1 - i : i + 1] * p.inter_scale : 0.f;
+#pragma unroll
+                for (int s = 0; s < CPL; ++s) acc[r][s] *= f;
+            }
+            product(pt, vs, C);
+#pragma unroll
+            for (int r = 0; r < 8; ++r) {
+                const int i = i0 + r;
+                if (i >= n) continue;
+                const size_t at = ((tok + i) * p.H + h) * D + c0;
+#pragma unroll
+                for (int s = 0; s < CPL; ++s) {
+                    if (p.out_f32)
+                        static_cast<float*>(p.out)[at + s] = acc[r][s];
+                    else
+                        static_cast<T*>(p.out)[at + s] = from_f32<T>(acc[r][s]);
+                }
+            }
+            __syncthreads();  // S is read above
+        }
+        // ---- state
+        {
+            constexpr int R = D / 16;
+            const int k0 = (tid / 16) * R, v0 = (tid % 16) * R;
+            const float2 dec = la_power2(g, n);
+            float acc[R][R] = {};
+            for (int j = 0; j < C; j += 4) {
+                float kw[R][4];
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    const float4 a = load4(kt + (k0 + r) * LT + j);
+                    kw[r][0] = a.x; kw[r][1] = a.y; kw[r][2] = a.z; kw[r][3] = a.w;
+                }
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    if (j + u >= n) break;
+                    const float f = pw[p.reverse ? j + u + 1 : n - 1 - j - u] * p.state_scale;
+                    float bv[R];
+#pragma unroll
+                    for (int s = 0; s < R; ++s) bv[s] = vs[(j + u) * D + v0 + s];
+#pragma unroll
+                    for (int r = 0; r < R; ++r) {
+                        const float a = kw[r][u] * f;
+#pragma unroll
+                        for (int s = 0; s < R; ++s) acc[r][s] = fmaf(a, bv[s], acc[r][s]);
+                    }
+                }
+            }
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+#pragma unroll
+                for (int s = 0; s < R; ++s) {
+                    float* x = S + (k0 + r) * D + v0 + s;
+                    *x = fmaf(*x, dec.x, fmaf(*x, dec.y, acc[r][s]));
+                }
+        }
+        __syncthreads();
+    }
+    // ---- what is behind the segment: its local state, or the document's last state
+    float* dst = nullptr;
+    if (p.state_only)
+        dst = p.local + ((size_t)(sg.first_id + sg.idx) * p.H + h) * DD;
+    else if (p.s_out && sg.idx == (p.reverse ? 0 : sg.count - 1))
+        dst = p.s_out + ((size_t)sg.doc * p.H + h) * DD;
+    if (dst)
+        for (int e = tid; e < D * D; e += 256)
+            dst[e] = p.state_t ? S[(e % D) * D + e / D] : S[e];
+}
+
+template <int D, typename T>
+cudaError_t launch_simt(const LaParams& p, int nseg, cudaStream_t st) {
+    cudaError_t e = cudaFuncSetAttribute(la_simt_kernel<D, T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         LaSimt<D>::BYTES);
+    if (e != cudaSuccess) return e;
+    la_simt_kernel<D, T><<<(unsigned)((size_t)nseg * p.H), 256, LaSimt<D>::BYTES, st>>>(p);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_pass(const LaParams& p, int nseg, int d, int dtype, cudaStream_t st) {
+    if (dtype == GDN_BF16)
+        return d == 128 ? launch_simt<128, __nv_bfloat16>(p, nseg, st) : launch_simt<64, __nv_bfloat16>(p, nseg, st);
+    return d == 128 ? launch_simt<128, float>(p, nseg, st) : launch_simt<64, float>(p, nseg, st);
+}
+
+// ============================================================================ shared heads
+// dk and dv of a k / v head shared by `group` heads: the sum of the heads' parts, in fp32 and in
+// head order.  part [T, H, d] fp32 -> out [T, H / group, d].
+template <typename T>
+__global__ void __launch_bounds__(256)
+la_group_sum_kernel(const float* __restrict__ part, T* __restrict__ out, size_t n4, int d4, int group) {
+    for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < n4; i += (size_t)gridDim.x * 256) {
+        const size_t head = i / d4;
+        const int x = (int)(i % d4);
+        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int m = 0; m < group; ++m) {
+            const float4 a = __ldcs(reinterpret_cast<const float4*>(part) + (head * group + m) * d4 + x);
+            s.x += a.x; s.y += a.y; s.z += a.z; s.w += a.w;
+        }
+        store4(out + i * 4, s);
+    }
+}
+
+cudaError_t launch_group_sum(const float* part, void* out, size_t tokens, int Hk, int d, int group, int dtype,
+                             cudaStream_t st) {
+    const size_t n4 = tokens * Hk * (d / 4);
+    const unsigned grid = (unsigned)min((n4 + 255) / 256, (size_t)148 * 16);
+    if (dtype == GDN_BF16)
+        la_group_sum_kernel<<<grid, 256, 0, st>>>(part, static_cast<__nv_bfloat16*>(out), n4, d / 4, group);
+    else
+        la_group_sum_kernel<<<grid, 256, 0, st>>>(part, static_cast<float*>(out), n4, d / 4, group);
+    return cudaGetLastError();
+}
+
+// ============================================================================ one token
+// S <- e^g S + k v^T, y = scale S^T q = scale (e^g S^T q + (k . q) v): one read and one write of the
+// fp32 state.  One CTA per (sequence, head, 64 columns), 128 threads; 16 lanes read 256
+// consecutive bytes of a row, every thread keeps its D/8 rows' values between the read and the
+// write.
+constexpr int kStepThreads = 128;
+constexpr int kStepCols = 64;
+
+template <int D, typename T>
+__global__ void __launch_bounds__(kStepThreads)
+la_step_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v,
+               const float* __restrict__ log_decay, float* __restrict__ state, T* __restrict__ y, int H,
+               int group, float scale) {
+    constexpr int LPR = kStepCols / 4, RPW = 32 / LPR, NW = kStepThreads / 32, ROWS = D / (RPW * NW);
+    __shared__ float s_k[D], s_q[D], s_kq;
+    __shared__ float4 s_red[NW][LPR];
+    const int nh = blockIdx.x, h = nh % H;
+    const size_t kv = (size_t)(nh / H) * (H / group) + h / group;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int cg = lane % LPR, rsub = lane / LPR;
+    const int col = blockIdx.y * kStepCols + cg * 4;
+    float* S = state + (size_t)nh * D * D;
+    float4 s[ROWS];
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i)
+        s[i] = __ldcs(reinterpret_cast<const float4*>(S + (size_t)((i * NW + warp) * RPW + rsub) * D + col));
+    const float a = expf(log_decay[h]);
+    const float4 vv = load4(v + kv * D + col);
+    if (warp == 0) {
+        float kq = 0.f;
+#pragma unroll
+        for (int j = 0; j < D / 32; ++j) {
+            const float x = to_f32(k[kv * D + lane + 32 * j]), z = to_f32(q[(size_t)nh * D + lane + 32 * j]);
+            s_k[lane + 32 * j] = x;
+            s_q[lane + 32 * j] = z;
+            kq = fmaf(x, z, kq);
+        }
+        kq = warp_sum(kq);
+        if (lane == 0) s_kq = kq;
+    }
+    __syncthreads();
+    float4 r = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+        const int row = (i * NW + warp) * RPW + rsub;
+        const float z = s_q[row], x = s_k[row];
+        r.x = fmaf(s[i].x, z, r.x); r.y = fmaf(s[i].y, z, r.y);
+        r.z = fmaf(s[i].z, z, r.z); r.w = fmaf(s[i].w, z, r.w);
+        s[i].x = fmaf(a, s[i].x, x * vv.x); s[i].y = fmaf(a, s[i].y, x * vv.y);
+        s[i].z = fmaf(a, s[i].z, x * vv.z); s[i].w = fmaf(a, s[i].w, x * vv.w);
+        __stcs(reinterpret_cast<float4*>(S + (size_t)row * D + col), s[i]);
+    }
+#pragma unroll
+    for (int o = LPR; o < 32; o <<= 1) {
+        r.x += __shfl_xor_sync(0xffffffffu, r.x, o); r.y += __shfl_xor_sync(0xffffffffu, r.y, o);
+        r.z += __shfl_xor_sync(0xffffffffu, r.z, o); r.w += __shfl_xor_sync(0xffffffffu, r.w, o);
+    }
+    if (rsub == 0) s_red[warp][cg] = r;
+    __syncthreads();
+    if (warp == 0 && rsub == 0) {
+#pragma unroll
+        for (int w = 1; w < NW; ++w) {
+            const float4 b = s_red[w][cg];
+            r.x += b.x; r.y += b.y; r.z += b.z; r.w += b.w;
+        }
+        const float kq = s_kq;
+        store4(y + (size_t)nh * D + col,
+               make_float4(scale * fmaf(a, r.x, kq * vv.x), scale * fmaf(a, r.y, kq * vv.y),
+                           scale * fmaf(a, r.z, kq * vv.z), scale * fmaf(a, r.w, kq * vv.w)));
+    }
+}
+
+template <int D, typename T>
+cudaError_t launch_step(const LaStepArgs& a, cudaStream_t st) {
+    la_step_kernel<D, T><<<dim3((unsigned)(a.N * a.H), D / kStepCols), kStepThreads, 0, st>>>(
+        static_cast<const T*>(a.q), static_cast<const T*>(a.k), static_cast<const T*>(a.v), a.log_decay, a.state,
+        static_cast<T*>(a.y), a.H, a.H / a.Hk, a.scale);
+    return cudaGetLastError();
+}
+
+// ============================================================================ plan
+// One segment per document where the documents alone give every SM work; otherwise segments long
+// enough for their start states (d x d fp32 each) to stay a small part of their tokens.
+LaPlan make_plan(int num_seqs, int T, int H, bool packed) {
+    const long long tokens = packed ? T : (long long)num_seqs * T;
+    LaPlan pl;
+    pl.L = (T + kLaChunk - 1) / kLaChunk * kLaChunk;
+    if ((long long)num_seqs * H < 148) {
+        const long long want = (tokens * H + 147) / 148;
+        long long L = (want + kLaChunk - 1) / kLaChunk * kLaChunk;
+        if (L < 512) L = 512;
+        if (L < pl.L) pl.L = (int)L;
+    }
+    pl.split = pl.L < T;
+    pl.nseg = packed ? T / pl.L + num_seqs : num_seqs * ((T + pl.L - 1) / pl.L);
+    return pl;
+}
+
+size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+
+}  // namespace
+
+LaLayout la_layout(bool backward, int num_seqs, int T, int H, int Hk, int d, bool packed) {
+    const LaPlan pl = make_plan(num_seqs, T, H, packed);
+    const size_t tokens = packed ? (size_t)T : (size_t)num_seqs * T;
+    LaLayout l;
+    l.off_local = 0;
+    l.off_dk = pl.split ? up256((size_t)pl.nseg * H * d * d * 4) : 0;
+    l.off_dv = l.off_dk;
+    l.total = l.off_dk;
+    if (backward && Hk < H) {
+        l.off_dv = l.off_dk + up256(tokens * H * d * 4);
+        l.total = l.off_dv + up256(tokens * H * d * 4);
+    }
+    return l;
+}
+
+cudaError_t launch_linear_attn(const LaArgs& a, cudaStream_t st) {
+    const bool packed = a.cu_seqlens != nullptr;
+    const LaPlan pl = make_plan(a.num_seqs, a.T, a.H, packed);
+    const LaLayout lay = la_layout(a.dy != nullptr, a.num_seqs, a.T, a.H, a.Hk, a.d, packed);
+    char* ws = static_cast<char*>(a.ws);
+    const int group = a.H / a.Hk;
+    LaParams p{};
+    p.log_decay = a.log_decay;
+    p.local = pl.split ? reinterpret_cast<float*>(ws + lay.off_local) : nullptr;
+    p.cu = a.cu_seqlens;
+    p.num_seqs = a.num_seqs;
+    p.T = a.T;
+    p.H = a.H;
+    p.L = pl.L;
+    p.status = a.status;
+    cudaError_t e;
+    const auto roles = [&](const void* q, int qdiv, const void* k, int kdiv, const void* v, int vdiv) {
+        p.q = q; p.qdiv = qdiv; p.k = k; p.kdiv = kdiv; p.v = v; p.vdiv = vdiv;
+    };
+    const auto run = [&](bool state_only) {
+        p.state_only = state_only;
+        return launch_pass(p, pl.nseg, a.d, a.dtype, st);
+    };
+    // forward in time: the local states of k, v, then y from s0 (or dq from s0 and dy)
+    p.p_scale = p.inter_scale = a.scale;
+    p.state_scale = 1.f;
+    roles(a.q, 1, a.k, group, a.v, group);
+    if (pl.split && (e = run(true)) != cudaSuccess) return e;
+    p.s_in = a.s0;
+    if (a.dy == nullptr) {
+        p.out = a.y;
+        p.s_out = a.s_final;
+        return run(false);
+    }
+    roles(a.dy, 1, a.v, group, a.k, group);
+    p.out = a.dq;
+    p.state_t = 1;
+    if ((e = run(false)) != cudaSuccess) return e;
+    // reversed: the local states of q, dy, then dv and ds0, then dk
+    p.reverse = 1;
+    p.inter_scale = 1.f;
+    p.state_scale = a.scale;
+    p.state_t = 0;
+    roles(a.k, group, a.q, 1, a.dy, 1);
+    if (pl.split && (e = run(true)) != cudaSuccess) return e;
+    float* part_k = reinterpret_cast<float*>(ws + lay.off_dk);
+    float* part_v = reinterpret_cast<float*>(ws + lay.off_dv);
+    p.out_f32 = group > 1;
+    p.s_in = a.ds_final;
+    p.s_out = a.ds0;
+    p.out = group > 1 ? part_v : a.dv_out;
+    if ((e = run(false)) != cudaSuccess) return e;
+    roles(a.v, group, a.dy, 1, a.q, 1);
+    p.out = group > 1 ? part_k : a.dk_out;
+    p.s_out = nullptr;
+    p.state_t = 1;
+    if ((e = run(false)) != cudaSuccess) return e;
+    if (group > 1) {
+        const size_t tokens = packed ? (size_t)a.T : (size_t)a.num_seqs * a.T;
+        if ((e = launch_group_sum(part_k, a.dk_out, tokens, a.Hk, a.d, group, a.dtype, st)) != cudaSuccess) return e;
+        return launch_group_sum(part_v, a.dv_out, tokens, a.Hk, a.d, group, a.dtype, st);
+    }
+    return cudaSuccess;
+}
+
+cudaError_t launch_linear_attn_step(const LaStepArgs& a, cudaStream_t st) {
+    if (a.dtype == GDN_BF16)
+        return a.d == 128 ? launch_step<128, __nv_bfloat16>(a, st) : launch_step<64, __nv_bfloat16>(a, st);
+    return a.d == 128 ? launch_step<128, float>(a, st) : launch_step<64, float>(a, st);
+}
+
+}  // namespace gdn

@@ -65,7 +65,8 @@ typedef enum {
     GDN_OP_DECODE = 2,
     GDN_OP_BACKWARD = 3,
     GDN_OP_PREFILL_SEGMENTED = 4, /* num_seqs carries the number of segments */
-    GDN_OP_QSA_SCORES = 5         /* gdn_qsa_block_scores: only num_seqs matters */
+    GDN_OP_QSA_SCORES = 5,        /* gdn_qsa_block_scores: only num_seqs matters */
+    GDN_OP_ADD_RMSNORM_BACKWARD = 6 /* gdn_add_rmsnorm_backward: T rows of dk columns */
 } gdn_op;
 
 /* Static description of a status code.  Never NULL. */
@@ -382,6 +383,133 @@ int gdn_qsa_indexer(const void* q, const void* k, const float* g, const int32_t*
                     int num_seqs, int T, int max_doc_len, int budget, void* k_hat,
                     int32_t* block_base, float* scores, int ld, int32_t* sel, void* ws,
                     size_t ws_bytes, void* stream);
+
+/*
+ * Decayed linear attention: per sequence and head, with one fixed decay e^g per head (g <= 0) and
+ * a state S in R^{dk x dv},
+ *
+ *     S_t = e^g S_{t-1} + k_t v_t^T          y_t = scale * S_t^T q_t
+ *
+ * the recurrence above without the delta rule's correction (beta's e_t is v_t) and with a decay that
+ * depends on the head alone.
+ *   q, y [.., H, dk]; k, v [.., Hk, dk] in dtype (bf16 or fp32): Hk divides H, and heads
+ *   h = m (H / Hk) .. (m + 1) (H / Hk) - 1 share k and v head m.  dk == dv in {64, 128}.
+ *   log_decay [H] fp32: g per head, finite and <= 0 (0: no decay), a constant: no gradient is formed.
+ *   s0, s_final, ds_final, ds0: [B or num_seqs, H, dk, dv] fp32, with H states (the heads' decays
+ *   differ even where k and v are shared).  s0 / ds_final NULL = 0; s_final / ds0 NULL = not written.
+ *   Inputs must be finite: a value that is not makes its whole 64-token chunk, and what follows in
+ *   its document and head, non-finite.  Other documents and heads are not touched by it.
+ *
+ * gdn_linear_attn -- B dense sequences of T tokens.  gdn_linear_attn_varlen -- one packed stream
+ * ([T, H, dk] tensors) of num_seqs documents; cu_seqlens as in gdn_prefill_varlen (empty documents
+ * give s_final = s0).  Computed in 64-token chunks; long sequences are cut into segments that run
+ * side by side, each from a start state that a first pass prepares in the workspace.
+ * For bf16 the scores and the chunk-start states are rounded to bf16 as operands of the tensor cores;
+ * sums and states are fp32 (s_final and ds0 are exact to fp32 rounding), fp32 inputs are computed in
+ * fp32 throughout.
+ * gdn_linear_attn_decode_step -- one token for each of N sequences: q, y [N, H, dk], k, v
+ * [N, Hk, dk]; state [N, H, dk, dv] fp32 is read once and updated in place.
+ * gdn_linear_attn_backward, _varlen -- gradients of L(y, s_final) given dy and ds_final: dq like q,
+ * dk_out and dv_out like k and v (summed over the heads that share them, in fp32 and in a fixed
+ * order), ds0 fp32.  dy must not alias an output.
+ * gdn_linear_attn_workspace_bytes -- device scratch of the four prompt calls (backward != 0 for the
+ * gradients); num_seqs = 0: B dense sequences of T tokens; num_seqs >= 1: packed (B = 1).
+ * Two calls that may overlap on the GPU need a workspace each.
+ * Errors: GDN_ERR_INVALID_ARG (null or misaligned pointer, bad size, Hk not a divisor of H, 2^31 or
+ * more tokens or (segment, head) pairs), GDN_ERR_UNSUPPORTED_SHAPE, GDN_ERR_WORKSPACE.
+ */
+int gdn_linear_attn_workspace_bytes(int backward, int B, int T, int H, int Hk, int dk, int dv,
+                                    int num_seqs, size_t* bytes);
+int gdn_linear_attn(const void* q, const void* k, const void* v, const float* log_decay,
+                    const float* s0, void* y, float* s_final, int B, int T, int H, int Hk, int dk,
+                    int dv, int dtype, float scale, void* ws, size_t ws_bytes, void* stream);
+int gdn_linear_attn_varlen(const void* q, const void* k, const void* v, const float* log_decay,
+                           const int32_t* cu_seqlens, int num_seqs, const float* s0, void* y,
+                           float* s_final, int T, int H, int Hk, int dk, int dv, int dtype,
+                           float scale, void* ws, size_t ws_bytes, void* stream);
+int gdn_linear_attn_decode_step(const void* q, const void* k, const void* v,
+                                const float* log_decay, float* state, void* y, int N, int H,
+                                int Hk, int dk, int dv, int dtype, float scale, void* stream);
+int gdn_linear_attn_backward(const void* q, const void* k, const void* v, const float* log_decay,
+                             const float* s0, const void* dy, const float* ds_final, void* dq,
+                             void* dk_out, void* dv_out, float* ds0, int B, int T, int H, int Hk,
+                             int dk, int dv, int dtype, float scale, void* ws, size_t ws_bytes,
+                             void* stream);
+int gdn_linear_attn_backward_varlen(const void* q, const void* k, const void* v,
+                                    const float* log_decay, const int32_t* cu_seqlens,
+                                    int num_seqs, const float* s0, const void* dy,
+                                    const float* ds_final, void* dq, void* dk_out, void* dv_out,
+                                    float* ds0, int T, int H, int Hk, int dk, int dv, int dtype,
+                                    float scale, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * gdn_rotary -- rotary positions of q and (Hk > 0) k, ahead of an attention or of the calls above.
+ * The first rotary_dim (even) values of every head form pairs (a, b): elements (i, i + rotary_dim / 2),
+ * or (2 i, 2 i + 1) when interleaved != 0.  Pair i of the token at position p turns by p * inv_freq[i]:
+ *
+ *     (a, b) -> scale * (a cos - b sin, b cos + a sin)
+ *
+ * and by minus that when inverse != 0 (with the same scale: the gradient of the forward call).  The
+ * other values are copied.  The angle is formed in 64 bits.
+ *   q [T, Hq, d], k [T, Hk, d] in dtype; a token's heads are contiguous and tokens are ld_* elements
+ *   apart (ld >= heads * d and a multiple of 8), so that q and k may be parts of one projection's
+ *   output.  q_out / k_out likewise; each may be its input (same pointer, same ld: in place), and
+ *   must not overlap it otherwise.
+ *   positions [T] int32 and inv_freq [rotary_dim / 2] fp32 on the device.  Hk = 0: k and k_out
+ *   may be NULL.  T >= 0.
+ * Errors: GDN_ERR_INVALID_ARG (null or misaligned pointer, bad size or ld), GDN_ERR_UNSUPPORTED_SHAPE
+ * (d not a multiple of 8 in 8..1024, rotary_dim odd or outside 2..d).  No workspace; one launch.
+ *
+ * gdn_rotary_inv_freq -- the frequencies, on the HOST: base^(-2 i / rotary_dim), i < rotary_dim / 2, for
+ *   GDN_ROTARY_PLAIN; divided by factor for GDN_ROTARY_LINEAR; of the base
+ *   base * factor^(rotary_dim / (rotary_dim - 2)) for GDN_ROTARY_NTK; and for GDN_ROTARY_YARN divided by
+ *   factor for pairs that make fewer than beta_slow turns within original_context positions, kept
+ *   for those that make more than beta_fast, with a linear ramp over the pair index between
+ *   (whole pair indices).  *scale receives 0.1 ln(factor) + 1 for YARN and 1 otherwise: gdn_rotary's scale.
+ */
+typedef enum {
+    GDN_ROTARY_PLAIN = 0,
+    GDN_ROTARY_LINEAR = 1,
+    GDN_ROTARY_NTK = 2,
+    GDN_ROTARY_YARN = 3
+} gdn_rotary_scaling;
+int gdn_rotary(const void* q, const void* k, void* q_out, void* k_out, const int32_t* positions,
+               const float* inv_freq, int T, int Hq, int Hk, int d, int rotary_dim, int64_t ld_q,
+               int64_t ld_k, int64_t ld_q_out, int64_t ld_k_out, int interleaved, int inverse,
+               float scale, int dtype, void* stream);
+int gdn_rotary_inv_freq(int rotary_dim, double base, int scaling, double factor,
+                        int64_t original_context, double beta_fast, double beta_slow,
+                        float* inv_freq, float* scale);
+
+/*
+ * gdn_add_rmsnorm -- the norm ahead of a layer's projections, with the residual's addition:
+ *
+ *     h = x + residual          o = (1 + w) * h / sqrt(mean(h^2) + eps)
+ *
+ * over rows of C values (zero-centred gain, as in gdn_gated_rmsnorm).  The sum is taken in fp32 and
+ * the norm is of that sum; h, in dtype, is its rounding.
+ *   x, residual, o, h [rows, C] in dtype (bf16 or fp32); w [C] fp32; residual NULL: h = x; h NULL: not
+ *   written.  h may be x or residual (in place); o may be x.  C a multiple of 8 in 8..16384.
+ *   0 <= rows < 2^31.
+ * gdn_add_rmsnorm_fp8 -- the same with an 8-bit o8 [rows, C] (e4m3) for an 8-bit product, and
+ *   scales [rows, C / group] fp32: scale = max |o| / 448 over each group of columns and
+ *   o8 = e4m3(o / scale), from the fp32 o; group = C (one scale a row) or 128 (C a multiple of 128).
+ *   A group of zeros has scale 0; a NaN makes its group's scale and values NaN.
+ * gdn_add_rmsnorm_backward -- from the stored h: dx = dL/dh [rows, C] in dtype, the gradient of
+ *   both x and residual, given d_o and d_h (the gradient that reaches h itself; NULL = 0), and dw
+ *   [C] fp32, summed over the rows in a fixed order.  ws/ws_bytes:
+ *   gdn_workspace_bytes(GDN_OP_ADD_RMSNORM_BACKWARD, 1, rows, 1, C, C, 0).  dx may be d_o or d_h.  With rows
+ *   = 0 dw is zeroed and the row tensors may be NULL.
+ * Errors: GDN_ERR_INVALID_ARG, GDN_ERR_UNSUPPORTED_SHAPE (C), GDN_ERR_WORKSPACE.
+ */
+int gdn_add_rmsnorm(const void* x, const void* residual, const float* w, void* o, void* h,
+                    int64_t rows, int C, int dtype, float eps, void* stream);
+int gdn_add_rmsnorm_fp8(const void* x, const void* residual, const float* w, void* o8,
+                        float* scales, void* h, int64_t rows, int C, int group, int dtype,
+                        float eps, void* stream);
+int gdn_add_rmsnorm_backward(const void* h, const float* w, const void* d_o, const void* d_h,
+                             void* dx, float* dw, int64_t rows, int C, int dtype, float eps,
+                             void* ws, size_t ws_bytes, void* stream);
 
 /*
  * gdn_selftest_wait_timeout -- exercises the failure path of the library's bounded waits.

@@ -1,0 +1,173 @@
+"""Host-side checks of the decayed linear attention's, the rotary positions' and the residual norm's calls:
+refusals before any launch, workspace sizes, the rotary frequencies."""
+import ctypes
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from gated_deltanet_linear_eqs_b200 import _abi, api
+from gated_deltanet_linear_eqs_b200.build import build
+
+A = 0x10000  # a 16-byte-aligned fake address: a rejected call touches nothing
+BAD, SHAPE, WS = _abi.GDN_ERR_INVALID_ARG, _abi.GDN_ERR_UNSUPPORTED_SHAPE, _abi.GDN_ERR_WORKSPACE
+
+
+@pytest.fixture(scope="module")
+def lib():
+    build()
+    return _abi.load()
+
+
+def dense(lib, **kw):
+    a = dict(q=A, k=A, v=A, g=A, s0=0, y=A, sf=0, B=1, T=4096, H=2, Hk=1, dk=128, dv=128, dt=0, scale=1.0, ws=A, wsb=1 << 40)
+    a.update(kw)
+    return lib.gdn_linear_attn(*a.values(), None)
+
+
+def varlen(lib, **kw):
+    a = dict(q=A, k=A, v=A, g=A, cu=A, n=2, s0=0, y=A, sf=0, T=4096, H=2, Hk=1, dk=64, dv=64, dt=1, scale=1.0, ws=A,
+             wsb=1 << 40)
+    a.update(kw)
+    return lib.gdn_linear_attn_varlen(*a.values(), None)
+
+
+def back(lib, **kw):
+    a = dict(q=A, k=A, v=A, g=A, s0=0, dy=A, dsf=0, dq=A, dk_=A, dv_=A, ds0=0, B=1, T=4096, H=2, Hk=1, dk=128, dv=128, dt=0,
+             scale=1.0, ws=A, wsb=1 << 40)
+    a.update(kw)
+    return lib.gdn_linear_attn_backward(*a.values(), None)
+
+
+def back_varlen(lib, **kw):
+    a = dict(q=A, k=A, v=A, g=A, cu=A, n=2, s0=0, dy=A, dsf=0, dq=A, dk_=A, dv_=A, ds0=0, T=4096, H=2, Hk=1, dk=128, dv=128,
+             dt=0, scale=1.0, ws=A, wsb=1 << 40)
+    a.update(kw)
+    return lib.gdn_linear_attn_backward_varlen(*a.values(), None)
+
+
+@pytest.mark.parametrize("call", [dense, varlen, back, back_varlen])
+@pytest.mark.parametrize("kw,code", [
+    (dict(q=0), BAD), (dict(k=A + 8), BAD), (dict(v=0), BAD), (dict(g=0), BAD), (dict(s0=A + 4), BAD), (dict(T=0), BAD),
+    (dict(H=0), BAD), (dict(Hk=0), BAD), (dict(H=3, Hk=2), BAD), (dict(dt=2), BAD), (dict(dk=96, dv=96), SHAPE),
+    (dict(dk=64, dv=128), SHAPE), (dict(ws=0), WS), (dict(wsb=4096), WS), (dict(ws=A + 8), WS),
+    (dict(T=2 ** 31 - 1, H=1 << 10), BAD)])
+def test_linear_attn_refusals(lib, call, kw, code):
+    assert call(lib, **kw) == code
+
+
+def test_linear_attn_more_refusals(lib):
+    assert dense(lib, y=0) == BAD and dense(lib, sf=A + 4) == BAD and dense(lib, B=0) == BAD
+    assert dense(lib, B=1 << 20, T=1 << 12) == BAD           # 2^32 tokens
+    assert varlen(lib, cu=0) == BAD and varlen(lib, n=0) == BAD and varlen(lib, y=A + 2) == BAD
+    for f in (back, back_varlen):
+        for n in ("dy", "dq", "dk_", "dv_"):
+            assert f(lib, **{n: 0}) == BAD
+        assert f(lib, ds0=A + 4) == BAD and f(lib, dsf=A + 8) == BAD
+    step = lambda **kw: lib.gdn_linear_attn_decode_step(*{**dict(q=A, k=A, v=A, g=A, s=A, y=A, N=4, H=4, Hk=2, dk=64, dv=64,
+                                                                 dt=0, scale=1.0), **kw}.values(), None)
+    assert step(q=0) == BAD and step(s=A + 4) == BAD and step(N=0) == BAD and step(Hk=3) == BAD and step(dt=9) == BAD
+    assert step(dk=32, dv=32) == SHAPE and step(N=1 << 30) == BAD
+
+
+def test_linear_attn_workspace(lib):
+    n = ctypes.c_size_t(0)
+    f = lambda *a: lib.gdn_linear_attn_workspace_bytes(*a, ctypes.byref(n))
+    # enough sequences and heads for every SM: one segment each, no states in between
+    assert f(0, 8, 4096, 32, 32, 128, 128, 0) == 0 and n.value == 0
+    # one long sequence: a state for each segment and head
+    assert f(0, 1, 32768, 16, 16, 128, 128, 0) == 0
+    assert n.value > 0 and n.value % (16 * 128 * 128 * 4) == 0
+    # shared heads' gradients: fp32 parts of dk and dv for every head
+    assert f(1, 8, 4096, 32, 8, 128, 128, 0) == 0 and n.value == 2 * 8 * 4096 * 32 * 128 * 4
+    for bad in ((0, 0, 1, 1, 1, 64, 64, 0), (0, 1, 0, 1, 1, 64, 64, 0), (0, 1, 1, 3, 2, 64, 64, 0), (0, 2, 5, 1, 1, 64, 64, 3),
+                (0, 1, 5, 1, 1, 64, 64, -1)):
+        assert f(*bad) == BAD
+    assert f(0, 1, 5, 1, 1, 32, 32, 0) == SHAPE
+    assert lib.gdn_linear_attn_workspace_bytes(0, 1, 5, 1, 1, 64, 64, 0, None) == BAD
+
+
+def test_rotary_refusals(lib):
+    def call(**kw):
+        a = dict(q=A, k=A, qo=A, ko=A, p=A, f=A, T=10, Hq=4, Hk=2, d=64, r=32, lq=256, lk=128, lqo=256, lko=128, il=0, inv=0,
+                 scale=1.0, dt=0)
+        a.update(kw)
+        return lib.gdn_rotary(*a.values(), None)
+    assert call(q=0) == BAD and call(qo=A + 8) == BAD and call(k=0) == BAD and call(p=0) == BAD and call(p=A + 2) == BAD
+    assert call(f=0) == BAD and call(T=-1) == BAD and call(Hq=0) == BAD and call(Hk=-1) == BAD and call(dt=3) == BAD
+    assert call(lq=248) == BAD and call(lk=132) == BAD and call(lqo=264) == BAD  # below a row; not of 8; in place
+    assert call(d=60) == SHAPE and call(d=2048, lq=8192, lk=4096) == SHAPE
+    assert call(r=31) == SHAPE and call(r=66) == SHAPE and call(r=0) == SHAPE
+
+
+def test_rotary_frequencies(lib):
+    f, s = api.gdn_rotary_inv_freq(128, base=1e4)
+    np.testing.assert_allclose(f.double().numpy(), 1e4 ** (-np.arange(64) / 64), rtol=2.0 ** -24)
+    assert s == 1.0
+    lin, _ = api.gdn_rotary_inv_freq(128, base=1e4, scaling="linear", factor=4)
+    np.testing.assert_allclose(lin.double().numpy(), f.double().numpy() / 4, rtol=2.0 ** -23)
+    ntk, _ = api.gdn_rotary_inv_freq(128, base=1e4, scaling="ntk", factor=4)
+    np.testing.assert_allclose([float(ntk[0]), float(ntk[-1])], [1.0, float(f[-1]) / 4], rtol=2.0 ** -22)
+    y, s = api.gdn_rotary_inv_freq(64, base=1e7, scaling="yarn", factor=4, original_context=262144)
+    assert s == pytest.approx(0.1 * math.log(4) + 1, rel=1e-6)
+    # 32 turns within 262144 positions fall to pair 14.2, one turn to pair 21.1: whole pairs 14 and 22
+    base = 1e7 ** (-np.arange(32) / 32)
+    slow = np.clip((np.arange(32) - 14) / 8, 0, 1)
+    np.testing.assert_allclose(y.double().numpy(), base / 4 * slow + base * (1 - slow), rtol=2.0 ** -23)
+    one, _ = api.gdn_rotary_inv_freq(2, base=1e4, scaling="ntk", factor=8)
+    assert one.tolist() == [1.0]
+    for kw in (dict(rotary_dim=0), dict(rotary_dim=7), dict(rotary_dim=64, base=1.0), dict(rotary_dim=64, base=float("nan")),
+               dict(rotary_dim=64, scaling="linear", factor=0.5), dict(rotary_dim=64, scaling="yarn", factor=2),
+               dict(rotary_dim=64, scaling="yarn", factor=2, original_context=100, beta_fast=1, beta_slow=2)):
+        with pytest.raises(api.GdnError):
+            api.gdn_rotary_inv_freq(**kw)
+    with pytest.raises(ValueError):
+        api.gdn_rotary_inv_freq(64, scaling="other")
+
+
+def test_add_norm_refusals(lib):
+    fwd = lambda **kw: lib.gdn_add_rmsnorm(*{**dict(x=A, r=A, w=A, o=A, h=A, rows=10, C=256, dt=0, eps=1e-6), **kw}.values(),
+                                           None)
+    q = lambda **kw: lib.gdn_add_rmsnorm_fp8(*{**dict(x=A, r=A, w=A, o=A, s=A, h=A, rows=10, C=256, g=128, dt=0, eps=1e-6),
+                                               **kw}.values(), None)
+    b = lambda **kw: lib.gdn_add_rmsnorm_backward(*{**dict(h=A, w=A, do=A, dh=0, dx=A, dw=A, rows=10, C=256, dt=0, eps=1e-6,
+                                                           ws=A, wsb=1 << 30), **kw}.values(), None)
+    for f in (fwd, q, b):
+        assert f(w=0) == BAD and f(rows=-1) == BAD and f(rows=1 << 31) == BAD and f(eps=-1.0) == BAD
+        assert f(eps=float("nan")) == BAD and f(dt=4) == BAD
+        assert f(C=4) == SHAPE and f(C=252) == SHAPE and f(C=16392) == SHAPE
+    for f in (fwd, q):
+        assert f(x=0) == BAD and f(o=A + 8) == BAD and f(r=A + 2) == BAD and f(h=A + 8) == BAD
+    assert q(s=0) == BAD and q(g=64) == BAD and q(C=264, g=128) == SHAPE
+    assert b(h=0) == BAD and b(do=0) == BAD and b(dx=0) == BAD and b(dw=0) == BAD and b(dh=A + 8) == BAD
+    assert b(ws=0) == WS and b(wsb=100) == WS and b(ws=A + 8) == WS
+    n = ctypes.c_size_t(0)
+    w = lambda rows, C: lib.gdn_workspace_bytes(_abi.GDN_OP_ADD_RMSNORM_BACKWARD, 1, rows, 1, C, C, 0, ctypes.byref(n))
+    assert w(3, 256) == 0 and n.value == 3 * 256 * 4
+    assert w(10 ** 6, 4096) == 0 and n.value == 592 * 4096 * 4
+    assert w(3, 12) == SHAPE
+
+
+def test_bindings_refuse_host_tensors_and_shapes():
+    t = torch.zeros(1, 8, 2, 64)
+    g = torch.zeros(2)
+    st = torch.zeros(1, 2, 64, 64)
+    with pytest.raises(ValueError, match="CUDA"):
+        api.gdn_linear_attn(t, t, t, g)
+    with pytest.raises(ValueError, match="CUDA"):
+        api.gdn_linear_attn_varlen(t[0], t[0], t[0], g, torch.zeros(2, dtype=torch.int32))
+    with pytest.raises(ValueError, match="CUDA"):
+        api.gdn_linear_attn_backward(t, t, t, g, t)
+    with pytest.raises(ValueError, match="CUDA"):
+        api.gdn_linear_attn_decode_step(t[:, 0], t[:, 0], t[:, 0], g, st)
+    with pytest.raises(ValueError, match="shared"):
+        api.gdn_linear_attn(t, t[:, :, :1].expand(1, 8, 3, 64), t, g)
+    with pytest.raises(ValueError, match="bf16 or fp32"):
+        api.gdn_linear_attn(t.half(), t.half(), t.half(), g)
+    with pytest.raises(ValueError, match="CUDA"):
+        api.gdn_rotary(t[0], None, torch.zeros(8, dtype=torch.int32), torch.zeros(32))
+    with pytest.raises(ValueError, match="CUDA"):
+        api.gdn_add_rmsnorm(t[0, :, 0], None, torch.zeros(64))
+    with pytest.raises(ValueError, match="CUDA"):
+        api.gdn_add_rmsnorm_backward(t[0, :, 0], torch.zeros(64), t[0, :, 0])

@@ -1,0 +1,251 @@
+"""GPU parity of the decayed linear attention (prompts, gradients, single tokens; through the C ABI)
+against its fp64 oracle.
+
+Tolerances, elementwise, from the roundings that a value passes through.  Let A be the same formula
+with the absolute values of all inputs: every partial sum is at most A.
+ * bf16 outputs: the scores (or the state) are rounded to bf16 once (half a step, 2^-8 of the value
+   each at most, so 2^-8 A in the sum) and the output is rounded to bf16 (2^-8 |y|); fp32 sums add
+   less than 2^-15 A.
+ * fp32 outputs and states: products of at most 128 + 64 + 128 terms and up to 40 chunks, each step
+   off by 2^-24 of a partial sum (the tensor cores' sums by 2^-23), decay factors by 2^-21: less than
+   2^-15 A.
+ * gradients of shared heads add the parts in fp32: within the same bounds."""
+import numpy as np
+import pytest
+import torch
+
+import oracle.linear_attn as oattn
+from gated_deltanet_linear_eqs_b200 import api
+from gated_deltanet_linear_eqs_b200.inputs import cu_seqlens_from
+
+pytestmark = pytest.mark.gpu
+
+DT = {"bf16": torch.bfloat16, "fp32": torch.float32}
+
+
+def make(lens, H, Hk, d, dtype, seed=0, decay="mixed"):
+    g = torch.Generator().manual_seed(seed)
+    T, N = sum(lens), len(lens)
+    r = lambda *s: torch.randn(*s, generator=g)
+    x = {n: r(T, h, d).to(DT[dtype]) for n, h in (("q", H), ("k", Hk), ("v", Hk), ("dy", H))}
+    x["s0"], x["ds_final"] = 0.5 * r(N, H, d, d), 0.2 * r(N, H, d, d)
+    ld = {"mixed": -torch.exp2(2.0 - 2.0 * torch.arange(H)), "none": torch.zeros(H),
+          "slow": torch.log1p(-torch.exp2(-6.0 - torch.arange(H)))}[decay]
+    if decay == "mixed":
+        ld[-1] = 0.0
+    x["log_decay"] = ld.float()
+    x["cu_seqlens"] = cu_seqlens_from(lens)
+    return x
+
+
+def cuda(x):
+    return {n: t.cuda() for n, t in x.items()}
+
+
+def close(got, ref, mag, dtype, what):
+    got = got.double().cpu().numpy()
+    assert np.all(np.isfinite(got)), f"{what}: not finite"
+    tol = 2.0 ** -15 * mag + 1e-30
+    if dtype == "bf16":
+        tol = tol + 2.0 ** -8 * (mag + np.abs(ref)) * (1 + 2.0 ** -7)
+    bad = np.abs(got - ref) > tol
+    assert not bad.any(), f"{what}: {bad.sum()} of {bad.size} off, worst {np.max(np.abs(got - ref) / tol):.3g} bounds"
+    if dtype == "bf16" and ref.size >= 4096:
+        # two independent roundings of at most half a step each, uniform in it: their root mean
+        # square is at most sqrt(2) 2^-8 / sqrt(3) = 0.82 2^-8 of the values
+        rel = np.linalg.norm(got - ref) / np.linalg.norm(ref)
+        assert rel <= 2.0 ** -8, f"{what}: relative error {rel:.3g}"
+
+
+def mags(x, scale):
+    a = {n: (t.double().abs().numpy() if n != "log_decay" else t.double().numpy()) for n, t in x.items()}
+    ya, sa = oattn.forward(a["q"], a["k"], a["v"], a["log_decay"], x["cu_seqlens"], s0=a["s0"], scale=scale)
+    ga = oattn.backward(a["q"], a["k"], a["v"], a["log_decay"], x["cu_seqlens"], a["dy"], s0=a["s0"],
+                        ds_final=a["ds_final"], scale=scale)
+    return ya, sa, ga
+
+
+LENS = [[1], [64], [65], [200], [1, 63, 0, 64, 2, 65, 0, 130], [0, 0, 3], [700, 0, 1, 640]]
+
+
+@pytest.mark.parametrize("lens", LENS, ids=lambda l: "-".join(map(str, l)))
+@pytest.mark.parametrize("H,Hk,d,dtype,decay", [
+    (1, 1, 64, "fp32", "mixed"), (2, 2, 128, "fp32", "slow"), (4, 1, 64, "fp32", "none"),
+    (1, 1, 64, "bf16", "slow"), (3, 3, 128, "bf16", "mixed"), (4, 2, 128, "bf16", "slow"),
+    (6, 2, 64, "bf16", "none"), (1, 1, 128, "bf16", "none")])
+def test_varlen_and_gradients(lens, H, Hk, d, dtype, decay):
+    x = make(lens, H, Hk, d, dtype, seed=sum(lens) + H, decay=decay)
+    scale = d ** -0.5
+    c = cuda(x)
+    y, sf = api.gdn_linear_attn_varlen(c["q"], c["k"], c["v"], c["log_decay"], c["cu_seqlens"], s0=c["s0"], scale=scale)
+    out = api.gdn_linear_attn_backward_varlen(c["q"], c["k"], c["v"], c["log_decay"], c["cu_seqlens"], c["dy"],
+                                              s0=c["s0"], ds_final=c["ds_final"], scale=scale)
+    torch.cuda.synchronize()
+    assert api.gdn_read_device_status() == 0
+    ya, sa, ga = mags(x, scale)
+    yr, sr = oattn.forward(x["q"], x["k"], x["v"], x["log_decay"], x["cu_seqlens"], s0=x["s0"], scale=scale)
+    gr = oattn.backward(x["q"], x["k"], x["v"], x["log_decay"], x["cu_seqlens"], x["dy"], s0=x["s0"],
+                        ds_final=x["ds_final"], scale=scale)
+    close(y, yr, ya, dtype, "y")
+    close(sf, sr, sa, "fp32", "s_final")
+    for n in ("dq", "dk", "dv"):
+        close(out[n], gr[n], ga[n], dtype, n)
+    close(out["ds0"], gr["ds0"], ga["ds0"], "fp32", "ds0")
+
+
+@pytest.mark.parametrize("B,T,H,Hk,d,dtype", [(2, 1, 2, 1, 64, "bf16"), (1, 1300, 1, 1, 128, "bf16"),
+                                              (3, 129, 2, 2, 128, "bf16"), (2, 577, 4, 2, 64, "fp32")])
+def test_dense_equals_packed(B, T, H, Hk, d, dtype):
+    """Dense sequences against the oracle, without states as well."""
+    x = make([T] * B, H, Hk, d, dtype, seed=T, decay="slow")
+    c = cuda(x)
+    b = lambda t: t.view(B, T, *t.shape[1:])
+    scale = 0.3
+    for states in (True, False):
+        s0, dsf = (c["s0"], c["ds_final"]) if states else (None, None)
+        y, sf = api.gdn_linear_attn(b(c["q"]), b(c["k"]), b(c["v"]), c["log_decay"], s0=s0, scale=scale,
+                                    want_final=states)
+        out = api.gdn_linear_attn_backward(b(c["q"]), b(c["k"]), b(c["v"]), c["log_decay"], b(c["dy"]), s0=s0,
+                                           ds_final=dsf, scale=scale, want_ds0=states)
+        torch.cuda.synchronize()
+        assert api.gdn_read_device_status() == 0
+        z = dict(x) if states else {**x, "s0": torch.zeros_like(x["s0"]), "ds_final": torch.zeros_like(x["ds_final"])}
+        ya, sa, ga = mags(z, scale)
+        yr, sr = oattn.forward(z["q"], z["k"], z["v"], z["log_decay"], z["cu_seqlens"], s0=z["s0"], scale=scale)
+        gr = oattn.backward(z["q"], z["k"], z["v"], z["log_decay"], z["cu_seqlens"], z["dy"], s0=z["s0"],
+                            ds_final=z["ds_final"], scale=scale)
+        close(y.flatten(0, 1), yr, ya, dtype, "y")
+        for n in ("dq", "dk", "dv"):
+            close(out[n].flatten(0, 1), gr[n], ga[n], dtype, n)
+        if states:
+            close(sf, sr, sa, "fp32", "s_final")
+            close(out["ds0"], gr["ds0"], ga["ds0"], "fp32", "ds0")
+        else:
+            assert sf is None and out["ds0"] is None
+
+
+def test_gradients_against_differences():
+    """fp32, the sum of y dy + s_final ds_final: a central difference along a random direction is exact for a
+    function that is linear in each tensor, up to the fp32 rounding of the two losses."""
+    x = make([70, 3], 2, 1, 64, "fp32", seed=5)
+    c = cuda(x)
+    g = api.gdn_linear_attn_backward_varlen(c["q"], c["k"], c["v"], c["log_decay"], c["cu_seqlens"], c["dy"],
+                                            s0=c["s0"], ds_final=c["ds_final"], scale=0.2)
+
+    def loss(a):
+        y, s = api.gdn_linear_attn_varlen(a["q"], a["k"], a["v"], a["log_decay"], a["cu_seqlens"], s0=a["s0"], scale=0.2)
+        return float((y.double() * a["dy"].double()).sum() + (s.double() * a["ds_final"].double()).sum())
+
+    gen = torch.Generator(device="cuda").manual_seed(0)
+    for n in ("q", "k", "v", "s0"):
+        e = torch.randn(c[n].shape, generator=gen, device="cuda")
+        num = (loss({**c, n: c[n] + e}) - loss({**c, n: c[n] - e})) / 2
+        ref = float((g["d" + n].double() * e.double()).sum())
+        terms = float((g["d" + n].double() * e.double()).square().sum().sqrt())
+        # rounding of 10^5 outputs of size ~100 at 2^-18 each, adding at random: 2^-18 * 100 * 300
+        assert abs(num - ref) <= 0.2 + 1e-4 * terms, (n, num, ref)
+
+
+@pytest.mark.parametrize("N,H,Hk,d,dtype", [(1, 1, 1, 64, "bf16"), (5, 6, 2, 128, "bf16"), (3, 2, 2, 128, "fp32"),
+                                            (33, 4, 1, 64, "fp32")])
+def test_decode_steps(N, H, Hk, d, dtype):
+    """Ten steps against the oracle's token loop (each step starts from the oracle's bounds of the last)."""
+    steps = 10
+    x = make([steps] * N, H, Hk, d, dtype, seed=N)
+    c = cuda(x)
+    b = lambda t: t.view(N, steps, *t.shape[1:])
+    st = c["s0"].clone()
+    ys = [api.gdn_linear_attn_decode_step(b(c["q"])[:, t].contiguous(), b(c["k"])[:, t].contiguous(),
+                                          b(c["v"])[:, t].contiguous(), c["log_decay"], st, scale=0.25)
+          for t in range(steps)]
+    y = torch.stack(ys, 1).flatten(0, 1)
+    yr, sr = oattn.forward(x["q"], x["k"], x["v"], x["log_decay"], x["cu_seqlens"], s0=x["s0"], scale=0.25)
+    ya, sa, _ = mags(x, 0.25)
+    close(st, sr, sa, "fp32", "state")
+    close(y, yr, ya, dtype, "y")
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("bf16", 64), ("fp32", 64)])
+def test_resume_and_long_segments(dtype, d):
+    """A prompt in two calls equals one; cut into many segments (one head, 5000 tokens) it equals the oracle."""
+    x = make([5000], 1, 1, d, dtype, seed=9, decay="slow")
+    c = cuda(x)
+    a = (c["log_decay"],)
+    y, sf = api.gdn_linear_attn(*(c[n][None] for n in "qkv"), *a, s0=c["s0"], scale=0.1)
+    y1, s1 = api.gdn_linear_attn(*(c[n][None, :1999].contiguous() for n in "qkv"), *a, s0=c["s0"], scale=0.1)
+    y2, s2 = api.gdn_linear_attn(*(c[n][None, 1999:].contiguous() for n in "qkv"), *a, s0=s1, scale=0.1)
+    ya, sa, _ = mags(x, 0.1)
+    yr, sr = oattn.forward(x["q"], x["k"], x["v"], x["log_decay"], x["cu_seqlens"], s0=x["s0"], scale=0.1)
+    close(y[0], yr, ya, dtype, "y")
+    close(torch.cat([y1, y2], 1)[0], yr, ya, dtype, "y in two calls")
+    close(sf, sr, sa, "fp32", "s_final")
+    close(s2, sr, sa, "fp32", "s_final in two calls")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_other_documents_and_heads_are_untouched(dtype):
+    """NaN and infinities in one document (up to its last, partial chunk) reach no other document, no other
+    head, and nothing before their 64-token chunk; rows behind the last document stay as they were."""
+    lens, H, d = [70, 100, 40], 2, 128
+    x = make(lens, H, H, d, dtype, seed=3, decay="slow")
+    c = cuda(x)
+    T = sum(lens)
+    run = lambda c, y=None: api.gdn_linear_attn_varlen(c["q"], c["k"], c["v"], c["log_decay"], c["cu_seqlens"],
+                                                       s0=c["s0"], y=y)
+    back = lambda c: api.gdn_linear_attn_backward_varlen(c["q"], c["k"], c["v"], c["log_decay"], c["cu_seqlens"],
+                                                         c["dy"], s0=c["s0"], ds_final=c["ds_final"])
+    y0, s0 = run(c)
+    b0 = back(c)
+    z = {n: t.clone() for n, t in c.items()}
+    for n in ("q", "k", "v", "dy"):
+        z[n][170 - 30:170, 0] = float("nan")     # the second document's last 30 tokens, head 0
+        z[n][170 - 20, 0, 5] = float("inf")
+    buf = torch.full((T + 3, H, d), 7.0, dtype=DT[dtype], device="cuda")
+    y1, s1 = run(z, y=buf[:T])
+    b1 = back(z)
+    torch.cuda.synchronize()
+    assert torch.equal(y1[:134], y0[:134]) and torch.equal(y1[170:], y0[170:]) and torch.equal(y1[:, 1], y0[:, 1])
+    assert torch.equal(s1[[0, 2]], s0[[0, 2]]) and torch.equal(s1[:, 1], s0[:, 1])
+    assert bool((buf[T:] == 7.0).all())
+    for n in ("dq", "dk", "dv"):
+        assert torch.equal(b1[n][:70], b0[n][:70]) and torch.equal(b1[n][170:], b0[n][170:])
+        assert torch.equal(b1[n][:, 1], b0[n][:, 1])
+    assert torch.equal(b1["ds0"][[0, 2]], b0["ds0"][[0, 2]])
+
+
+def test_same_result_every_time_and_captured():
+    """Runs are bit-equal; a captured graph replays them on new inputs; two streams with a workspace each."""
+    x = make([900, 70, 1], 2, 1, 128, "bf16", seed=1, decay="slow")
+    z = make([900, 70, 1], 2, 1, 128, "bf16", seed=2, decay="slow")
+    c, w = cuda(x), cuda(z)
+    n = api.gdn_linear_attn_workspace_bytes(1, 971, 2, 1, 128, 128, 3, backward=True)
+    ws = [torch.empty(n, dtype=torch.uint8, device="cuda") for _ in range(2)]
+
+    def both(c, ws):
+        y, s = api.gdn_linear_attn_varlen(c["q"], c["k"], c["v"], c["log_decay"], c["cu_seqlens"], s0=c["s0"], ws=ws)
+        g = api.gdn_linear_attn_backward_varlen(c["q"], c["k"], c["v"], c["log_decay"], c["cu_seqlens"], c["dy"],
+                                                s0=c["s0"], ds_final=c["ds_final"], ws=ws)
+        return [y, s, g["dq"], g["dk"], g["dv"], g["ds0"]]
+
+    ref, ref2 = both(c, ws[0]), both(w, ws[0])
+    assert all(torch.equal(a, b) for a, b in zip(ref, both(c, ws[0])))
+    static = {k: t.clone() for k, t in c.items()}
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        out = both(static, ws[0])
+    for src, want in ((c, ref), (w, ref2), (c, ref)):
+        for k, t in src.items():
+            static[k].copy_(t)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, want))
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s1):
+        o1 = both(c, ws[0])
+    with torch.cuda.stream(s2):
+        o2 = both(w, ws[1])
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(o1, ref)) and all(torch.equal(a, b) for a, b in zip(o2, ref2))
+    assert api.gdn_read_device_status() == 0
