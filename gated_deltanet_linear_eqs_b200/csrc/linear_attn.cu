@@ -213,8 +213,7 @@ cudaError_t launch_simt(const LaParams& p, int nseg, cudaStream_t st) {
 }
 
 cudaError_t launch_pass(const LaParams& p, int nseg, int d, int dtype, cudaStream_t st) {
-    if (dtype == GDN_BF16)
-        return d == 128 ? launch_simt<128, __nv_bfloat16>(p, nseg, st) : launch_simt<64, __nv_bfloat16>(p, nseg, st);
+    if (dtype == GDN_BF16) return launch_la_tc(p, nseg, d, st);
     return d == 128 ? launch_simt<128, float>(p, nseg, st) : launch_simt<64, float>(p, nseg, st);
 }
 

@@ -124,6 +124,9 @@ __device__ __forceinline__ size_t la_state_index(int kk, int vv, int state_t) {
     return state_t ? (size_t)vv * D + kk : (size_t)kk * D + vv;
 }
 
+// The bf16 passes on the tensor cores (linear_attn_tc.cu).
+cudaError_t launch_la_tc(const LaParams& p, int nseg, int d, cudaStream_t st);
+
 struct LaPlan {
     int L;       // segment length
     int nseg;    // segments (packed: an upper bound)

@@ -1,0 +1,462 @@
+// linear_attn_tc.cu -- the bf16 passes of the decayed linear attention on tcgen05.
+//
+// Formulas, roles and segments: linear_attn.cuh.  One CTA per (segment, head) walks its 64-token chunks.
+// With the state kept transposed (row v, column k), a chunk is five products:
+//     VT  = V^T I              (the transposed V, exact, as fp32 in TMEM)
+//     SC  = K Q^T              (scores, row j, column i)
+//     Ys  = S^T Q^T            S^T in bf16, an A operand in TMEM
+//     LOC = V~ K               V~ = VT diag(weights), an A operand in TMEM
+//     Yi  = V^T P              P = SC decayed and masked, bf16, in shared memory
+// and y_i = Yi + e^{g (i + 1)} Ys, S <- e^{g n} S + LOC.
+//  - The state lives in fp32 registers of the compute warps and is only rounded to bf16 as Ys's
+//    operand.  LOC is a fresh fp32 accumulator each chunk: added into the state by the CUDA cores, its
+//    sums do not suffer from the tensor cores' truncating accumulation over a long sequence.
+//  - The decay weights would cost the products' exactness if they were rounded to bf16 with V.  So a
+//    weighted value is cut into three bf16 pieces (8 bits each: exactly the fp32 value) and LOC is three
+//    products; s_final then has fp32 accuracy.  P is rounded to bf16 once (y is bf16).
+//  - A operands in TMEM rather than shared memory: the products are bound by shared-memory bandwidth
+//    (an A of 128 x 16 costs as much of it as a B of 128 columns), which V~ and S^T do not touch.
+// Warps 0-7 compute (two per TMEM lane quadrant), warp 8 loads by TMA through a ring of stages, warp 9
+// issues the products.  Every wait is bounded; one that gives up records GDN_ERR_TIMEOUT.
+#include <mutex>
+
+#include "linear_attn.cuh"
+#include "sm100.cuh"
+
+namespace gdn {
+
+namespace {
+
+using namespace sm100;
+
+constexpr int kTcThreads = 320;
+
+template <int D, bool STATE>
+struct TcLayout {
+    static constexpr int KB = D / 64;             // 64-column panels of a tile
+    static constexpr int TILE = KB * 8192;        // 64 tokens x D, 128-byte rows
+    static constexpr int NT = STATE ? 2 : 3;      // K, V (, Q)
+    static constexpr int STAGES = 3;
+    static constexpr int STAGE = NT * TILE;
+    static constexpr int P = STAGES * STAGE;      // [j][i] bf16
+    static constexpr int EYE = P + 8192;          // 64 x 64 identity
+    static constexpr int TAB = EYE + 8192;        // decay of the scores: [128], zero below 64
+    static constexpr int SW = TAB + 512;          // weights of V~: [64]
+    static constexpr int FI = SW + 256;           // factors of Ys: [64]
+    static constexpr int BAR = FI + 256;
+    static constexpr int MISC = BAR + 16 * 8;     // TMEM base, abort flag, zero word
+    static constexpr int BYTES = MISC + 16;
+    static constexpr uint32_t T_SC = 0, T_VT = 64, T_V3 = 128, T_LOC = 160, T_YI = 288, T_YS = 352, T_S = 416;
+};
+enum { B_FULL = 0, B_EMPTY = 3, B_VT = 6, B_SC, B_LOC, B_Y, C_FIX, C_V, C_P, C_S, C_Y, B_FIN };
+
+__device__ __forceinline__ uint32_t pack_rn(float a, float b) {
+    const __nv_bfloat162 x = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&x);
+}
+// the upper halves of two words: a (low half) and b
+__device__ __forceinline__ uint32_t pack_hi(float a, float b) {
+    return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
+}
+__device__ __forceinline__ float hi_part(float x) { return __uint_as_float(__float_as_uint(x) & 0xffff0000u); }
+
+template <int D, bool REV, bool STATE>
+__global__ void __launch_bounds__(kTcThreads, 1)
+la_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+             const __grid_constant__ CUtensorMap tm_v, const LaParams p) {
+    using L = TcLayout<D, STATE>;
+    constexpr int KB = L::KB, C = kLaChunk;
+    const int h = blockIdx.x % p.H, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    LaSegment sg;
+    if (!la_find_segment(p, blockIdx.x / p.H, &sg)) return;
+    if (STATE && sg.idx == (REV ? 0 : sg.count - 1)) return;  // no segment starts behind it
+    const int nch = (sg.len + C - 1) / C;
+
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t* bars = reinterpret_cast<uint64_t*>(sm + L::BAR);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + L::MISC);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + L::MISC + 4);
+    volatile int* never = reinterpret_cast<volatile int*>(sm + L::MISC + 8);
+    const float g = p.log_decay[h];
+    if (tid == 0) {
+        for (int b = 0; b < C_FIX; ++b) mbar_init(&bars[b], 1);
+        for (int b = C_FIX; b < B_FIN; ++b) mbar_init(&bars[b], 8);
+        mbar_init(&bars[B_FIN], 1);
+        *abort_flag = 0;
+        *never = 0;
+        fence_mbar_init();
+    }
+    if (warp == 9) tmem_alloc(tmem_slot, 512);
+    // the identity and the decay of the scores
+    for (int e = tid; e < 512; e += kTcThreads) {
+        const int r = e >> 3, c = e & 7;
+        uint32_t w[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            w[u] = r == 8 * c + 2 * u ? 0x3f80u : r == 8 * c + 2 * u + 1 ? 0x3f800000u : 0u;
+        *reinterpret_cast<uint4*>(sm + L::EYE + swz(r, c)) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    float* tab = reinterpret_cast<float*>(sm + L::TAB);
+    float* sw = reinterpret_cast<float*>(sm + L::SW);
+    float* fi = reinterpret_cast<float*>(sm + L::FI);
+    for (int e = tid; e < 128; e += kTcThreads) tab[e] = e < 64 ? 0.f : expf(g * (float)(e - 64)) * p.p_scale;
+    fence_proxy_async_smem();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    auto fail = [&](int bar) {
+        *abort_flag = 1;
+        record_status(p.status, GDN_ERR_TIMEOUT);
+        (void)bar;
+    };
+    auto wwait = [&](int bar, uint32_t parity) {
+        const bool ok = mbar_wait_warp(&bars[bar], parity, abort_flag);
+        if (!ok && lane == 0) fail(bar);
+        return ok;
+    };
+    // chunk `cc` of the walk: its place in the segment and its tokens
+    auto place = [&](int cc) { return REV ? nch - 1 - cc : cc; };
+
+    if (warp == 8) {
+        // ---------------------------------------------------------------- loads
+        if (lane == 0) {
+            int cc = 0;
+            for (; cc < nch; ++cc) {
+                const int s = cc % L::STAGES;
+                if (cc >= L::STAGES && !mbar_wait(&bars[B_EMPTY + s], ((cc / L::STAGES) - 1) & 1, abort_flag)) {
+                    fail(B_EMPTY + s);
+                    break;
+                }
+                uint64_t* full = &bars[B_FULL + s];
+                mbar_arrive_expect_tx(full, L::STAGE);
+                const int z = sg.t0 + place(cc) * C;
+                uint8_t* dst = sm + s * L::STAGE;
+#pragma unroll
+                for (int b = 0; b < KB; ++b) {
+                    tma_load_3d(dst + b * 8192, &tm_k, 64 * b, h / p.kdiv, z, full);
+                    tma_load_3d(dst + L::TILE + b * 8192, &tm_v, 64 * b, h / p.vdiv, z, full);
+                    if (!STATE) tma_load_3d(dst + 2 * L::TILE + b * 8192, &tm_q, 64 * b, h / p.qdiv, z, full);
+                }
+            }
+            // copies still in flight land before the CTA may end (bounded)
+            for (int k = cc > L::STAGES ? cc - L::STAGES : 0; k < cc; ++k)
+                mbar_wait(&bars[B_FULL + k % L::STAGES], (k / L::STAGES) & 1, never, 100000000ull);
+        }
+        __syncwarp();
+    } else if (warp == 9) {
+        // ---------------------------------------------------------------- products (one lane)
+        if (lane == 0) {
+            constexpr uint32_t ID_VT = idesc_bf16(128, 64, true, false);
+            constexpr uint32_t ID_SC = idesc_bf16(64, 64, false, false);
+            constexpr uint32_t ID_YS = idesc_bf16(128, 64, false, false);
+            constexpr uint32_t ID_LOC = idesc_bf16(128, D, false, true);
+            constexpr uint32_t ID_YI = idesc_bf16(128, 64, true, true);
+            // V^T as an MN-major A of 128 rows; for D = 64 rows 64..127 repeat rows 0..63 (LBO 0)
+            constexpr uint32_t VLBO = D == 128 ? 8192 : 0;
+            const uint32_t s0 = smem_u32(sm);
+            bool ok = true;
+            for (int cc = 0; cc < nch && ok; ++cc) {
+                const int s = cc % L::STAGES;
+                const uint32_t k = s0 + s * L::STAGE, v = k + L::TILE, q = v + L::TILE;
+                const uint32_t ph = cc & 1;
+                const bool tail = place(cc) * C + C > sg.len;
+                ok = mbar_wait(&bars[B_FULL + s], (cc / L::STAGES) & 1, abort_flag);
+                if (ok && tail) ok = mbar_wait(&bars[C_FIX], 0, abort_flag);
+                if (!ok) break;
+                tc_fence_after();
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                    mma_bf16(tmem + L::T_VT, sdesc(v + kk * 2048, VLBO, 1024), sdesc(s0 + L::EYE + kk * 32, 16, 1024),
+                             ID_VT, kk != 0);
+                mma_commit(&bars[B_VT]);
+                if (!STATE) {
+#pragma unroll
+                    for (int kk = 0; kk < 4 * KB; ++kk) {
+                        const uint32_t o = (kk >> 2) * 8192 + (kk & 3) * 32;
+                        mma_bf16(tmem + L::T_SC, sdesc(k + o, 16, 1024), sdesc(q + o, 16, 1024), ID_SC, kk != 0);
+                    }
+                    mma_commit(&bars[B_SC]);
+                    // the state before the chunk is stored, and the last chunk's outputs are read
+                    ok = mbar_wait(&bars[C_S], ph, abort_flag) &&
+                         (cc == 0 || mbar_wait(&bars[C_Y], ph ^ 1, abort_flag));
+                    if (!ok) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int kk = 0; kk < 4 * KB; ++kk)
+                        mma_bf16_ta(tmem + L::T_YS, tmem + L::T_S + 8 * kk,
+                                    sdesc(q + (kk >> 2) * 8192 + (kk & 3) * 32, 16, 1024), ID_YS, kk != 0);
+                }
+                ok = mbar_wait(&bars[C_V], ph, abort_flag);
+                if (!ok) break;
+                tc_fence_after();
+#pragma unroll
+                for (int t = 0; t < 3; ++t)
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk) {
+                        const uint32_t a = t == 2 ? L::T_V3 + 8 * kk
+                                                  : L::T_VT + 32 * (kk >> 1) + 16 * t + 8 * (kk & 1);
+                        mma_bf16_ta(tmem + L::T_LOC, tmem + a, sdesc(k + kk * 2048, 8192, 1024), ID_LOC,
+                                    (t | kk) != 0);
+                    }
+                mma_commit(&bars[B_LOC]);
+                if (!STATE) {
+                    ok = mbar_wait(&bars[C_P], ph, abort_flag);
+                    if (!ok) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        mma_bf16(tmem + L::T_YI, sdesc(v + kk * 2048, VLBO, 1024),
+                                 sdesc(s0 + L::P + kk * 2048, 8192, 1024), ID_YI, kk != 0);
+                    mma_commit(&bars[B_Y]);
+                }
+                mma_commit(&bars[B_EMPTY + s]);
+            }
+            if (!ok && !*abort_flag) fail(B_FIN);
+            // no product may still be running when the CTA ends
+            mma_commit(&bars[B_FIN]);
+            mbar_wait(&bars[B_FIN], 0, never, 100000000ull);
+        }
+        __syncwarp();
+    } else {
+        // ---------------------------------------------------------------- compute
+        const int quad = warp & 3, half = warp >> 2;
+        const int row = quad * 32 + lane;                 // TMEM lane: the v index (D = 64: twice)
+        const int vv = row & (D - 1);
+        const bool mine = row < D;                        // writes results
+        const uint32_t tl = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+        constexpr int NS = D / 2;                         // state columns of this thread: k = half NS ..
+        const size_t DD = (size_t)D * D;
+        float S[NS];
+        auto index = [&](int x) {  // of element x in memory
+            const int k = half * NS + x;
+            return p.state_t ? vv * D + k : k * D + vv;
+        };
+        if (STATE) {
+#pragma unroll
+            for (int x = 0; x < NS; ++x) S[x] = 0.f;
+        } else {
+            const float* s_in = p.s_in ? p.s_in + ((size_t)sg.doc * p.H + h) * DD : nullptr;
+#pragma unroll
+            for (int x = 0; x < NS; ++x) S[x] = s_in ? s_in[index(x)] : 0.f;
+            const int behind = REV ? sg.count - 1 - sg.idx : sg.idx;
+            if (behind > 0) {
+                const float2 all = la_power2(g, p.L);
+                const float2 last = la_power2(g, sg.doc_len - (sg.count - 1) * p.L);
+                for (int b = 0; b < behind; ++b) {
+                    const int r = REV ? sg.count - 1 - b : b;
+                    const float2 w = r == sg.count - 1 ? last : all;
+                    const float* loc = p.local + ((size_t)(sg.first_id + r) * p.H + h) * DD;
+#pragma unroll
+                    for (int x = 0; x < NS; ++x) S[x] = fmaf(S[x], w.x, fmaf(S[x], w.y, loc[index(x)]));
+                }
+            }
+        }
+        // the state in bf16 as the A operand of Ys
+        auto store_state = [&]() {
+            uint32_t w[NS / 2];
+#pragma unroll
+            for (int x = 0; x < NS / 2; ++x) w[x] = pack_rn(S[2 * x], S[2 * x + 1]);
+#pragma unroll
+            for (int x = 0; x < NS / 2; x += 16) tmem_st16(tl + L::T_S + half * (NS / 2) + x, w + x);
+            tc_fence_before();
+            if (lane == 0) mbar_arrive(&bars[C_S]);
+        };
+        if (!STATE && nch > 0) store_state();
+        const float2 dec_full = la_power2(g, C);
+        float2 dec = dec_full;
+        int cur_n = -1;
+        // after a wait that gave up the warps walk on (the waits then return at once), so that all of them
+        // still meet at the named barriers; their results are not written
+        bool ok = true;
+        for (int cc = 0; cc < nch; ++cc) {
+            const int c = place(cc), n = min(C, sg.len - c * C), s = cc % L::STAGES;
+            const uint32_t ph = cc & 1;
+            if (n != cur_n) {  // the tables that depend on the chunk's length
+                named_sync(1, 256);
+                if (tid < C) {
+                    sw[tid] = REV ? expf(g * (float)(tid + 1)) * p.state_scale
+                                  : tid < n ? expf(g * (float)(n - 1 - tid)) * p.state_scale : 0.f;
+                    fi[tid] = REV ? (tid < n ? expf(g * (float)(n - 1 - tid)) * p.inter_scale : 0.f)
+                                  : expf(g * (float)(tid + 1)) * p.inter_scale;
+                }
+                dec = n == C ? dec_full : la_power2(g, n);
+                cur_n = n;
+                named_sync(1, 256);
+            }
+            if (n < C) {
+                // rows past the document's end hold other documents' tokens (or nothing): K and V are zeroed
+                ok = wwait(B_FULL + s, (cc / L::STAGES) & 1) && ok;
+                for (int e = tid; e < (C - n) * 8 * 2 * KB; e += 256) {
+                    const int r = n + (e >> 3) / (2 * KB), panel = (e >> 3) % (2 * KB);
+                    *reinterpret_cast<uint4*>(sm + s * L::STAGE + panel * 8192 + r * 128 + (e & 7) * 16) =
+                        make_uint4(0, 0, 0, 0);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars[C_FIX]);
+            }
+            // ---- V~: this thread's row, tokens 32 half .. +31
+            ok = wwait(B_VT, ph) && ok;
+            tc_fence_after();
+            {
+                float x[32];
+                tmem_ld32(tl + L::T_VT + 32 * half, x);
+                uint32_t a[16], b[16], d[16];
+#pragma unroll
+                for (int u = 0; u < 16; u += 2) {
+                    const float4 w4 = *reinterpret_cast<const float4*>(sw + 32 * half + 2 * u);
+                    const float w[4] = {w4.x, w4.y, w4.z, w4.w};
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float y0 = x[2 * (u + e)] * w[2 * e], y1 = x[2 * (u + e) + 1] * w[2 * e + 1];
+                        const float r0 = y0 - hi_part(y0), r1 = y1 - hi_part(y1);
+                        a[u + e] = pack_hi(y0, y1);
+                        b[u + e] = pack_hi(r0, r1);
+                        d[u + e] = pack_hi(r0 - hi_part(r0), r1 - hi_part(r1));
+                    }
+                }
+                tmem_st16(tl + L::T_VT + 32 * half, a);
+                tmem_st16(tl + L::T_VT + 32 * half + 16, b);
+                tmem_st16(tl + L::T_V3 + 16 * half, d);
+                tc_fence_before();
+                if (lane == 0) mbar_arrive(&bars[C_V]);
+            }
+            // ---- P: rows j = 16 quad .. +15, columns i = 32 half .. +31
+            if (!STATE) {
+                ok = wwait(B_SC, ph) && ok;
+                tc_fence_after();
+                float x[16];
+                tmem_ld_frag<4>(tl + L::T_SC + 32 * half, x);
+                const int j0 = 16 * quad + (lane >> 2), i0 = 32 * half + 2 * (lane & 3);
+                const float* t0 = tab + 64 + (REV ? j0 - i0 : i0 - j0);
+                constexpr int dir = REV ? -1 : 1;
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        const float y0 = x[4 * u + 2 * r] * t0[dir * (8 * u - 8 * r)];
+                        const float y1 = x[4 * u + 2 * r + 1] * t0[dir * (8 * u + 1 - 8 * r)];
+                        const int j = j0 + 8 * r;
+                        *reinterpret_cast<uint32_t*>(sm + L::P + swz(j, 4 * half + u) + 4 * (lane & 3)) =
+                            pack_rn(y0, y1);
+                    }
+                tc_fence_before();
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars[C_P]);
+            }
+            // ---- state behind the chunk
+            ok = wwait(B_LOC, ph) && ok;
+            tc_fence_after();
+#pragma unroll
+            for (int b = 0; b < NS; b += 32) {
+                float x[32];
+                tmem_ld32(tl + L::T_LOC + half * NS + b, x);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) S[b + e] = fmaf(S[b + e], dec.x, fmaf(S[b + e], dec.y, x[e]));
+            }
+            if (!STATE && cc + 1 < nch) store_state();
+            // ---- outputs: this thread's column v, tokens 32 half .. +31
+            if (!STATE) {
+                ok = wwait(B_Y, ph) && ok;
+                tc_fence_after();
+                float a[32], b[32];
+                tmem_ld32x2(tl + L::T_YI + 32 * half, tl + L::T_YS + 32 * half, a, b);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars[C_Y]);
+                const size_t at = ((size_t)(sg.t0 + c * C + 32 * half) * p.H + h) * D + vv;
+                const size_t step = (size_t)p.H * D;
+#pragma unroll
+                for (int u = 0; u < 32; u += 4) {
+                    const float4 f4 = *reinterpret_cast<const float4*>(fi + 32 * half + u);
+                    const float f[4] = {f4.x, f4.y, f4.z, f4.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float y = fmaf(f[e], b[u + e], a[u + e]);
+                        if (mine && ok && 32 * half + u + e < n) {
+                            if (p.out_f32)
+                                static_cast<float*>(p.out)[at + (u + e) * step] = y;
+                            else
+                                static_cast<__nv_bfloat16*>(p.out)[at + (u + e) * step] = __float2bfloat16_rn(y);
+                        }
+                    }
+                }
+            }
+        }
+        // ---- what is behind the segment
+        float* dst = nullptr;
+        if (STATE)
+            dst = p.local + ((size_t)(sg.first_id + sg.idx) * p.H + h) * DD;
+        else if (p.s_out && sg.idx == (REV ? 0 : sg.count - 1))
+            dst = p.s_out + ((size_t)sg.doc * p.H + h) * DD;
+        if (ok && dst && mine)
+#pragma unroll
+            for (int x = 0; x < NS; ++x) dst[index(x)] = S[x];
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 9) tmem_dealloc(tmem, 512);
+}
+
+// ============================================================================ host side
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiledFn encode_fn() {
+    static EncodeTiledFn fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        cudaDriverEntryPointQueryResult q;
+        void* f = nullptr;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<EncodeTiledFn>(f);
+    });
+    return fn;
+}
+
+// [tokens, heads, d] bf16, boxes of 64 tokens x 1 head x 64 columns; tokens past the end read as zero
+bool make_map(CUtensorMap* m, const void* base, long long tokens, int heads, int d) {
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return false;
+    cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)tokens};
+    cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)heads * d * 2};
+    cuuint32_t box[3] = {64, 1, 64}, es[3] = {1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, es,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, bool REV, bool STATE>
+cudaError_t launch(const LaParams& p, int nseg, cudaStream_t st) {
+    const long long tokens = p.cu ? p.T : (long long)p.num_seqs * p.T;
+    CUtensorMap mq, mk, mv;
+    if (!make_map(&mk, p.k, tokens, p.H / p.kdiv, D) || !make_map(&mv, p.v, tokens, p.H / p.vdiv, D) ||
+        !make_map(&mq, p.q, tokens, p.H / p.qdiv, D))
+        return cudaErrorInvalidValue;
+    constexpr int bytes = TcLayout<D, STATE>::BYTES + 1024;
+    const cudaError_t e = cudaFuncSetAttribute(la_tc_kernel<D, REV, STATE>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+    la_tc_kernel<D, REV, STATE><<<(unsigned)((size_t)nseg * p.H), kTcThreads, bytes, st>>>(mq, mk, mv, p);
+    return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch_d(const LaParams& p, int nseg, cudaStream_t st) {
+    if (p.state_only) return p.reverse ? launch<D, true, true>(p, nseg, st) : launch<D, false, true>(p, nseg, st);
+    return p.reverse ? launch<D, true, false>(p, nseg, st) : launch<D, false, false>(p, nseg, st);
+}
+
+}  // namespace
+
+cudaError_t launch_la_tc(const LaParams& p, int nseg, int d, cudaStream_t st) {
+    return d == 128 ? launch_d<128>(p, nseg, st) : launch_d<64>(p, nseg, st);
+}
+
+}  // namespace gdn

@@ -243,6 +243,17 @@ __device__ __forceinline__ void mma_bf16(uint32_t d_tmem, uint64_t a, uint64_t b
         : "memory");
 }
 
+// The same with A in TMEM: row m in lane m, the 16-bit elements 2 c and 2 c + 1 of K in column c.
+__device__ __forceinline__ void mma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc,
+                                            uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
 // kind::tf32 instruction descriptor, both operands K-major, f32 accumulator.  (On this hardware
 // the MN-major flags give no result for 32-bit operands: transposed operands are stored
 // transposed instead.)  The MMA uses the upper 19 bits of each 32-bit operand (truncation).
@@ -417,6 +428,17 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const float* v) {
         "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};\n\t"
         "tcgen05.wait::st.sync.aligned;" ::"r"(taddr),
         GDN_W8(0), GDN_W8(8), GDN_W8(16), GDN_W8(24)
+        : "memory");
+}
+
+// w[0..15] -> 16 consecutive columns, completed before returning.
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* w) {
+    __syncwarp();
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};\n\t"
+        "tcgen05.wait::st.sync.aligned;" ::"r"(taddr),
+        GDN_W8(0), GDN_W8(8)
         : "memory");
 }
 
