@@ -16,8 +16,10 @@
 //    products; s_final then has fp32 accuracy.  P is rounded to bf16 once (y is bf16).
 //  - A operands in TMEM rather than shared memory: the products are bound by shared-memory bandwidth
 //    (an A of 128 x 16 costs as much of it as a B of 128 columns), which V~ and S^T do not touch.
-// Warps 0-7 compute (two per TMEM lane quadrant), warp 8 loads by TMA through a ring of stages, warp 9
-// issues the products.  Every wait is bounded; one that gives up records GDN_ERR_TIMEOUT.
+// Warps 0-7 prepare a chunk (V~ and P: two warps a TMEM lane quadrant), warps 8-15 finish it (the state,
+// the outputs), so that one chunk's front runs beside its predecessor's back; warp 16 loads by TMA
+// through a ring of stages, warp 17 issues the products.  Full chunks' outputs leave by TMA.
+// Every wait is bounded; one that gives up records GDN_ERR_TIMEOUT.
 #include <mutex>
 
 #include "linear_attn.cuh"
@@ -29,7 +31,7 @@ namespace {
 
 using namespace sm100;
 
-constexpr int kTcThreads = 320;
+constexpr int kTcThreads = 576;
 
 template <int D, bool STATE>
 struct TcLayout {
@@ -40,7 +42,8 @@ struct TcLayout {
     static constexpr int STAGE = NT * TILE;
     static constexpr int P = STAGES * STAGE;      // [j][i] bf16
     static constexpr int EYE = P + 8192;          // 64 x 64 identity
-    static constexpr int TAB = EYE + 8192;        // decay of the scores: [128], zero below 64
+    static constexpr int Y = EYE + 8192;          // outputs on their way to global memory, like a tile
+    static constexpr int TAB = Y + (STATE ? 0 : TILE);  // decay of the scores: [128], zero below 64
     static constexpr int SW = TAB + 512;          // weights of V~: [64]
     static constexpr int FI = SW + 256;           // factors of Ys: [64]
     static constexpr int BAR = FI + 256;
@@ -48,6 +51,7 @@ struct TcLayout {
     static constexpr int BYTES = MISC + 16;
     static constexpr uint32_t T_SC = 0, T_VT = 64, T_V3 = 128, T_LOC = 160, T_YI = 288, T_YS = 352, T_S = 416;
 };
+// B_*: arrivals of copies and products; C_*: of the compute warps (8 each)
 enum { B_FULL = 0, B_EMPTY = 3, B_VT = 6, B_SC, B_LOC, B_Y, C_FIX, C_V, C_P, C_S, C_Y, B_FIN };
 
 __device__ __forceinline__ uint32_t pack_rn(float a, float b) {
@@ -58,12 +62,12 @@ __device__ __forceinline__ uint32_t pack_rn(float a, float b) {
 __device__ __forceinline__ uint32_t pack_hi(float a, float b) {
     return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
 }
-__device__ __forceinline__ float hi_part(float x) { return __uint_as_float(__float_as_uint(x) & 0xffff0000u); }
+constexpr uint64_t kHiMask = 0xffff0000ffff0000ull;  // the bf16 piece of each value of a pair, truncated
 
 template <int D, bool REV, bool STATE>
 __global__ void __launch_bounds__(kTcThreads, 1)
 la_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-             const __grid_constant__ CUtensorMap tm_v, const LaParams p) {
+             const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_y, const LaParams p) {
     using L = TcLayout<D, STATE>;
     constexpr int KB = L::KB, C = kLaChunk;
     const int h = blockIdx.x % p.H, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -87,7 +91,7 @@ la_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
         *never = 0;
         fence_mbar_init();
     }
-    if (warp == 9) tmem_alloc(tmem_slot, 512);
+    if (warp == 17) tmem_alloc(tmem_slot, 512);
     // the identity and the decay of the scores
     for (int e = tid; e < 512; e += kTcThreads) {
         const int r = e >> 3, c = e & 7;
@@ -120,7 +124,7 @@ la_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
     // chunk `cc` of the walk: its place in the segment and its tokens
     auto place = [&](int cc) { return REV ? nch - 1 - cc : cc; };
 
-    if (warp == 8) {
+    if (warp == 16) {
         // ---------------------------------------------------------------- loads
         if (lane == 0) {
             int cc = 0;
@@ -146,7 +150,7 @@ la_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                 mbar_wait(&bars[B_FULL + k % L::STAGES], (k / L::STAGES) & 1, never, 100000000ull);
         }
         __syncwarp();
-    } else if (warp == 9) {
+    } else if (warp == 17) {
         // ---------------------------------------------------------------- products (one lane)
         if (lane == 0) {
             constexpr uint32_t ID_VT = idesc_bf16(128, 64, true, false);
@@ -158,14 +162,13 @@ la_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
             constexpr uint32_t VLBO = D == 128 ? 8192 : 0;
             const uint32_t s0 = smem_u32(sm);
             bool ok = true;
-            for (int cc = 0; cc < nch && ok; ++cc) {
-                const int s = cc % L::STAGES;
-                const uint32_t k = s0 + s * L::STAGE, v = k + L::TILE, q = v + L::TILE;
-                const uint32_t ph = cc & 1;
-                const bool tail = place(cc) * C + C > sg.len;
-                ok = mbar_wait(&bars[B_FULL + s], (cc / L::STAGES) & 1, abort_flag);
-                if (ok && tail) ok = mbar_wait(&bars[C_FIX], 0, abort_flag);
-                if (!ok) break;
+            auto stage = [&](int cc) { return s0 + (cc % L::STAGES) * L::STAGE; };
+            // VT and SC of a chunk: the regions are free once the last LOC and Yi are issued
+            auto front = [&](int cc) {
+                const uint32_t k = stage(cc), v = k + L::TILE, q = v + L::TILE;
+                ok = mbar_wait(&bars[B_FULL + cc % L::STAGES], (cc / L::STAGES) & 1, abort_flag);
+                if (ok && place(cc) * C + C > sg.len) ok = mbar_wait(&bars[C_FIX], 0, abort_flag);
+                if (!ok) return;
                 tc_fence_after();
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
@@ -179,11 +182,18 @@ la_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                         mma_bf16(tmem + L::T_SC, sdesc(k + o, 16, 1024), sdesc(q + o, 16, 1024), ID_SC, kk != 0);
                     }
                     mma_commit(&bars[B_SC]);
-                    // the state before the chunk is stored, and the last chunk's outputs are read
-                    ok = mbar_wait(&bars[C_S], ph, abort_flag) &&
-                         (cc == 0 || mbar_wait(&bars[C_Y], ph ^ 1, abort_flag));
-                    if (!ok) break;
-                    tc_fence_after();
+                }
+            };
+            if (nch > 0) front(0);
+            for (int cc = 0; cc < nch && ok; ++cc) {
+                const uint32_t k = stage(cc), v = k + L::TILE, q = v + L::TILE;
+                const uint32_t ph = cc & 1;
+                // the state before the chunk is stored (and the last LOC read), the last outputs are read
+                ok = mbar_wait(&bars[C_S], ph, abort_flag) &&
+                     (STATE || cc == 0 || mbar_wait(&bars[C_Y], ph ^ 1, abort_flag));
+                if (!ok) break;
+                tc_fence_after();
+                if (!STATE) {
 #pragma unroll
                     for (int kk = 0; kk < 4 * KB; ++kk)
                         mma_bf16_ta(tmem + L::T_YS, tmem + L::T_S + 8 * kk,
@@ -212,7 +222,8 @@ la_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                                  sdesc(s0 + L::P + kk * 2048, 8192, 1024), ID_YI, kk != 0);
                     mma_commit(&bars[B_Y]);
                 }
-                mma_commit(&bars[B_EMPTY + s]);
+                mma_commit(&bars[B_EMPTY + cc % L::STAGES]);
+                if (cc + 1 < nch) front(cc + 1);
             }
             if (!ok && !*abort_flag) fail(B_FIN);
             // no product may still be running when the CTA ends
@@ -220,102 +231,56 @@ la_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
             mbar_wait(&bars[B_FIN], 0, never, 100000000ull);
         }
         __syncwarp();
-    } else {
-        // ---------------------------------------------------------------- compute
+    } else if (warp < 8) {
+        // ---------------------------------------------------------------- front: V~ and P
+        // After a wait that gave up the warps walk on (the waits then return at once), so that all of them
+        // still meet at the named barriers.
         const int quad = warp & 3, half = warp >> 2;
-        const int row = quad * 32 + lane;                 // TMEM lane: the v index (D = 64: twice)
-        const int vv = row & (D - 1);
-        const bool mine = row < D;                        // writes results
         const uint32_t tl = tmem + (static_cast<uint32_t>(quad * 32) << 16);
-        constexpr int NS = D / 2;                         // state columns of this thread: k = half NS ..
-        const size_t DD = (size_t)D * D;
-        float S[NS];
-        auto index = [&](int x) {  // of element x in memory
-            const int k = half * NS + x;
-            return p.state_t ? vv * D + k : k * D + vv;
-        };
-        if (STATE) {
-#pragma unroll
-            for (int x = 0; x < NS; ++x) S[x] = 0.f;
-        } else {
-            const float* s_in = p.s_in ? p.s_in + ((size_t)sg.doc * p.H + h) * DD : nullptr;
-#pragma unroll
-            for (int x = 0; x < NS; ++x) S[x] = s_in ? s_in[index(x)] : 0.f;
-            const int behind = REV ? sg.count - 1 - sg.idx : sg.idx;
-            if (behind > 0) {
-                const float2 all = la_power2(g, p.L);
-                const float2 last = la_power2(g, sg.doc_len - (sg.count - 1) * p.L);
-                for (int b = 0; b < behind; ++b) {
-                    const int r = REV ? sg.count - 1 - b : b;
-                    const float2 w = r == sg.count - 1 ? last : all;
-                    const float* loc = p.local + ((size_t)(sg.first_id + r) * p.H + h) * DD;
-#pragma unroll
-                    for (int x = 0; x < NS; ++x) S[x] = fmaf(S[x], w.x, fmaf(S[x], w.y, loc[index(x)]));
-                }
-            }
-        }
-        // the state in bf16 as the A operand of Ys
-        auto store_state = [&]() {
-            uint32_t w[NS / 2];
-#pragma unroll
-            for (int x = 0; x < NS / 2; ++x) w[x] = pack_rn(S[2 * x], S[2 * x + 1]);
-#pragma unroll
-            for (int x = 0; x < NS / 2; x += 16) tmem_st16(tl + L::T_S + half * (NS / 2) + x, w + x);
-            tc_fence_before();
-            if (lane == 0) mbar_arrive(&bars[C_S]);
-        };
-        if (!STATE && nch > 0) store_state();
-        const float2 dec_full = la_power2(g, C);
-        float2 dec = dec_full;
         int cur_n = -1;
-        // after a wait that gave up the warps walk on (the waits then return at once), so that all of them
-        // still meet at the named barriers; their results are not written
-        bool ok = true;
         for (int cc = 0; cc < nch; ++cc) {
-            const int c = place(cc), n = min(C, sg.len - c * C), s = cc % L::STAGES;
+            const int n = min(C, sg.len - place(cc) * C);
             const uint32_t ph = cc & 1;
-            if (n != cur_n) {  // the tables that depend on the chunk's length
+            if (n != cur_n) {  // the weights depend on the chunk's length
                 named_sync(1, 256);
-                if (tid < C) {
+                if (tid < C)
                     sw[tid] = REV ? expf(g * (float)(tid + 1)) * p.state_scale
                                   : tid < n ? expf(g * (float)(n - 1 - tid)) * p.state_scale : 0.f;
-                    fi[tid] = REV ? (tid < n ? expf(g * (float)(n - 1 - tid)) * p.inter_scale : 0.f)
-                                  : expf(g * (float)(tid + 1)) * p.inter_scale;
-                }
-                dec = n == C ? dec_full : la_power2(g, n);
                 cur_n = n;
                 named_sync(1, 256);
             }
             if (n < C) {
                 // rows past the document's end hold other documents' tokens (or nothing): K and V are zeroed
-                ok = wwait(B_FULL + s, (cc / L::STAGES) & 1) && ok;
+                wwait(B_FULL + cc % L::STAGES, (cc / L::STAGES) & 1);
                 for (int e = tid; e < (C - n) * 8 * 2 * KB; e += 256) {
                     const int r = n + (e >> 3) / (2 * KB), panel = (e >> 3) % (2 * KB);
-                    *reinterpret_cast<uint4*>(sm + s * L::STAGE + panel * 8192 + r * 128 + (e & 7) * 16) =
+                    *reinterpret_cast<uint4*>(sm + (cc % L::STAGES) * L::STAGE + panel * 8192 + r * 128 + (e & 7) * 16) =
                         make_uint4(0, 0, 0, 0);
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bars[C_FIX]);
             }
-            // ---- V~: this thread's row, tokens 32 half .. +31
-            ok = wwait(B_VT, ph) && ok;
+            // ---- V~: row v = 32 quad + lane (D = 64: twice), tokens 32 half .. +31, in three pieces
+            wwait(B_VT, ph);
             tc_fence_after();
             {
                 float x[32];
                 tmem_ld32(tl + L::T_VT + 32 * half, x);
                 uint32_t a[16], b[16], d[16];
+                const uint64_t minus = pair(-1.f, -1.f);
 #pragma unroll
                 for (int u = 0; u < 16; u += 2) {
-                    const float4 w4 = *reinterpret_cast<const float4*>(sw + 32 * half + 2 * u);
-                    const float w[4] = {w4.x, w4.y, w4.z, w4.w};
+                    const float4 w = *reinterpret_cast<const float4*>(sw + 32 * half + 2 * u);
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const float y0 = x[2 * (u + e)] * w[2 * e], y1 = x[2 * (u + e) + 1] * w[2 * e + 1];
-                        const float r0 = y0 - hi_part(y0), r1 = y1 - hi_part(y1);
-                        a[u + e] = pack_hi(y0, y1);
-                        b[u + e] = pack_hi(r0, r1);
-                        d[u + e] = pack_hi(r0 - hi_part(r0), r1 - hi_part(r1));
+                        const uint64_t y = mul2(pair(x[2 * (u + e)], x[2 * (u + e) + 1]),
+                                                e ? pair(w.z, w.w) : pair(w.x, w.y));
+                        const uint64_t r = fma2(y & kHiMask, minus, y);
+                        const uint64_t z = fma2(r & kHiMask, minus, r);
+                        a[u + e] = __byte_perm((uint32_t)y, (uint32_t)(y >> 32), 0x7632);
+                        b[u + e] = __byte_perm((uint32_t)r, (uint32_t)(r >> 32), 0x7632);
+                        d[u + e] = __byte_perm((uint32_t)z, (uint32_t)(z >> 32), 0x7632);
                     }
                 }
                 tmem_st16(tl + L::T_VT + 32 * half, a);
@@ -326,7 +291,7 @@ la_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
             }
             // ---- P: rows j = 16 quad .. +15, columns i = 32 half .. +31
             if (!STATE) {
-                ok = wwait(B_SC, ph) && ok;
+                wwait(B_SC, ph);
                 tc_fence_after();
                 float x[16];
                 tmem_ld_frag<4>(tl + L::T_SC + 32 * half, x);
@@ -339,8 +304,7 @@ la_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                     for (int r = 0; r < 2; ++r) {
                         const float y0 = x[4 * u + 2 * r] * t0[dir * (8 * u - 8 * r)];
                         const float y1 = x[4 * u + 2 * r + 1] * t0[dir * (8 * u + 1 - 8 * r)];
-                        const int j = j0 + 8 * r;
-                        *reinterpret_cast<uint32_t*>(sm + L::P + swz(j, 4 * half + u) + 4 * (lane & 3)) =
+                        *reinterpret_cast<uint32_t*>(sm + L::P + swz(j0 + 8 * r, 4 * half + u) + 4 * (lane & 3)) =
                             pack_rn(y0, y1);
                     }
                 tc_fence_before();
@@ -348,45 +312,157 @@ la_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bars[C_P]);
             }
+        }
+    } else {
+        // ---------------------------------------------------------------- back: the state and the outputs
+        const int wb = warp - 8, quad = wb & 3, half = wb >> 2, tb = tid - 256;
+        const int vv = (quad * 32 + lane) & (D - 1);      // the state's row; D = 64: lanes 64.. repeat it
+        const bool mine = quad * 32 < D;                  // this warp writes results
+        const uint32_t tl = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+        constexpr int NS = D / 2;                         // state columns of this thread: half NS ..
+        const size_t DD = (size_t)D * D;
+        uint64_t S[NS / 2];
+        const float* s_in = !STATE && p.s_in ? p.s_in + ((size_t)sg.doc * p.H + h) * DD : nullptr;
+        // element (v, k) in memory
+        const int at0 = p.state_t ? vv * D + half * NS : half * NS * D + vv, at1 = p.state_t ? 1 : D;
+#pragma unroll
+        for (int x = 0; x < NS / 2; ++x)
+            S[x] = s_in ? pair(s_in[at0 + 2 * x * at1], s_in[at0 + (2 * x + 1) * at1]) : 0;
+        const int behind = STATE ? 0 : REV ? sg.count - 1 - sg.idx : sg.idx;
+        if (behind > 0) {
+            const float2 all = la_power2(g, p.L);
+            const float2 last = la_power2(g, sg.doc_len - (sg.count - 1) * p.L);
+            for (int b = 0; b < behind; ++b) {
+                const int r = REV ? sg.count - 1 - b : b;
+                const float2 w = r == sg.count - 1 ? last : all;
+                const uint64_t wx = pair(w.x, w.x), wy = pair(w.y, w.y);
+                const float* loc = p.local + ((size_t)(sg.first_id + r) * p.H + h) * DD;
+#pragma unroll
+                for (int x = 0; x < NS / 2; ++x)
+                    S[x] = fma2(S[x], wx, fma2(S[x], wy, pair(loc[at0 + 2 * x * at1], loc[at0 + (2 * x + 1) * at1])));
+            }
+        }
+        // the state in bf16 as the A operand of Ys (8 columns of it at a time)
+        auto store_state = [&](int x0) {
+            uint32_t w[8];
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+                float a, b;
+                unpair(S[x0 + x], a, b);
+                w[x] = pack_rn(a, b);
+            }
+            tmem_st8(tl + L::T_S + half * (NS / 2) + x0, w);
+        };
+        if (!STATE) {
+#pragma unroll
+            for (int x = 0; x < NS / 2; x += 8) store_state(x);
+            tc_fence_before();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[C_S]);
+        float2 dec = make_float2(0.f, 0.f);
+        int cur_n = -1;
+        bool ok = true;
+        for (int cc = 0; cc < nch; ++cc) {
+            const int c = place(cc), n = min(C, sg.len - c * C);
+            const uint32_t ph = cc & 1;
+            if (n != cur_n) {  // the factors that depend on the chunk's length
+                if (!STATE) {
+                    named_sync(2, 256);
+                    if (tb < C)
+                        fi[tb] = REV ? (tb < n ? expf(g * (float)(n - 1 - tb)) * p.inter_scale : 0.f)
+                                     : expf(g * (float)(tb + 1)) * p.inter_scale;
+                    named_sync(2, 256);
+                }
+                dec = la_power2(g, n);
+                cur_n = n;
+            }
             // ---- state behind the chunk
             ok = wwait(B_LOC, ph) && ok;
             tc_fence_after();
+            {
+                const uint64_t wx = pair(dec.x, dec.x), wy = pair(dec.y, dec.y);
 #pragma unroll
-            for (int b = 0; b < NS; b += 32) {
-                float x[32];
-                tmem_ld32(tl + L::T_LOC + half * NS + b, x);
+                for (int b = 0; b < NS / 2; b += 8) {
+                    float x[16];
+                    tmem_ld16(tl + L::T_LOC + half * NS + 2 * b, x);
 #pragma unroll
-                for (int e = 0; e < 32; ++e) S[b + e] = fmaf(S[b + e], dec.x, fmaf(S[b + e], dec.y, x[e]));
+                    for (int e = 0; e < 8; ++e)
+                        S[b + e] = fma2(S[b + e], wx, fma2(S[b + e], wy, pair(x[2 * e], x[2 * e + 1])));
+                    if (!STATE) store_state(b);
+                }
             }
-            if (!STATE && cc + 1 < nch) store_state();
-            // ---- outputs: this thread's column v, tokens 32 half .. +31
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars[C_S]);
+            // ---- outputs: columns v = 32 quad .. +31, tokens 32 half .. +31
             if (!STATE) {
+                if (tb == 0) bulk_wait_read();  // the last chunk's outputs have left the staging tile
                 ok = wwait(B_Y, ph) && ok;
                 tc_fence_after();
-                float a[32], b[32];
-                tmem_ld32x2(tl + L::T_YI + 32 * half, tl + L::T_YS + 32 * half, a, b);
+                named_sync(2, 256);
+                const size_t row0 = (size_t)(sg.t0 + c * C), step = (size_t)p.H * D;
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {   // 16 lanes each
+                    float y[16], z[16];
+                    tmem_ld_frag<4>(tl + (16u * r << 16) + L::T_YI + 32 * half, y);
+                    tmem_ld_frag<4>(tl + (16u * r << 16) + L::T_YS + 32 * half, z);
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        const float2 f = *reinterpret_cast<const float2*>(fi + 32 * half + 8 * u + 2 * (lane & 3));
+                        const uint64_t f2 = pair(f.x, f.y);
+#pragma unroll
+                        for (int e = 4 * u; e < 4 * u + 4; e += 2)
+                            unpair(fma2(f2, pair(z[e], z[e + 1]), pair(y[e], y[e + 1])), y[e], y[e + 1]);
+                    }
+                    if (!mine) continue;
+                    if (p.out_f32) {
+                        float* o = static_cast<float*>(p.out) + row0 * step + (size_t)h * D;
+                        if (ok)
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) {
+                                const int i = 32 * half + 8 * (e >> 2) + 2 * (lane & 3) + (e & 1);
+                                const int v = 32 * quad + 16 * r + 8 * ((e >> 1) & 1) + (lane >> 2);
+                                if (i < n) o[(size_t)i * step + v] = y[e];
+                            }
+                    } else {
+                        // transposed into the staging tile, 8 x 8 blocks of (token, v)
+#pragma unroll
+                        for (int u = 0; u < 4; u += 2) {
+                            const int m = lane >> 3;
+                            const int i = 32 * half + 8 * (u + (m >> 1)) + (lane & 7);
+                            const int v8 = 4 * quad + 2 * r + (m & 1);
+                            stsm_x4_t(smem_u32(sm + L::Y + (v8 >> 3) * 8192) + swz(i, v8 & 7),
+                                      pack_rn(y[4 * u], y[4 * u + 1]), pack_rn(y[4 * u + 2], y[4 * u + 3]),
+                                      pack_rn(y[4 * u + 4], y[4 * u + 5]), pack_rn(y[4 * u + 6], y[4 * u + 7]));
+                        }
+                    }
+                }
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bars[C_Y]);
-                const size_t at = ((size_t)(sg.t0 + c * C + 32 * half) * p.H + h) * D + vv;
-                const size_t step = (size_t)p.H * D;
+                if (!p.out_f32) {
+                    fence_proxy_async_smem();
+                    named_sync(2, 256);
+                    if (n == C) {
+                        if (tb == 0 && ok) {
 #pragma unroll
-                for (int u = 0; u < 32; u += 4) {
-                    const float4 f4 = *reinterpret_cast<const float4*>(fi + 32 * half + u);
-                    const float f[4] = {f4.x, f4.y, f4.z, f4.w};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float y = fmaf(f[e], b[u + e], a[u + e]);
-                        if (mine && ok && 32 * half + u + e < n) {
-                            if (p.out_f32)
-                                static_cast<float*>(p.out)[at + (u + e) * step] = y;
-                            else
-                                static_cast<__nv_bfloat16*>(p.out)[at + (u + e) * step] = __float2bfloat16_rn(y);
+                            for (int b = 0; b < KB; ++b)
+                                tma_store_3d(&tm_y, sm + L::Y + b * 8192, 64 * b, h, (int)row0);
+                            bulk_commit();
+                        }
+                    } else if (ok) {  // the document's last rows
+                        __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.out) + row0 * step + (size_t)h * D;
+                        for (int e = tb; e < n * (D / 8); e += 256) {
+                            const int i = e / (D / 8), v8 = e % (D / 8);
+                            *reinterpret_cast<uint4*>(o + (size_t)i * step + 8 * v8) =
+                                *reinterpret_cast<const uint4*>(sm + L::Y + (v8 >> 3) * 8192 + swz(i, v8 & 7));
                         }
                     }
                 }
             }
         }
+        if (!STATE && tb == 0) bulk_wait_read();
         // ---- what is behind the segment
         float* dst = nullptr;
         if (STATE)
@@ -395,12 +471,17 @@ la_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
             dst = p.s_out + ((size_t)sg.doc * p.H + h) * DD;
         if (ok && dst && mine)
 #pragma unroll
-            for (int x = 0; x < NS; ++x) dst[index(x)] = S[x];
+            for (int x = 0; x < NS / 2; ++x) {
+                float a, b;
+                unpair(S[x], a, b);
+                dst[at0 + 2 * x * at1] = a;
+                dst[at0 + (2 * x + 1) * at1] = b;
+            }
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 9) tmem_dealloc(tmem, 512);
+    if (warp == 17) tmem_dealloc(tmem, 512);
 }
 
 // ============================================================================ host side
@@ -435,15 +516,17 @@ bool make_map(CUtensorMap* m, const void* base, long long tokens, int heads, int
 template <int D, bool REV, bool STATE>
 cudaError_t launch(const LaParams& p, int nseg, cudaStream_t st) {
     const long long tokens = p.cu ? p.T : (long long)p.num_seqs * p.T;
-    CUtensorMap mq, mk, mv;
+    CUtensorMap mq, mk, mv, my;
     if (!make_map(&mk, p.k, tokens, p.H / p.kdiv, D) || !make_map(&mv, p.v, tokens, p.H / p.vdiv, D) ||
         !make_map(&mq, p.q, tokens, p.H / p.qdiv, D))
         return cudaErrorInvalidValue;
+    my = mq;
+    if (!STATE && !p.out_f32 && !make_map(&my, p.out, tokens, p.H, D)) return cudaErrorInvalidValue;
     constexpr int bytes = TcLayout<D, STATE>::BYTES + 1024;
     const cudaError_t e = cudaFuncSetAttribute(la_tc_kernel<D, REV, STATE>,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
-    la_tc_kernel<D, REV, STATE><<<(unsigned)((size_t)nseg * p.H), kTcThreads, bytes, st>>>(mq, mk, mv, p);
+    la_tc_kernel<D, REV, STATE><<<(unsigned)((size_t)nseg * p.H), kTcThreads, bytes, st>>>(mq, mk, mv, my, p);
     return cudaGetLastError();
 }
 
