@@ -1,11 +1,10 @@
 // linear_attn_tc.cu -- the bf16 passes of the decayed linear attention on tcgen05.
 //
 // Formulas, roles and segments: linear_attn.cuh.  One CTA per (segment, head) walks its 64-token chunks.
-// With the state kept transposed (row v, column k), a chunk is five products:
-//     VT  = V^T I              (the transposed V, exact, as fp32 in TMEM)
+// With the state kept transposed (row v, column k), a chunk is four products:
 //     SC  = K Q^T              (scores, row j, column i)
+//     LOC = V~ K               V~ = V^T diag(weights), an A operand in TMEM
 //     Ys  = S^T Q^T            S^T in bf16, an A operand in TMEM
-//     LOC = V~ K               V~ = VT diag(weights), an A operand in TMEM
 //     Yi  = V^T P              P = SC decayed and masked, bf16, in shared memory
 // and y_i = Yi + e^{g (i + 1)} Ys, S <- e^{g n} S + LOC.
 //  - The state lives in fp32 registers of the compute warps and is only rounded to bf16 as Ys's
@@ -16,10 +15,11 @@
 //    products; s_final then has fp32 accuracy.  P is rounded to bf16 once (y is bf16).
 //  - A operands in TMEM rather than shared memory: the products are bound by shared-memory bandwidth
 //    (an A of 128 x 16 costs as much of it as a B of 128 columns), which V~ and S^T do not touch.
-// Warps 0-7 prepare a chunk (V~ and P: two warps a TMEM lane quadrant), warps 8-15 finish it (the state,
-// the outputs), so that one chunk's front runs beside its predecessor's back; warp 16 loads by TMA
-// through a ring of stages, warp 17 issues the products.  Full chunks' outputs leave by TMA.
-// Every wait is bounded; one that gives up records GDN_ERR_TIMEOUT.
+// Warps 0-7 prepare a chunk (V~, transposed on the way from shared memory to TMEM by ldmatrix, and P; two
+// warps a TMEM lane quadrant), warps 8-15 finish it (the state, the outputs), so that one chunk's front
+// runs beside its predecessor's back; warp 16 loads by TMA through a ring of stages, warp 17 issues the
+// products.  Full chunks' outputs leave by TMA.  Every wait is bounded; one that gives up records
+// GDN_ERR_TIMEOUT.
 #include <mutex>
 
 #include "linear_attn.cuh"
@@ -31,7 +31,11 @@ namespace {
 
 using namespace sm100;
 
-constexpr int kTcThreads = 576;
+constexpr int kTcThreads = 640;  // five warpgroups, the last with two idle warps
+// Registers a thread: 96 at launch (640 threads), then moved to the back warps, which hold the state.  The
+// shares must not exceed what the block was launched with: 128 (2 x 80 + 2 x 128 + 56) <= 640 x 96.
+constexpr int kLaunchRegs = 96, kFrontRegs = 80, kBackRegs = 128, kIoRegs = 56;
+static_assert(128 * (2 * kFrontRegs + 2 * kBackRegs + kIoRegs) <= kTcThreads * kLaunchRegs, "register shares");
 
 template <int D, bool STATE>
 struct TcLayout {
@@ -41,26 +45,21 @@ struct TcLayout {
     static constexpr int STAGES = 3;
     static constexpr int STAGE = NT * TILE;
     static constexpr int P = STAGES * STAGE;      // [j][i] bf16
-    static constexpr int EYE = P + 8192;          // 64 x 64 identity
-    static constexpr int Y = EYE + 8192;          // outputs on their way to global memory, like a tile
+    static constexpr int Y = P + 8192;            // outputs on their way to global memory, like a tile
     static constexpr int TAB = Y + (STATE ? 0 : TILE);  // decay of the scores: [128], zero below 64
     static constexpr int SW = TAB + 512;          // weights of V~: [64]
     static constexpr int FI = SW + 256;           // factors of Ys: [64]
     static constexpr int BAR = FI + 256;
     static constexpr int MISC = BAR + 16 * 8;     // TMEM base, abort flag, zero word
     static constexpr int BYTES = MISC + 16;
-    static constexpr uint32_t T_SC = 0, T_VT = 64, T_V3 = 128, T_LOC = 160, T_YI = 288, T_YS = 352, T_S = 416;
+    static constexpr uint32_t T_SC = 0, T_V = 64, T_LOC = 160, T_YI = 288, T_YS = 352, T_S = 416;
 };
 // B_*: arrivals of copies and products; C_*: of the compute warps (8 each)
-enum { B_FULL = 0, B_EMPTY = 3, B_VT = 6, B_SC, B_LOC, B_Y, C_FIX, C_V, C_P, C_S, C_Y, B_FIN };
+enum { B_FULL = 0, B_EMPTY = 3, B_SC = 6, B_LOC, B_Y, C_FIX, C_V, C_P, C_L, C_S, C_Y, B_FIN };
 
 __device__ __forceinline__ uint32_t pack_rn(float a, float b) {
     const __nv_bfloat162 x = __floats2bfloat162_rn(a, b);
     return *reinterpret_cast<const uint32_t*>(&x);
-}
-// the upper halves of two words: a (low half) and b
-__device__ __forceinline__ uint32_t pack_hi(float a, float b) {
-    return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
 }
 constexpr uint64_t kHiMask = 0xffff0000ffff0000ull;  // the bf16 piece of each value of a pair, truncated
 
@@ -92,20 +91,10 @@ la_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
         fence_mbar_init();
     }
     if (warp == 17) tmem_alloc(tmem_slot, 512);
-    // the identity and the decay of the scores
-    for (int e = tid; e < 512; e += kTcThreads) {
-        const int r = e >> 3, c = e & 7;
-        uint32_t w[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-            w[u] = r == 8 * c + 2 * u ? 0x3f80u : r == 8 * c + 2 * u + 1 ? 0x3f800000u : 0u;
-        *reinterpret_cast<uint4*>(sm + L::EYE + swz(r, c)) = make_uint4(w[0], w[1], w[2], w[3]);
-    }
     float* tab = reinterpret_cast<float*>(sm + L::TAB);
     float* sw = reinterpret_cast<float*>(sm + L::SW);
     float* fi = reinterpret_cast<float*>(sm + L::FI);
     for (int e = tid; e < 128; e += kTcThreads) tab[e] = e < 64 ? 0.f : expf(g * (float)(e - 64)) * p.p_scale;
-    fence_proxy_async_smem();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -124,6 +113,10 @@ la_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
     // chunk `cc` of the walk: its place in the segment and its tokens
     auto place = [&](int cc) { return REV ? nch - 1 - cc : cc; };
 
+    constexpr bool MOVE = D == 128;  // D = 64 needs no more than 96 registers
+    if (warp >= 16) {
+        if constexpr (MOVE) regs_down<kIoRegs>();
+    }
     if (warp == 16) {
         // ---------------------------------------------------------------- loads
         if (lane == 0) {
@@ -153,7 +146,6 @@ la_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
     } else if (warp == 17) {
         // ---------------------------------------------------------------- products (one lane)
         if (lane == 0) {
-            constexpr uint32_t ID_VT = idesc_bf16(128, 64, true, false);
             constexpr uint32_t ID_SC = idesc_bf16(64, 64, false, false);
             constexpr uint32_t ID_YS = idesc_bf16(128, 64, false, false);
             constexpr uint32_t ID_LOC = idesc_bf16(128, D, false, true);
@@ -163,56 +155,45 @@ la_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
             const uint32_t s0 = smem_u32(sm);
             bool ok = true;
             auto stage = [&](int cc) { return s0 + (cc % L::STAGES) * L::STAGE; };
-            // VT and SC of a chunk: the regions are free once the last LOC and Yi are issued
+            // a chunk is in shared memory; its scores (their region is free: the last P is stored)
             auto front = [&](int cc) {
-                const uint32_t k = stage(cc), v = k + L::TILE, q = v + L::TILE;
+                const uint32_t k = stage(cc), q = k + 2 * L::TILE;
                 ok = mbar_wait(&bars[B_FULL + cc % L::STAGES], (cc / L::STAGES) & 1, abort_flag);
                 if (ok && place(cc) * C + C > sg.len) ok = mbar_wait(&bars[C_FIX], 0, abort_flag);
-                if (!ok) return;
+                if (STATE || !ok) return;
                 tc_fence_after();
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
-                    mma_bf16(tmem + L::T_VT, sdesc(v + kk * 2048, VLBO, 1024), sdesc(s0 + L::EYE + kk * 32, 16, 1024),
-                             ID_VT, kk != 0);
-                mma_commit(&bars[B_VT]);
-                if (!STATE) {
-#pragma unroll
-                    for (int kk = 0; kk < 4 * KB; ++kk) {
-                        const uint32_t o = (kk >> 2) * 8192 + (kk & 3) * 32;
-                        mma_bf16(tmem + L::T_SC, sdesc(k + o, 16, 1024), sdesc(q + o, 16, 1024), ID_SC, kk != 0);
-                    }
-                    mma_commit(&bars[B_SC]);
+                for (int kk = 0; kk < 4 * KB; ++kk) {
+                    const uint32_t o = (kk >> 2) * 8192 + (kk & 3) * 32;
+                    mma_bf16(tmem + L::T_SC, sdesc(k + o, 16, 1024), sdesc(q + o, 16, 1024), ID_SC, kk != 0);
                 }
+                mma_commit(&bars[B_SC]);
             };
             if (nch > 0) front(0);
             for (int cc = 0; cc < nch && ok; ++cc) {
                 const uint32_t k = stage(cc), v = k + L::TILE, q = v + L::TILE;
                 const uint32_t ph = cc & 1;
-                // the state before the chunk is stored (and the last LOC read), the last outputs are read
-                ok = mbar_wait(&bars[C_S], ph, abort_flag) &&
-                     (STATE || cc == 0 || mbar_wait(&bars[C_Y], ph ^ 1, abort_flag));
-                if (!ok) break;
-                tc_fence_after();
-                if (!STATE) {
-#pragma unroll
-                    for (int kk = 0; kk < 4 * KB; ++kk)
-                        mma_bf16_ta(tmem + L::T_YS, tmem + L::T_S + 8 * kk,
-                                    sdesc(q + (kk >> 2) * 8192 + (kk & 3) * 32, 16, 1024), ID_YS, kk != 0);
-                }
-                ok = mbar_wait(&bars[C_V], ph, abort_flag);
+                // V~ is stored; the last LOC is read
+                ok = mbar_wait(&bars[C_V], ph, abort_flag) && (cc == 0 || mbar_wait(&bars[C_L], ph ^ 1, abort_flag));
                 if (!ok) break;
                 tc_fence_after();
 #pragma unroll
                 for (int t = 0; t < 3; ++t)
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk) {
-                        const uint32_t a = t == 2 ? L::T_V3 + 8 * kk
-                                                  : L::T_VT + 32 * (kk >> 1) + 16 * t + 8 * (kk & 1);
-                        mma_bf16_ta(tmem + L::T_LOC, tmem + a, sdesc(k + kk * 2048, 8192, 1024), ID_LOC,
-                                    (t | kk) != 0);
-                    }
+                    for (int kk = 0; kk < 4; ++kk)
+                        mma_bf16_ta(tmem + L::T_LOC, tmem + L::T_V + 32 * t + 8 * kk, sdesc(k + kk * 2048, 8192, 1024),
+                                    ID_LOC, (t | kk) != 0);
                 mma_commit(&bars[B_LOC]);
                 if (!STATE) {
+                    // the state before the chunk is stored; the last outputs are read
+                    ok = mbar_wait(&bars[C_S], ph, abort_flag) &&
+                         (cc == 0 || mbar_wait(&bars[C_Y], ph ^ 1, abort_flag));
+                    if (!ok) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int kk = 0; kk < 4 * KB; ++kk)
+                        mma_bf16_ta(tmem + L::T_YS, tmem + L::T_S + 8 * kk,
+                                    sdesc(q + (kk >> 2) * 8192 + (kk & 3) * 32, 16, 1024), ID_YS, kk != 0);
                     ok = mbar_wait(&bars[C_P], ph, abort_flag);
                     if (!ok) break;
                     tc_fence_after();
@@ -232,6 +213,7 @@ la_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
         }
         __syncwarp();
     } else if (warp < 8) {
+        if constexpr (MOVE) regs_down<kFrontRegs>();
         // ---------------------------------------------------------------- front: V~ and P
         // After a wait that gave up the warps walk on (the waits then return at once), so that all of them
         // still meet at the named barriers.
@@ -249,43 +231,52 @@ la_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                 cur_n = n;
                 named_sync(1, 256);
             }
+            wwait(B_FULL + cc % L::STAGES, (cc / L::STAGES) & 1);
+            uint8_t* stage = sm + (cc % L::STAGES) * L::STAGE;
             if (n < C) {
                 // rows past the document's end hold other documents' tokens (or nothing): K and V are zeroed
-                wwait(B_FULL + cc % L::STAGES, (cc / L::STAGES) & 1);
                 for (int e = tid; e < (C - n) * 8 * 2 * KB; e += 256) {
                     const int r = n + (e >> 3) / (2 * KB), panel = (e >> 3) % (2 * KB);
-                    *reinterpret_cast<uint4*>(sm + (cc % L::STAGES) * L::STAGE + panel * 8192 + r * 128 + (e & 7) * 16) =
-                        make_uint4(0, 0, 0, 0);
+                    *reinterpret_cast<uint4*>(stage + panel * 8192 + r * 128 + (e & 7) * 16) = make_uint4(0, 0, 0, 0);
                 }
                 fence_proxy_async_smem();
-                __syncwarp();
+                named_sync(1, 256);
                 if (lane == 0) mbar_arrive(&bars[C_FIX]);
             }
-            // ---- V~: row v = 32 quad + lane (D = 64: twice), tokens 32 half .. +31, in three pieces
-            wwait(B_VT, ph);
-            tc_fence_after();
+            // ---- V~: rows v = 32 quad .. +31 (D = 64: twice), tokens 32 half .. +31, in three pieces
             {
-                float x[32];
-                tmem_ld32(tl + L::T_VT + 32 * half, x);
-                uint32_t a[16], b[16], d[16];
                 const uint64_t minus = pair(-1.f, -1.f);
+                uint32_t w[2][3][8];
 #pragma unroll
-                for (int u = 0; u < 16; u += 2) {
-                    const float4 w = *reinterpret_cast<const float4*>(sw + 32 * half + 2 * u);
+                for (int r = 0; r < 2; ++r)  // 16 rows each
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const uint64_t y = mul2(pair(x[2 * (u + e)], x[2 * (u + e) + 1]),
-                                                e ? pair(w.z, w.w) : pair(w.x, w.y));
-                        const uint64_t r = fma2(y & kHiMask, minus, y);
-                        const uint64_t z = fma2(r & kHiMask, minus, r);
-                        a[u + e] = __byte_perm((uint32_t)y, (uint32_t)(y >> 32), 0x7632);
-                        b[u + e] = __byte_perm((uint32_t)r, (uint32_t)(r >> 32), 0x7632);
-                        d[u + e] = __byte_perm((uint32_t)z, (uint32_t)(z >> 32), 0x7632);
+                    for (int u = 0; u < 4; u += 2) {
+                        const int m = lane >> 3;
+                        const int j = 32 * half + 8 * (u + (m >> 1)) + (lane & 7);
+                        const int v8 = (4 * quad + 2 * r + (m & 1)) & (D / 8 - 1);
+                        uint32_t x[4];
+                        ldsm_x4_t(smem_u32(stage + L::TILE + (v8 >> 3) * 8192) + swz(j, v8 & 7), x[0], x[1], x[2], x[3]);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float2 f = *reinterpret_cast<const float2*>(sw + 32 * half + 8 * (u + (e >> 1)) +
+                                                                              2 * (lane & 3));
+                            const uint64_t y = mul2(pair(__uint_as_float(x[e] << 16), __uint_as_float(x[e] & 0xffff0000u)),
+                                                    pair(f.x, f.y));
+                            const uint64_t s1 = fma2(y & kHiMask, minus, y);
+                            const uint64_t s2 = fma2(s1 & kHiMask, minus, s1);
+                            w[r][0][2 * u + e] = __byte_perm((uint32_t)y, (uint32_t)(y >> 32), 0x7632);
+                            w[r][1][2 * u + e] = __byte_perm((uint32_t)s1, (uint32_t)(s1 >> 32), 0x7632);
+                            w[r][2][2 * u + e] = __byte_perm((uint32_t)s2, (uint32_t)(s2 >> 32), 0x7632);
+                        }
                     }
-                }
-                tmem_st16(tl + L::T_VT + 32 * half, a);
-                tmem_st16(tl + L::T_VT + 32 * half + 16, b);
-                tmem_st16(tl + L::T_V3 + 16 * half, d);
+                if (cc > 0) wwait(B_LOC, ph ^ 1);  // the last V~ is read
+                tc_fence_after();
+#pragma unroll
+                for (int t = 0; t < 3; ++t)
+#pragma unroll
+                    for (int r = 0; r < 2; ++r)
+                        tmem_st_frag4(tl + (16u * r << 16) + L::T_V + 32 * t + 16 * half, w[r][t]);
+                tmem_st_wait();
                 tc_fence_before();
                 if (lane == 0) mbar_arrive(&bars[C_V]);
             }
@@ -313,8 +304,9 @@ la_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                 if (lane == 0) mbar_arrive(&bars[C_P]);
             }
         }
-    } else {
+    } else if (warp < 16) {
         // ---------------------------------------------------------------- back: the state and the outputs
+        if constexpr (MOVE) regs_up<kBackRegs>();
         const int wb = warp - 8, quad = wb & 3, half = wb >> 2, tb = tid - 256;
         const int vv = (quad * 32 + lane) & (D - 1);      // the state's row; D = 64: lanes 64.. repeat it
         const bool mine = quad * 32 < D;                  // this warp writes results
@@ -342,24 +334,24 @@ la_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                     S[x] = fma2(S[x], wx, fma2(S[x], wy, pair(loc[at0 + 2 * x * at1], loc[at0 + (2 * x + 1) * at1])));
             }
         }
-        // the state in bf16 as the A operand of Ys (8 columns of it at a time)
-        auto store_state = [&](int x0) {
-            uint32_t w[8];
+        // the state in bf16 as the A operand of Ys
+        auto store_state = [&]() {
 #pragma unroll
-            for (int x = 0; x < 8; ++x) {
-                float a, b;
-                unpair(S[x0 + x], a, b);
-                w[x] = pack_rn(a, b);
+            for (int x0 = 0; x0 < NS / 2; x0 += 16) {
+                uint32_t w[16];
+#pragma unroll
+                for (int x = 0; x < 16; ++x) {
+                    float a, b;
+                    unpair(S[x0 + x], a, b);
+                    w[x] = pack_rn(a, b);
+                }
+                tmem_st16(tl + L::T_S + half * (NS / 2) + x0, w);
             }
-            tmem_st8(tl + L::T_S + half * (NS / 2) + x0, w);
-        };
-        if (!STATE) {
-#pragma unroll
-            for (int x = 0; x < NS / 2; x += 8) store_state(x);
             tc_fence_before();
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars[C_S]);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars[C_S]);
+        };
+        if (!STATE) store_state();
         float2 dec = make_float2(0.f, 0.f);
         int cur_n = -1;
         bool ok = true;
@@ -383,23 +375,23 @@ la_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
             {
                 const uint64_t wx = pair(dec.x, dec.x), wy = pair(dec.y, dec.y);
 #pragma unroll
-                for (int b = 0; b < NS / 2; b += 8) {
-                    float x[16];
-                    tmem_ld16(tl + L::T_LOC + half * NS + 2 * b, x);
+                for (int b = 0; b < NS / 2; b += 16) {
+                    float x[32];
+                    tmem_ld32(tl + L::T_LOC + half * NS + 2 * b, x);
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
+                    for (int e = 0; e < 16; ++e)
                         S[b + e] = fma2(S[b + e], wx, fma2(S[b + e], wy, pair(x[2 * e], x[2 * e + 1])));
-                    if (!STATE) store_state(b);
                 }
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bars[C_S]);
+            if (lane == 0) mbar_arrive(&bars[C_L]);
             // ---- outputs: columns v = 32 quad .. +31, tokens 32 half .. +31
             if (!STATE) {
                 if (tb == 0) bulk_wait_read();  // the last chunk's outputs have left the staging tile
-                ok = wwait(B_Y, ph) && ok;
+                ok = wwait(B_Y, ph) && ok;  // Ys has read the state, too
                 tc_fence_after();
+                if (cc + 1 < nch) store_state();
                 named_sync(2, 256);
                 const size_t row0 = (size_t)(sg.t0 + c * C), step = (size_t)p.H * D;
 #pragma unroll
@@ -526,6 +518,12 @@ cudaError_t launch(const LaParams& p, int nseg, cudaStream_t st) {
     const cudaError_t e = cudaFuncSetAttribute(la_tc_kernel<D, REV, STATE>,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
+    if (D == 128) {  // the register shares rest on what the kernel is launched with
+        cudaFuncAttributes at;
+        const cudaError_t f = cudaFuncGetAttributes(&at, la_tc_kernel<D, REV, STATE>);
+        if (f != cudaSuccess) return f;
+        if (at.numRegs < kLaunchRegs) return cudaErrorInvalidConfiguration;
+    }
     la_tc_kernel<D, REV, STATE><<<(unsigned)((size_t)nseg * p.H), kTcThreads, bytes, st>>>(mq, mk, mv, my, p);
     return cudaGetLastError();
 }

@@ -423,6 +423,16 @@ __device__ __forceinline__ void tmem_ld16x3(uint32_t ta, uint32_t tb, uint32_t t
     }
 }
 
+// Registers of the calling warpgroup (four warps, all of which call it): set to N, up or down.
+template <int N>
+__device__ __forceinline__ void regs_up() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_down() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 // v[0..31] -> 32 consecutive columns, completed before returning.
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const float* v) {
     uint32_t w[32];
@@ -438,16 +448,6 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const float* v) {
         : "memory");
 }
 
-// w[0..7] -> 8 consecutive columns, completed before returning.
-__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* w) {
-    __syncwarp();
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n\t"
-        "tcgen05.wait::st.sync.aligned;" ::"r"(taddr),
-        GDN_W8(0)
-        : "memory");
-}
-
 // w[0..15] -> 16 consecutive columns, completed before returning.
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* w) {
     __syncwarp();
@@ -458,6 +458,16 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* w) {
         GDN_W8(0), GDN_W8(8)
         : "memory");
 }
+
+// 16x128b shape over 16 lanes from the lane field of taddr, 16 columns: thread t of the warp gives, for
+// column group g of 4, w[2 g] = (lane + t / 4, column 4 g + t % 4) and w[2 g + 1] = (lane + t / 4 + 8, the same
+// column).  Not complete before tmem_st_wait().
+__device__ __forceinline__ void tmem_st_frag4(uint32_t taddr, const uint32_t* w) {
+    __syncwarp();
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), GDN_W8(0)
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // 16x256b shape over 16 lanes from the lane field of taddr, NG = 2 or 4 groups of 8 columns:
 // thread t of the warp receives, for group g, v[4 g + 0..1] = (lane + t / 4, columns
