@@ -21,6 +21,7 @@
 // products.  Full chunks' outputs leave by TMA.  Every wait is bounded; one that gives up records
 // GDN_ERR_TIMEOUT.
 #include <mutex>
+#include <type_traits>
 
 #include "linear_attn.cuh"
 #include "sm100.cuh"
@@ -144,70 +145,88 @@ la_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
         }
         __syncwarp();
     } else if (warp == 17) {
-        // ---------------------------------------------------------------- products (one lane)
-        if (lane == 0) {
-            constexpr uint32_t ID_SC = idesc_bf16(64, 64, false, false);
-            constexpr uint32_t ID_YS = idesc_bf16(128, 64, false, false);
-            constexpr uint32_t ID_LOC = idesc_bf16(128, D, false, true);
-            constexpr uint32_t ID_YI = idesc_bf16(128, 64, true, true);
-            // V^T as an MN-major A of 128 rows; for D = 64 rows 64..127 repeat rows 0..63 (LBO 0)
-            constexpr uint32_t VLBO = D == 128 ? 8192 : 0;
-            const uint32_t s0 = smem_u32(sm);
-            bool ok = true;
-            auto stage = [&](int cc) { return s0 + (cc % L::STAGES) * L::STAGE; };
-            // a chunk is in shared memory; its scores (their region is free: the last P is stored)
-            auto front = [&](int cc) {
-                const uint32_t k = stage(cc), q = k + 2 * L::TILE;
-                ok = mbar_wait(&bars[B_FULL + cc % L::STAGES], (cc / L::STAGES) & 1, abort_flag);
-                if (ok && place(cc) * C + C > sg.len) ok = mbar_wait(&bars[C_FIX], 0, abort_flag);
-                if (STATE || !ok) return;
-                tc_fence_after();
-#pragma unroll
-                for (int kk = 0; kk < 4 * KB; ++kk) {
-                    const uint32_t o = (kk >> 2) * 8192 + (kk & 3) * 32;
-                    mma_bf16(tmem + L::T_SC, sdesc(k + o, 16, 1024), sdesc(q + o, 16, 1024), ID_SC, kk != 0);
-                }
+        // ---------------------------------------------------------------- products
+        // The whole warp walks; one lane issues.  (With a single lane walking, every product's descriptors
+        // go through vector registers: 110 cycles a product, and the issue alone took 3700 a chunk.)
+        const bool leader = elect_one();
+        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+        constexpr uint32_t ID_SC = idesc_bf16(64, 64, false, false);
+        constexpr uint32_t ID_YS = idesc_bf16(128, 64, false, false);
+        constexpr uint32_t ID_LOC = idesc_bf16(128, D, false, true);
+        constexpr uint32_t ID_YI = idesc_bf16(128, 64, true, true);
+        // V^T as an MN-major A of 128 rows; for D = 64 rows 64..127 repeat rows 0..63 (LBO 0)
+        constexpr uint32_t VLBO = D == 128 ? 8192 : 0;
+        const uint32_t s0 = smem_u32(sm);
+        bool ok = true;
+        auto wait = [&](int bar, uint32_t parity) { return mbar_wait_warp(&bars[bar], parity, abort_flag); };
+        auto stage = [&](int cc) { return s0 + (cc % L::STAGES) * L::STAGE; };
+        // products over the K steps of 16: A and B advance by constants
+        auto steps = [&](auto f) {
+            f(std::integral_constant<int, 0>());
+            f(std::integral_constant<int, 1>());
+            f(std::integral_constant<int, 2>());
+            f(std::integral_constant<int, 3>());
+        };
+        // a chunk is in shared memory; its scores (their region is free: the last P is stored)
+        auto front = [&](int cc) {
+            ok = wait(B_FULL + cc % L::STAGES, (cc / L::STAGES) & 1);
+            if (ok && place(cc) * C + C > sg.len) ok = wait(C_FIX, 0);
+            if (STATE || !ok) return;
+            tc_fence_after();
+            if (leader) {
+                const uint32_t k = desc_lo(stage(cc), 16), q = k + (2 * L::TILE >> 4);
+                steps([&](auto kk) { mma_ss<ID_SC, kk != 0>(tm + L::T_SC, k + 2 * kk, q + 2 * kk); });
+                if constexpr (KB == 2)
+                    steps([&](auto kk) { mma_ss<ID_SC, true>(tm + L::T_SC, k + 512 + 2 * kk, q + 512 + 2 * kk); });
                 mma_commit(&bars[B_SC]);
-            };
-            if (nch > 0) front(0);
-            for (int cc = 0; cc < nch && ok; ++cc) {
-                const uint32_t k = stage(cc), v = k + L::TILE, q = v + L::TILE;
-                const uint32_t ph = cc & 1;
-                // V~ is stored; the last LOC is read
-                ok = mbar_wait(&bars[C_V], ph, abort_flag) && (cc == 0 || mbar_wait(&bars[C_L], ph ^ 1, abort_flag));
+            }
+            __syncwarp();
+        };
+        if (nch > 0) front(0);
+        for (int cc = 0; cc < nch && ok; ++cc) {
+            const uint32_t st = stage(cc), ph = cc & 1;
+            // V~ is stored; the last LOC is read
+            ok = wait(C_V, ph) && (cc == 0 || wait(C_L, ph ^ 1));
+            if (!ok) break;
+            tc_fence_after();
+            if (leader) {
+                const uint32_t k = desc_lo(st, 8192);
+                steps([&](auto kk) { mma_ts<ID_LOC, kk != 0>(tm + L::T_LOC, tm + L::T_V + 8 * kk, k + 128 * kk); });
+                steps([&](auto kk) { mma_ts<ID_LOC, true>(tm + L::T_LOC, tm + L::T_V + 32 + 8 * kk, k + 128 * kk); });
+                steps([&](auto kk) { mma_ts<ID_LOC, true>(tm + L::T_LOC, tm + L::T_V + 64 + 8 * kk, k + 128 * kk); });
+                mma_commit(&bars[B_LOC]);
+            }
+            __syncwarp();
+            if (!STATE) {
+                // the state before the chunk is stored; the last outputs are read
+                ok = wait(C_S, ph) && (cc == 0 || wait(C_Y, ph ^ 1));
                 if (!ok) break;
                 tc_fence_after();
-#pragma unroll
-                for (int t = 0; t < 3; ++t)
-#pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        mma_bf16_ta(tmem + L::T_LOC, tmem + L::T_V + 32 * t + 8 * kk, sdesc(k + kk * 2048, 8192, 1024),
-                                    ID_LOC, (t | kk) != 0);
-                mma_commit(&bars[B_LOC]);
-                if (!STATE) {
-                    // the state before the chunk is stored; the last outputs are read
-                    ok = mbar_wait(&bars[C_S], ph, abort_flag) &&
-                         (cc == 0 || mbar_wait(&bars[C_Y], ph ^ 1, abort_flag));
-                    if (!ok) break;
-                    tc_fence_after();
-#pragma unroll
-                    for (int kk = 0; kk < 4 * KB; ++kk)
-                        mma_bf16_ta(tmem + L::T_YS, tmem + L::T_S + 8 * kk,
-                                    sdesc(q + (kk >> 2) * 8192 + (kk & 3) * 32, 16, 1024), ID_YS, kk != 0);
-                    ok = mbar_wait(&bars[C_P], ph, abort_flag);
-                    if (!ok) break;
-                    tc_fence_after();
-#pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        mma_bf16(tmem + L::T_YI, sdesc(v + kk * 2048, VLBO, 1024),
-                                 sdesc(s0 + L::P + kk * 2048, 8192, 1024), ID_YI, kk != 0);
+                if (leader) {
+                    const uint32_t q = desc_lo(st + 2 * L::TILE, 16);
+                    steps([&](auto kk) { mma_ts<ID_YS, kk != 0>(tm + L::T_YS, tm + L::T_S + 8 * kk, q + 2 * kk); });
+                    if constexpr (KB == 2)
+                        steps([&](auto kk) {
+                            mma_ts<ID_YS, true>(tm + L::T_YS, tm + L::T_S + 32 + 8 * kk, q + 512 + 2 * kk);
+                        });
+                }
+                __syncwarp();
+                ok = wait(C_P, ph);
+                if (!ok) break;
+                tc_fence_after();
+                if (leader) {
+                    const uint32_t v = desc_lo(st + L::TILE, VLBO), pp = desc_lo(s0 + L::P, 8192);
+                    steps([&](auto kk) { mma_ss<ID_YI, kk != 0>(tm + L::T_YI, v + 128 * kk, pp + 128 * kk); });
                     mma_commit(&bars[B_Y]);
                 }
-                mma_commit(&bars[B_EMPTY + cc % L::STAGES]);
-                if (cc + 1 < nch) front(cc + 1);
             }
-            if (!ok && !*abort_flag) fail(B_FIN);
-            // no product may still be running when the CTA ends
+            if (leader) mma_commit(&bars[B_EMPTY + cc % L::STAGES]);
+            __syncwarp();
+            if (cc + 1 < nch) front(cc + 1);
+        }
+        if (!ok && lane == 0 && !*abort_flag) fail(B_FIN);
+        // no product may still be running when the CTA ends
+        if (leader) {
             mma_commit(&bars[B_FIN]);
             mbar_wait(&bars[B_FIN], 0, never, 100000000ull);
         }
