@@ -107,7 +107,7 @@ la_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
         (void)bar;
     };
     auto wwait = [&](int bar, uint32_t parity) {
-        const bool ok = mbar_wait_warp(&bars[bar], parity, abort_flag);
+        const bool ok = mbar_wait_lane(&bars[bar], parity, abort_flag);
         if (!ok && lane == 0) fail(bar);
         return ok;
     };
@@ -158,7 +158,7 @@ la_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
         constexpr uint32_t VLBO = D == 128 ? 8192 : 0;
         const uint32_t s0 = smem_u32(sm);
         bool ok = true;
-        auto wait = [&](int bar, uint32_t parity) { return mbar_wait_warp(&bars[bar], parity, abort_flag); };
+        auto wait = [&](int bar, uint32_t parity) { return mbar_wait_lane(&bars[bar], parity, abort_flag); };
         auto stage = [&](int cc) { return s0 + (cc % L::STAGES) * L::STAGE; };
         // products over the K steps of 16: A and B advance by constants
         auto steps = [&](auto f) {
@@ -265,7 +265,8 @@ la_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
             // ---- V~: rows v = 32 quad .. +31 (D = 64: twice), tokens 32 half .. +31, in three pieces
             {
                 const uint64_t minus = pair(-1.f, -1.f);
-                uint32_t w[2][3][8];
+                uint32_t w[3][16];
+                __syncwarp();
 #pragma unroll
                 for (int r = 0; r < 2; ++r)  // 16 rows each
 #pragma unroll
@@ -283,20 +284,17 @@ la_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                                                     pair(f.x, f.y));
                             const uint64_t s1 = fma2(y & kHiMask, minus, y);
                             const uint64_t s2 = fma2(s1 & kHiMask, minus, s1);
-                            w[r][0][2 * u + e] = __byte_perm((uint32_t)y, (uint32_t)(y >> 32), 0x7632);
-                            w[r][1][2 * u + e] = __byte_perm((uint32_t)s1, (uint32_t)(s1 >> 32), 0x7632);
-                            w[r][2][2 * u + e] = __byte_perm((uint32_t)s2, (uint32_t)(s2 >> 32), 0x7632);
+                            w[0][8 * r + 2 * u + e] = __byte_perm((uint32_t)y, (uint32_t)(y >> 32), 0x7632);
+                            w[1][8 * r + 2 * u + e] = __byte_perm((uint32_t)s1, (uint32_t)(s1 >> 32), 0x7632);
+                            w[2][8 * r + 2 * u + e] = __byte_perm((uint32_t)s2, (uint32_t)(s2 >> 32), 0x7632);
                         }
                     }
                 if (cc > 0) wwait(B_LOC, ph ^ 1);  // the last V~ is read
                 tc_fence_after();
 #pragma unroll
-                for (int t = 0; t < 3; ++t)
-#pragma unroll
-                    for (int r = 0; r < 2; ++r)
-                        tmem_st_frag4(tl + (16u * r << 16) + L::T_V + 32 * t + 16 * half, w[r][t]);
-                tmem_st_wait();
+                for (int t = 0; t < 3; ++t) tmem_st_frag(tl + L::T_V + 32 * t + 16 * half, w[t]);
                 tc_fence_before();
+                __syncwarp();
                 if (lane == 0) mbar_arrive(&bars[C_V]);
             }
             // ---- P: rows j = 16 quad .. +15, columns i = 32 half .. +31
@@ -437,6 +435,7 @@ la_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                                 if (i < n) o[(size_t)i * step + v] = y[e];
                             }
                     } else {
+                        __syncwarp();
                         // transposed into the staging tile, 8 x 8 blocks of (token, v)
 #pragma unroll
                         for (int u = 0; u < 4; u += 2) {

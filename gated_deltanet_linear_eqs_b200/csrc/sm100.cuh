@@ -102,6 +102,35 @@ __device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity,
     return __all_sync(0xffffffffu, ok);
 }
 
+// mbar_wait_warp with one polling lane: 32 lanes' polls of one barrier are served one after the other (190
+// cycles for a phase that is complete, a few with one lane).  The poll is predicated, and every branch here
+// goes by a vote, so the warp stays converged for the warp-collective instructions that follow.
+__device__ __forceinline__ bool mbar_wait_lane(uint64_t* bar, uint32_t parity, const volatile int* abort,
+                                               uint64_t limit_ns = 2000000000ull) {
+    const uint32_t first = (threadIdx.x & 31) == 0;
+    const uint32_t addr = smem_u32(bar);
+    long long c0 = 0;
+#pragma unroll 1
+    for (uint32_t it = 1;; ++it) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p, q;\n\t"
+            "mov.u32 %0, 0;\n\t"
+            "setp.ne.u32 q, %3, 0;\n\t"
+            "@q mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+            "@q selp.u32 %0, 1, 0, p;\n\t}\n"
+            : "=&r"(ok)
+            : "r"(addr), "r"(parity), "r"(first)
+            : "memory");
+        if (__any_sync(0xffffffffu, ok)) return true;
+        if ((it & 63) == 0) {
+            const long long now = clock64();
+            if (c0 == 0) c0 = now;
+            if (__any_sync(0xffffffffu, *abort != 0 || now - c0 > static_cast<long long>(limit_ns) * 2)) return false;
+        }
+    }
+}
+
 // Busy-polling form of mbar_wait for latency-critical waits: test_wait never suspends the
 // thread, so the wait ends within a few cycles of the phase completing.  Same limits and result
 // as mbar_wait.
@@ -483,15 +512,18 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* w) {
         : "memory");
 }
 
-// 16x128b shape over 16 lanes from the lane field of taddr, 16 columns: thread t of the warp gives, for
-// column group g of 4, w[2 g] = (lane + t / 4, column 4 g + t % 4) and w[2 g + 1] = (lane + t / 4 + 8, the same
-// column).  Not complete before tmem_st_wait().
-__device__ __forceinline__ void tmem_st_frag4(uint32_t taddr, const uint32_t* w) {
+// 16x128b shape over 32 lanes (two times 16), 16 columns: thread t of the warp gives, for r = 0, 1 and column
+// group g of 4, w[8 r + 2 g] = (lane 16 r + t / 4, column 4 g + t % 4) and w[8 r + 2 g + 1] = (lane
+// 16 r + t / 4 + 8, the same column).  Completed before returning.
+__device__ __forceinline__ void tmem_st_frag(uint32_t taddr, const uint32_t* w) {
     __syncwarp();
-    asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), GDN_W8(0)
-                 : "memory");
+    asm volatile(
+        "tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%2,%3,%4,%5,%6,%7,%8,%9};\n\t"
+        "tcgen05.st.sync.aligned.16x128b.x4.b32 [%1], {%10,%11,%12,%13,%14,%15,%16,%17};\n\t"
+        "tcgen05.wait::st.sync.aligned;" ::"r"(taddr),
+        "r"(taddr + (16u << 16)), GDN_W8(0), GDN_W8(8)
+        : "memory");
 }
-__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // 16x256b shape over 16 lanes from the lane field of taddr, NG = 2 or 4 groups of 8 columns:
 // thread t of the warp receives, for group g, v[4 g + 0..1] = (lane + t / 4, columns
