@@ -17,7 +17,7 @@
 //    (an A of 128 x 16 costs as much of it as a B of 128 columns), which V~ and S^T do not touch.
 // Warps 0-7 prepare a chunk (V~, transposed on the way from shared memory to TMEM by ldmatrix, and P; two
 // warps a TMEM lane quadrant), warps 8-15 finish it (the state, the outputs), so that one chunk's front
-// runs beside its predecessor's back; warp 16 loads by TMA through a ring of stages, warp 17 issues the
+// runs beside its predecessor's back; warp 16 loads by TMA through a ring of stages, warps 17 and 18 issue the
 // products.  Full chunks' outputs leave by TMA.  Every wait is bounded; one that gives up records
 // GDN_ERR_TIMEOUT.
 #include <mutex>
@@ -32,7 +32,7 @@ namespace {
 
 using namespace sm100;
 
-constexpr int kTcThreads = 640;  // five warpgroups, the last with two idle warps
+constexpr int kTcThreads = 640;  // five warpgroups, the last with an idle warp
 // Registers a thread: 96 at launch (640 threads), then moved to the back warps, which hold the state.  The
 // shares must not exceed what the block was launched with: 128 (2 x 80 + 2 x 128 + 56) <= 640 x 96.
 constexpr int kLaunchRegs = 96, kFrontRegs = 80, kBackRegs = 128, kIoRegs = 56;
@@ -51,12 +51,12 @@ struct TcLayout {
     static constexpr int SW = TAB + 512;          // weights of V~: [64]
     static constexpr int FI = SW + 256;           // factors of Ys: [64]
     static constexpr int BAR = FI + 256;
-    static constexpr int MISC = BAR + 16 * 8;     // TMEM base, abort flag, zero word
+    static constexpr int MISC = BAR + 20 * 8;     // TMEM base, abort flag, zero word
     static constexpr int BYTES = MISC + 16;
     static constexpr uint32_t T_SC = 0, T_V = 64, T_LOC = 160, T_YI = 288, T_YS = 352, T_S = 416;
 };
 // B_*: arrivals of copies and products; C_*: of the compute warps (8 each)
-enum { B_FULL = 0, B_EMPTY = 3, B_SC = 6, B_LOC, B_Y, C_FIX, C_V, C_P, C_L, C_S, C_Y, B_FIN };
+enum { B_FULL = 0, B_EMPTY = 3, B_SC = 6, B_LOC, B_Y, C_FIX, C_V, C_P, C_L, C_S, C_Y, B_FIN, B_COUNT = B_FIN + 2 };
 
 __device__ __forceinline__ uint32_t pack_rn(float a, float b) {
     const __nv_bfloat162 x = __floats2bfloat162_rn(a, b);
@@ -84,9 +84,9 @@ la_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
     volatile int* never = reinterpret_cast<volatile int*>(sm + L::MISC + 8);
     const float g = p.log_decay[h];
     if (tid == 0) {
-        for (int b = 0; b < C_FIX; ++b) mbar_init(&bars[b], 1);
-        for (int b = C_FIX; b < B_FIN; ++b) mbar_init(&bars[b], 8);
-        mbar_init(&bars[B_FIN], 1);
+        // a stage is free when both issuing warps' products have read it
+        for (int b = 0; b < B_COUNT; ++b)
+            mbar_init(&bars[b], b >= C_FIX && b < B_FIN ? 8 : !STATE && b >= B_EMPTY && b < B_SC ? 2 : 1);
         *abort_flag = 0;
         *never = 0;
         fence_mbar_init();
@@ -144,10 +144,12 @@ la_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                 mbar_wait(&bars[B_FULL + k % L::STAGES], (k / L::STAGES) & 1, never, 100000000ull);
         }
         __syncwarp();
-    } else if (warp == 17) {
+    } else if (warp == 17 || (!STATE && warp == 18)) {
         // ---------------------------------------------------------------- products
-        // The whole warp walks; one lane issues.  (With a single lane walking, every product's descriptors
-        // go through vector registers: 110 cycles a product, and the issue alone took 3700 a chunk.)
+        // Two warps issue, SC and LOC the one, Ys and Yi the other: an issuing warp is held while its products
+        // run, and the waits of one chain then run beside the products of the other.  A whole warp walks and
+        // one lane issues.  (With a single lane walking, every product's descriptors go through vector
+        // registers: 110 cycles a product.)
         const bool leader = elect_one();
         const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
         constexpr uint32_t ID_SC = idesc_bf16(64, 64, false, false);
@@ -159,7 +161,6 @@ la_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
         const uint32_t s0 = smem_u32(sm);
         bool ok = true;
         auto wait = [&](int bar, uint32_t parity) { return mbar_wait_lane(&bars[bar], parity, abort_flag); };
-        auto stage = [&](int cc) { return s0 + (cc % L::STAGES) * L::STAGE; };
         // products over the K steps of 16: A and B advance by constants
         auto steps = [&](auto f) {
             f(std::integral_constant<int, 0>());
@@ -167,39 +168,54 @@ la_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
             f(std::integral_constant<int, 2>());
             f(std::integral_constant<int, 3>());
         };
-        // a chunk is in shared memory; its scores (their region is free: the last P is stored)
-        auto front = [&](int cc) {
-            ok = wait(B_FULL + cc % L::STAGES, (cc / L::STAGES) & 1);
-            if (ok && place(cc) * C + C > sg.len) ok = wait(C_FIX, 0);
-            if (STATE || !ok) return;
-            tc_fence_after();
-            if (leader) {
-                const uint32_t k = desc_lo(stage(cc), 16), q = k + (2 * L::TILE >> 4);
-                steps([&](auto kk) { mma_ss<ID_SC, kk != 0>(tm + L::T_SC, k + 2 * kk, q + 2 * kk); });
-                if constexpr (KB == 2)
-                    steps([&](auto kk) { mma_ss<ID_SC, true>(tm + L::T_SC, k + 512 + 2 * kk, q + 512 + 2 * kk); });
-                mma_commit(&bars[B_SC]);
+        int s = 0;             // the chunk's stage
+        uint32_t st = s0;      // and its address
+        uint32_t full_ph = 0;  // the parity of its arrival
+        auto next_stage = [&]() {
+            st += L::STAGE;
+            if (++s == L::STAGES) {
+                s = 0;
+                st = s0;
+                full_ph ^= 1;
             }
-            __syncwarp();
         };
-        if (nch > 0) front(0);
-        for (int cc = 0; cc < nch && ok; ++cc) {
-            const uint32_t st = stage(cc), ph = cc & 1;
-            // V~ is stored; the last LOC is read
-            ok = wait(C_V, ph) && (cc == 0 || wait(C_L, ph ^ 1));
-            if (!ok) break;
-            tc_fence_after();
-            if (leader) {
-                const uint32_t k = desc_lo(st, 8192);
-                steps([&](auto kk) { mma_ts<ID_LOC, kk != 0>(tm + L::T_LOC, tm + L::T_V + 8 * kk, k + 128 * kk); });
-                steps([&](auto kk) { mma_ts<ID_LOC, true>(tm + L::T_LOC, tm + L::T_V + 32 + 8 * kk, k + 128 * kk); });
-                steps([&](auto kk) { mma_ts<ID_LOC, true>(tm + L::T_LOC, tm + L::T_V + 64 + 8 * kk, k + 128 * kk); });
-                mma_commit(&bars[B_LOC]);
+        if (warp == 17) {
+            for (int cc = 0; cc < nch; ++cc, next_stage()) {
+                const uint32_t ph = cc & 1;
+                // the chunk is in shared memory; its scores' region is free (the last P is stored)
+                ok = wait(B_FULL + s, full_ph) && (place(cc) * C + C <= sg.len || wait(C_FIX, 0)) &&
+                     (STATE || cc == 0 || wait(C_P, ph ^ 1));
+                if (!ok) break;
+                tc_fence_after();
+                if (!STATE) {
+                    if (leader) {
+                        const uint32_t k = desc_lo(st, 16), q = k + (2 * L::TILE >> 4);
+                        steps([&](auto kk) { mma_ss<ID_SC, kk != 0>(tm + L::T_SC, k + 2 * kk, q + 2 * kk); });
+                        if constexpr (KB == 2)
+                            steps([&](auto kk) { mma_ss<ID_SC, true>(tm + L::T_SC, k + 512 + 2 * kk, q + 512 + 2 * kk); });
+                        mma_commit(&bars[B_SC]);
+                    }
+                    __syncwarp();
+                }
+                // V~ is stored; the last LOC is read
+                ok = wait(C_V, ph) && (cc == 0 || wait(C_L, ph ^ 1));
+                if (!ok) break;
+                tc_fence_after();
+                if (leader) {
+                    const uint32_t k = desc_lo(st, 8192);
+                    steps([&](auto kk) { mma_ts<ID_LOC, kk != 0>(tm + L::T_LOC, tm + L::T_V + 8 * kk, k + 128 * kk); });
+                    steps([&](auto kk) { mma_ts<ID_LOC, true>(tm + L::T_LOC, tm + L::T_V + 32 + 8 * kk, k + 128 * kk); });
+                    steps([&](auto kk) { mma_ts<ID_LOC, true>(tm + L::T_LOC, tm + L::T_V + 64 + 8 * kk, k + 128 * kk); });
+                    mma_commit(&bars[B_LOC]);
+                    mma_commit(&bars[B_EMPTY + s]);
+                }
+                __syncwarp();
             }
-            __syncwarp();
-            if (!STATE) {
-                // the state before the chunk is stored; the last outputs are read
-                ok = wait(C_S, ph) && (cc == 0 || wait(C_Y, ph ^ 1));
+        } else {
+            for (int cc = 0; cc < nch; ++cc, next_stage()) {
+                const uint32_t ph = cc & 1;
+                // the chunk is in shared memory, the state before it stored, the last outputs read
+                ok = wait(B_FULL + s, full_ph) && wait(C_S, ph) && (cc == 0 || wait(C_Y, ph ^ 1));
                 if (!ok) break;
                 tc_fence_after();
                 if (leader) {
@@ -211,24 +227,23 @@ la_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                         });
                 }
                 __syncwarp();
-                ok = wait(C_P, ph);
+                ok = wait(C_P, ph);  // (V's zeroed rows too: the warps that zero them store P afterwards)
                 if (!ok) break;
                 tc_fence_after();
                 if (leader) {
                     const uint32_t v = desc_lo(st + L::TILE, VLBO), pp = desc_lo(s0 + L::P, 8192);
                     steps([&](auto kk) { mma_ss<ID_YI, kk != 0>(tm + L::T_YI, v + 128 * kk, pp + 128 * kk); });
                     mma_commit(&bars[B_Y]);
+                    mma_commit(&bars[B_EMPTY + s]);
                 }
+                __syncwarp();
             }
-            if (leader) mma_commit(&bars[B_EMPTY + cc % L::STAGES]);
-            __syncwarp();
-            if (cc + 1 < nch) front(cc + 1);
         }
         if (!ok && lane == 0 && !*abort_flag) fail(B_FIN);
         // no product may still be running when the CTA ends
         if (leader) {
-            mma_commit(&bars[B_FIN]);
-            mbar_wait(&bars[B_FIN], 0, never, 100000000ull);
+            mma_commit(&bars[B_FIN + warp - 17]);
+            mbar_wait(&bars[B_FIN + warp - 17], 0, never, 100000000ull);
         }
         __syncwarp();
     } else if (warp < 8) {
@@ -266,6 +281,12 @@ la_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
             {
                 const uint64_t minus = pair(-1.f, -1.f);
                 uint32_t w[3][16];
+                uint64_t f[4];  // of tokens 8 u + 2 (lane % 4) + 0..1
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const float2 x = *reinterpret_cast<const float2*>(sw + 32 * half + 8 * u + 2 * (lane & 3));
+                    f[u] = pair(x.x, x.y);
+                }
                 __syncwarp();
 #pragma unroll
                 for (int r = 0; r < 2; ++r)  // 16 rows each
@@ -278,10 +299,8 @@ la_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                         ldsm_x4_t(smem_u32(stage + L::TILE + (v8 >> 3) * 8192) + swz(j, v8 & 7), x[0], x[1], x[2], x[3]);
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            const float2 f = *reinterpret_cast<const float2*>(sw + 32 * half + 8 * (u + (e >> 1)) +
-                                                                              2 * (lane & 3));
                             const uint64_t y = mul2(pair(__uint_as_float(x[e] << 16), __uint_as_float(x[e] & 0xffff0000u)),
-                                                    pair(f.x, f.y));
+                                                    f[u + (e >> 1)]);
                             const uint64_t s1 = fma2(y & kHiMask, minus, y);
                             const uint64_t s2 = fma2(s1 & kHiMask, minus, s1);
                             w[0][8 * r + 2 * u + e] = __byte_perm((uint32_t)y, (uint32_t)(y >> 32), 0x7632);
@@ -300,6 +319,7 @@ la_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
             // ---- P: rows j = 16 quad .. +15, columns i = 32 half .. +31
             if (!STATE) {
                 wwait(B_SC, ph);
+                if (cc > 0) wwait(B_Y, ph ^ 1);  // the last P is read
                 tc_fence_after();
                 float x[16];
                 tmem_ld_frag<4>(tl + L::T_SC + 32 * half, x);
@@ -390,14 +410,21 @@ la_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
             ok = wwait(B_LOC, ph) && ok;
             tc_fence_after();
             {
-                const uint64_t wx = pair(dec.x, dec.x), wy = pair(dec.y, dec.y);
+                // e^{g n} in one float would be off the same way every time; the rest of it is made up for
+                // every eighth chunk (what entered since then is over-corrected by 8 2^-25 at most)
+                const uint64_t wx = pair(dec.x, dec.x);
 #pragma unroll
                 for (int b = 0; b < NS / 2; b += 16) {
                     float x[32];
                     tmem_ld32(tl + L::T_LOC + half * NS + 2 * b, x);
+                    if ((cc & 7) == 7) {
+                        const uint64_t wy = pair(8.f * dec.y, 8.f * dec.y);
 #pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        S[b + e] = fma2(S[b + e], wx, fma2(S[b + e], wy, pair(x[2 * e], x[2 * e + 1])));
+                        for (int e = 0; e < 16; ++e)
+                            unpair(fma2(S[b + e], wy, pair(x[2 * e], x[2 * e + 1])), x[2 * e], x[2 * e + 1]);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) S[b + e] = fma2(S[b + e], wx, pair(x[2 * e], x[2 * e + 1]));
                 }
             }
             tc_fence_before();
