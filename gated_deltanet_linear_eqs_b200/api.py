@@ -7,8 +7,8 @@ runs in the library's kernels; a non-OK status raises ``GdnError``.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import functools
 
 import torch
 
@@ -581,53 +581,76 @@ def gdn_qsa_indexer(q, k, g, cu_seqlens, max_doc_len, budget=512, stream=None):
     return gdn_qsa_select_blocks(scores, cu_seqlens, budget, stream=stream), k_hat, base, scores
 
 
-def _on(*tensors):
-    """The device that the tensors share, made current for the call (a launch goes to the current
-    device, whatever device its pointers are on)."""
-    dev = None
-    for t in tensors:
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError("every tensor must be a CUDA tensor")
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise ValueError(f"tensors on {dev} and {t.device}: one device is needed")
-    return contextlib.nullcontext() if dev.index == torch.cuda.current_device() else \
-        torch.cuda.device(dev)
+# The calls below serve decode steps of a few microseconds on the GPU, so their checks are kept short: one
+# comparison a tensor, the reasons looked for only when it fails (_refuse), the stream taken as a raw handle.
+
+def _on_device(fn):
+    """Runs the call with its first tensor's device current: a launch goes to the current device, whatever
+    device its pointers are on."""
+    @functools.wraps(fn)
+    def call(first, *args, **kw):
+        dev = first.get_device()
+        if dev < 0 or dev == torch._C._cuda_getDevice():
+            return fn(first, *args, **kw)
+        with torch.cuda.device(dev):
+            return fn(first, *args, **kw)
+    return call
+
+
+def _raw_stream(stream, dev):
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _refuse(t, name, dtype, shape, dev):
+    _need(t, name, dtype, shape)
+    raise ValueError(f"{name} is on device {t.get_device()}, the first tensor on {dev}")
+
+
+def _want(t, name, dtype, shape, dev):
+    """A contiguous tensor of the given type and shape on device dev."""
+    if t is None or t.dtype != dtype or t.shape != shape or t.get_device() != dev or \
+            not t.is_contiguous() or dev < 0:
+        _refuse(t, name, dtype, shape, dev)
 
 
 def _dtype(t, name):
-    if t.dtype not in _DT:
+    dt = t.dtype
+    if dt not in _DT:
         raise ValueError(f"{name} must be bf16 or fp32")
-    return t.dtype
+    return dt
+
+
+@functools.lru_cache(maxsize=1024)
+def _attn_ws_bytes(backward, B, T, H, Hk, dk, dv, num_seqs):
+    n = ctypes.c_size_t(0)
+    _check(_lib().gdn_linear_attn_workspace_bytes(backward, B, T, H, Hk, dk, dv, num_seqs, ctypes.byref(n)),
+           "gdn_linear_attn_workspace_bytes")
+    return int(n.value)
 
 
 def gdn_linear_attn_workspace_bytes(B, T, H, Hk, dk, dv, num_seqs=0, backward=False):
     """Bytes of device scratch of gdn_linear_attn (num_seqs = 0) and gdn_linear_attn_varlen
     (num_seqs documents, B = 1), or of their backward calls."""
-    n = ctypes.c_size_t(0)
-    _check(_lib().gdn_linear_attn_workspace_bytes(int(bool(backward)), B, T, H, Hk, dk, dv,
-                                                  num_seqs, ctypes.byref(n)),
-           "gdn_linear_attn_workspace_bytes")
-    return int(n.value)
+    return _attn_ws_bytes(int(bool(backward)), B, T, H, Hk, dk, dv, num_seqs)
 
 
-def _attn_workspace(q, Hk, dv, num_seqs, backward, ws):
-    B, T, H, dk = q.shape
-    n = gdn_linear_attn_workspace_bytes(B, T, H, Hk, dk, dv, num_seqs, backward)
-    if n == 0:
-        return None, 0
+def _scratch(n, ws, dev):
+    """(the tensor, its pointer, its bytes): ws if given (any contiguous tensor), else n bytes."""
     if ws is None:
-        ws = torch.empty(n, dtype=torch.uint8, device=q.device)
-    elif not ws.is_contiguous():
-        raise ValueError("ws must be contiguous")
-    return ws, ws.numel() * ws.element_size()
+        if n == 0:
+            return None, None, 0
+        ws = torch.empty(n, dtype=torch.uint8, device=dev)
+    elif ws.get_device() != dev or not ws.is_contiguous():
+        raise ValueError("ws must be contiguous and on the other tensors' device")
+    return ws, ws.data_ptr(), ws.numel() * ws.element_size()
 
 
-def _need_attn(q, k, v, log_decay):
-    """Shapes of q [B,T,H,d], k and v [B,T,Hk,d], log_decay [H]; returns (dtype, B, T, H, Hk, d)."""
+def _attn_shapes(q, k, v, log_decay):
+    """Checks q [B,T,H,d], k and v [B,T,Hk,d], log_decay [H]; returns (dtype, device, B, T, H, Hk, d)."""
     dt = _dtype(q, "q/k/v")
     if q.dim() != 4 or k.dim() != 4:
         raise ValueError("q, k and v must be [B, T, heads, d] (packed: [1, T, heads, d] or "
@@ -636,156 +659,170 @@ def _need_attn(q, k, v, log_decay):
     Hk = k.shape[2]
     if Hk < 1 or H % Hk:
         raise ValueError(f"{Hk} heads of k and v cannot be shared by {H} heads of q")
-    _need(q, "q", dt)
-    _need(k, "k", dt, (B, T, Hk, d))
-    _need(v, "v", dt, (B, T, Hk, d))
-    _need(log_decay, "log_decay", torch.float32, (H,))
-    return dt, B, T, H, Hk, d
+    dev = q.get_device()
+    _want(q, "q", dt, (B, T, H, d), dev)
+    _want(k, "k", dt, (B, T, Hk, d), dev)
+    _want(v, "v", dt, (B, T, Hk, d), dev)
+    _want(log_decay, "log_decay", torch.float32, (H,), dev)
+    return dt, dev, B, T, H, Hk, d
 
 
+def _states(t, name, shape, dev, make=False):
+    """An optional fp32 state tensor: checked, or made where it is wanted."""
+    if t is None:
+        return torch.empty(shape, dtype=torch.float32, device=dev) if make else None
+    _want(t, name, torch.float32, shape, dev)
+    return t
+
+
+@_on_device
 def gdn_linear_attn(q, k, v, log_decay, s0=None, scale=1.0, y=None, s_final=None, want_final=True,
                     ws=None, stream=None):
     """Decayed linear attention S_t = e^g S_{t-1} + k_t v_t^T, y_t = scale S_t^T q_t of dense
     sequences: q [B,T,H,d], k and v [B,T,Hk,d] (bf16 or fp32; Hk divides H), log_decay [H] fp32
     (g <= 0, a constant), s0 [B,H,d,d] fp32 or None.  Returns (y, s_final)."""
-    dt, B, T, H, Hk, d = _need_attn(q, k, v, log_decay)
-    _need(s0, "s0", torch.float32, (B, H, d, d), optional=True)
-    with _on(q, k, v, log_decay, s0, y, s_final, ws):
-        y = torch.empty_like(q) if y is None else y
-        _need(y, "y", dt, (B, T, H, d))
-        if s_final is None and want_final:
-            s_final = torch.empty((B, H, d, d), dtype=torch.float32, device=q.device)
-        _need(s_final, "s_final", torch.float32, (B, H, d, d), optional=True)
-        ws, wsb = _attn_workspace(q, Hk, d, 0, False, ws)
-        rc = _lib().gdn_linear_attn(_p(q), _p(k), _p(v), _p(log_decay), _p(s0), _p(y),
-                                    _p(s_final), B, T, H, Hk, d, d, _DT[dt], float(scale), _p(ws),
-                                    wsb, _stream(stream))
-    _check(rc, "gdn_linear_attn")
+    dt, dev, B, T, H, Hk, d = _attn_shapes(q, k, v, log_decay)
+    s0 = _states(s0, "s0", (B, H, d, d), dev)
+    if y is None:
+        y = torch.empty_like(q)
+    else:
+        _want(y, "y", dt, q.shape, dev)
+    s_final = _states(s_final, "s_final", (B, H, d, d), dev, want_final)
+    ws, wsp, wsb = _scratch(_attn_ws_bytes(0, B, T, H, Hk, d, d, 0), ws, dev)
+    rc = _lib().gdn_linear_attn(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), _ptr(s0),
+                                y.data_ptr(), _ptr(s_final), B, T, H, Hk, d, d, _DT[dt], scale, wsp,
+                                wsb, _raw_stream(stream, dev))
+    if rc:
+        _check(rc, "gdn_linear_attn")
     return y, s_final
 
 
+def _packed(q, *more):
+    return tuple(x.unsqueeze(0) for x in (q, *more)) if q.dim() == 3 else (q, *more)
+
+
+def _documents(B, cu_seqlens, dev):
+    if B != 1:
+        raise ValueError("packed documents are one stream: q must be [1, T, H, d] or [T, H, d]")
+    n = cu_seqlens.numel()
+    _want(cu_seqlens, "cu_seqlens", torch.int32, (n,), dev)
+    return n - 1
+
+
+@_on_device
 def gdn_linear_attn_varlen(q, k, v, log_decay, cu_seqlens, s0=None, scale=1.0, y=None,
                            s_final=None, want_final=True, ws=None, stream=None):
     """gdn_linear_attn of packed documents: q [1,T,H,d] or [T,H,d] (k, v likewise), cu_seqlens
     int32 [N+1] on the device, s0 [N,H,d,d] fp32 or None.  Returns (y like q, s_final)."""
-    shape = q.shape
-    if q.dim() == 3:
-        q, k, v = (x.unsqueeze(0) for x in (q, k, v))
-    dt, B, T, H, Hk, d = _need_attn(q, k, v, log_decay)
-    if B != 1:
-        raise ValueError("packed documents are one stream: q must be [1, T, H, d] or [T, H, d]")
-    _need(cu_seqlens, "cu_seqlens", torch.int32)
-    N = cu_seqlens.numel() - 1
-    _need(s0, "s0", torch.float32, (N, H, d, d), optional=True)
-    with _on(q, k, v, log_decay, cu_seqlens, s0, y, s_final, ws):
-        y = torch.empty(shape, dtype=dt, device=q.device) if y is None else y
-        _need(y, "y", dt, shape)
-        if s_final is None and want_final:
-            s_final = torch.empty((N, H, d, d), dtype=torch.float32, device=q.device)
-        _need(s_final, "s_final", torch.float32, (N, H, d, d), optional=True)
-        ws, wsb = _attn_workspace(q, Hk, d, N, False, ws)
-        rc = _lib().gdn_linear_attn_varlen(_p(q), _p(k), _p(v), _p(log_decay), _p(cu_seqlens), N,
-                                           _p(s0), _p(y), _p(s_final), T, H, Hk, d, d, _DT[dt],
-                                           float(scale), _p(ws), wsb, _stream(stream))
-    _check(rc, "gdn_linear_attn_varlen")
+    if y is None:
+        y = torch.empty_like(q)
+    else:
+        _want(y, "y", q.dtype, q.shape, q.get_device())
+    q, k, v = _packed(q, k, v)
+    dt, dev, B, T, H, Hk, d = _attn_shapes(q, k, v, log_decay)
+    N = _documents(B, cu_seqlens, dev)
+    s0 = _states(s0, "s0", (N, H, d, d), dev)
+    s_final = _states(s_final, "s_final", (N, H, d, d), dev, want_final)
+    ws, wsp, wsb = _scratch(_attn_ws_bytes(0, 1, T, H, Hk, d, d, N), ws, dev)
+    rc = _lib().gdn_linear_attn_varlen(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
+                                       cu_seqlens.data_ptr(), N, _ptr(s0), y.data_ptr(), _ptr(s_final), T,
+                                       H, Hk, d, d, _DT[dt], scale, wsp, wsb, _raw_stream(stream, dev))
+    if rc:
+        _check(rc, "gdn_linear_attn_varlen")
     return y, s_final
 
 
+@_on_device
 def gdn_linear_attn_decode_step(q, k, v, log_decay, state, scale=1.0, y=None, stream=None):
     """One token of N sequences: q [N,H,d], k and v [N,Hk,d], state [N,H,d,d] fp32 (updated in
     place).  Returns y [N,H,d]."""
     dt = _dtype(q, "q/k/v")
     N, H, d = q.shape
     Hk = k.shape[1]
-    _need(q, "q", dt)
-    _need(k, "k", dt, (N, Hk, d))
-    _need(v, "v", dt, (N, Hk, d))
-    _need(log_decay, "log_decay", torch.float32, (H,))
-    _need(state, "state", torch.float32, (N, H, d, d))
-    with _on(q, k, v, log_decay, state, y):
-        y = torch.empty_like(q) if y is None else y
-        _need(y, "y", dt, (N, H, d))
-        rc = _lib().gdn_linear_attn_decode_step(_p(q), _p(k), _p(v), _p(log_decay), _p(state),
-                                                _p(y), N, H, Hk, d, d, _DT[dt], float(scale),
-                                                _stream(stream))
-    _check(rc, "gdn_linear_attn_decode_step")
+    dev = q.get_device()
+    _want(q, "q", dt, (N, H, d), dev)
+    _want(k, "k", dt, (N, Hk, d), dev)
+    _want(v, "v", dt, (N, Hk, d), dev)
+    _want(log_decay, "log_decay", torch.float32, (H,), dev)
+    _want(state, "state", torch.float32, (N, H, d, d), dev)
+    if y is None:
+        y = torch.empty_like(q)
+    else:
+        _want(y, "y", dt, q.shape, dev)
+    rc = _lib().gdn_linear_attn_decode_step(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
+                                            state.data_ptr(), y.data_ptr(), N, H, Hk, d, d, _DT[dt],
+                                            scale, _raw_stream(stream, dev))
+    if rc:
+        _check(rc, "gdn_linear_attn_decode_step")
     return y
 
 
+@_on_device
 def gdn_linear_attn_backward(q, k, v, log_decay, dy, s0=None, ds_final=None, scale=1.0,
                              want_ds0=True, ws=None, stream=None):
     """Gradients of gdn_linear_attn's (y, s_final) given dy [B,T,H,d] and ds_final.  Returns dict
     dq, dk, dv (like q, k, v) and ds0 [B,H,d,d] (None unless want_ds0)."""
-    dt, B, T, H, Hk, d = _need_attn(q, k, v, log_decay)
-    _need(dy, "dy", dt, q.shape)
-    _need(s0, "s0", torch.float32, (B, H, d, d), optional=True)
-    _need(ds_final, "ds_final", torch.float32, (B, H, d, d), optional=True)
-    with _on(q, k, v, log_decay, dy, s0, ds_final, ws):
-        out = dict(dq=torch.empty_like(q), dk=torch.empty_like(k), dv=torch.empty_like(v),
-                   ds0=torch.empty((B, H, d, d), dtype=torch.float32, device=q.device)
-                   if want_ds0 else None)
-        ws, wsb = _attn_workspace(q, Hk, d, 0, True, ws)
-        rc = _lib().gdn_linear_attn_backward(_p(q), _p(k), _p(v), _p(log_decay), _p(s0), _p(dy),
-                                             _p(ds_final), _p(out["dq"]), _p(out["dk"]),
-                                             _p(out["dv"]), _p(out["ds0"]), B, T, H, Hk, d, d,
-                                             _DT[dt], float(scale), _p(ws), wsb, _stream(stream))
-    _check(rc, "gdn_linear_attn_backward")
-    return out
+    dt, dev, B, T, H, Hk, d = _attn_shapes(q, k, v, log_decay)
+    _want(dy, "dy", dt, q.shape, dev)
+    s0 = _states(s0, "s0", (B, H, d, d), dev)
+    ds_final = _states(ds_final, "ds_final", (B, H, d, d), dev)
+    dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+    ds0 = _states(None, "ds0", (B, H, d, d), dev, want_ds0)
+    ws, wsp, wsb = _scratch(_attn_ws_bytes(1, B, T, H, Hk, d, d, 0), ws, dev)
+    rc = _lib().gdn_linear_attn_backward(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
+                                         _ptr(s0), dy.data_ptr(), _ptr(ds_final), dq.data_ptr(),
+                                         dk.data_ptr(), dv.data_ptr(), _ptr(ds0), B, T, H, Hk, d, d,
+                                         _DT[dt], scale, wsp, wsb, _raw_stream(stream, dev))
+    if rc:
+        _check(rc, "gdn_linear_attn_backward")
+    return dict(dq=dq, dk=dk, dv=dv, ds0=ds0)
 
 
+@_on_device
 def gdn_linear_attn_backward_varlen(q, k, v, log_decay, cu_seqlens, dy, s0=None, ds_final=None,
                                     scale=1.0, want_ds0=True, ws=None, stream=None):
     """Gradients of gdn_linear_attn_varlen given dy (like q) and ds_final [N,H,d,d].  Returns
     dict dq, dk, dv (like q, k, v) and ds0 [N,H,d,d] (None unless want_ds0)."""
-    if dy.shape != q.shape:
-        raise ValueError(f"dy must have shape {tuple(q.shape)}, got {tuple(dy.shape)}")
-    shapes = [x.shape for x in (q, k, v)]
-    if q.dim() == 3:
-        q, k, v, dy = (x.unsqueeze(0) for x in (q, k, v, dy))
-    dt, B, T, H, Hk, d = _need_attn(q, k, v, log_decay)
-    if B != 1:
-        raise ValueError("packed documents are one stream: q must be [1, T, H, d] or [T, H, d]")
-    _need(dy, "dy", dt, q.shape)
-    _need(cu_seqlens, "cu_seqlens", torch.int32)
-    N = cu_seqlens.numel() - 1
-    _need(s0, "s0", torch.float32, (N, H, d, d), optional=True)
-    _need(ds_final, "ds_final", torch.float32, (N, H, d, d), optional=True)
-    with _on(q, k, v, log_decay, cu_seqlens, dy, s0, ds_final, ws):
-        out = {n: torch.empty(s, dtype=dt, device=q.device)
-               for n, s in zip(("dq", "dk", "dv"), shapes)}
-        out["ds0"] = torch.empty((N, H, d, d), dtype=torch.float32, device=q.device) \
-            if want_ds0 else None
-        ws, wsb = _attn_workspace(q, Hk, d, N, True, ws)
-        rc = _lib().gdn_linear_attn_backward_varlen(
-            _p(q), _p(k), _p(v), _p(log_decay), _p(cu_seqlens), N, _p(s0), _p(dy), _p(ds_final),
-            _p(out["dq"]), _p(out["dk"]), _p(out["dv"]), _p(out["ds0"]), T, H, Hk, d, d, _DT[dt],
-            float(scale), _p(ws), wsb, _stream(stream))
-    _check(rc, "gdn_linear_attn_backward_varlen")
-    return out
+    _want(dy, "dy", q.dtype, q.shape, q.get_device())
+    dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+    q, k, v = _packed(q, k, v)
+    dt, dev, B, T, H, Hk, d = _attn_shapes(q, k, v, log_decay)
+    N = _documents(B, cu_seqlens, dev)
+    s0 = _states(s0, "s0", (N, H, d, d), dev)
+    ds_final = _states(ds_final, "ds_final", (N, H, d, d), dev)
+    ds0 = _states(None, "ds0", (N, H, d, d), dev, want_ds0)
+    ws, wsp, wsb = _scratch(_attn_ws_bytes(1, 1, T, H, Hk, d, d, N), ws, dev)
+    rc = _lib().gdn_linear_attn_backward_varlen(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), cu_seqlens.data_ptr(), N, _ptr(s0),
+        dy.data_ptr(), _ptr(ds_final), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _ptr(ds0), T, H, Hk, d, d,
+        _DT[dt], scale, wsp, wsb, _raw_stream(stream, dev))
+    if rc:
+        _check(rc, "gdn_linear_attn_backward_varlen")
+    return dict(dq=dq, dk=dk, dv=dv, ds0=ds0)
 
 
-def _need_heads(t, name, dtype, T=None, d=None):
+def _heads(t, name, dtype, dev, tokens=None, heads=None, d=None):
     """A [T, heads, d] or [B, T, heads, d] tensor whose heads are contiguous and whose tokens are a
     fixed distance apart; returns (tokens, heads, d, distance)."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() not in (3, 4):
+    shape, st = t.shape, t.stride()
+    if len(shape) not in (3, 4):
         raise ValueError(f"{name} must be [T, heads, d] or [B, T, heads, d]")
-    h, hd = t.shape[-2:]
-    n = t.numel() // max(1, h * hd)
-    ld = t.stride(-3) if t.shape[-3] > 1 else t.stride(0) if t.dim() == 4 and t.shape[0] > 1 \
-        else h * hd
-    inner = (hd <= 1 or t.stride(-1) == 1) and (h <= 1 or t.stride(-2) == hd)
-    outer = t.dim() == 3 or t.shape[0] <= 1 or t.stride(0) == t.shape[1] * ld
-    if n and not (inner and outer):
+    h, hd = shape[-2:]
+    n = shape[0] if len(shape) == 3 else shape[0] * shape[1]
+    ld = st[-3] if shape[-3] > 1 else st[0] if len(shape) == 4 and shape[0] > 1 else h * hd
+    if t.dtype != dtype or t.get_device() != dev or dev < 0:
+        _need(t, name, dtype)
+        raise ValueError(f"{name} must be {dtype} on the first tensor's device")
+    if n and ((hd > 1 and st[-1] != 1) or (h > 1 and st[-2] != hd) or
+              (len(shape) == 4 and shape[0] > 1 and st[0] != shape[1] * ld)):
         raise ValueError(f"{name}: a token's heads must be contiguous and its tokens evenly spaced")
-    if (T is not None and n != T) or (d is not None and hd != d):
-        raise ValueError(f"{name} must have {T} tokens of heads of {d}")
-    return n, h, hd, max(ld, h * hd)
+    if (tokens is not None and n != tokens) or (heads is not None and h != heads) or \
+            (d is not None and hd != d):
+        raise ValueError(f"{name} has {n} tokens of {h} heads of {hd}; the other tensors do not")
+    return n, h, hd, ld if ld > h * hd or n > 1 else h * hd
 
 
+@_on_device
 def gdn_rotary(q, k, positions, inv_freq, interleaved=False, inverse=False, scale=1.0, q_out=None,
                k_out=None, stream=None):
     """Rotary positions of q [T,Hq,d] and k [T,Hk,d] (or [B,T,..]; k may be None): the first
@@ -794,29 +831,32 @@ def gdn_rotary(q, k, positions, inv_freq, interleaved=False, inverse=False, scal
     views into one projection (contiguous heads, evenly spaced tokens).  positions int32 (one
     per token), inv_freq fp32 on the device.  q_out / k_out may be q / k.  Returns (q_out, k_out)."""
     dt = _dtype(q, "q/k")
-    T, Hq, d, ldq = _need_heads(q, "q", dt)
-    _need(positions, "positions", torch.int32)
+    dev = q.get_device()
+    T, Hq, d, ldq = _heads(q, "q", dt, dev)
+    Hk, ldk, ldko = 0, 0, 0
+    _want(positions, "positions", torch.int32, positions.shape, dev)
     if positions.numel() != T:
         raise ValueError(f"positions must have {T} entries, got {positions.numel()}")
-    _need(inv_freq, "inv_freq", torch.float32)
+    r = 2 * inv_freq.numel()
+    _want(inv_freq, "inv_freq", torch.float32, (r // 2,), dev)
     if k is None:
-        Hk, ldk, k_out = 0, 0, None
+        k_out = None
     else:
-        _, Hk, _, ldk = _need_heads(k, "k", dt, T, d)
-    with _on(q, k, positions, inv_freq, q_out, k_out):
-        if q_out is None:
-            q_out = torch.empty(q.shape, dtype=dt, device=q.device)
-        if k is not None and k_out is None:
-            k_out = torch.empty(k.shape, dtype=dt, device=k.device)
-        _, ho, _, ldqo = _need_heads(q_out, "q_out", dt, T, d)
-        hko, ldko = (0, 0) if k is None else _need_heads(k_out, "k_out", dt, T, d)[1::2]
-        if ho != Hq or hko != Hk:
-            raise ValueError("q_out and k_out must have the heads of q and k")
-        rc = _lib().gdn_rotary(_p(q), _p(k), _p(q_out), _p(k_out), _p(positions), _p(inv_freq), T,
-                               Hq, Hk, d, 2 * inv_freq.numel(), ldq, ldk, ldqo, ldko,
-                               int(bool(interleaved)), int(bool(inverse)), float(scale), _DT[dt],
-                               _stream(stream))
-    _check(rc, "gdn_rotary")
+        _, Hk, _, ldk = _heads(k, "k", dt, dev, T, None, d)
+        if k_out is None:
+            k_out, ldko = torch.empty(k.shape, dtype=dt, device=k.device), Hk * d
+        else:
+            ldko = _heads(k_out, "k_out", dt, dev, T, Hk, d)[3]
+    if q_out is None:
+        q_out, ldqo = torch.empty(q.shape, dtype=dt, device=q.device), Hq * d
+    else:
+        ldqo = _heads(q_out, "q_out", dt, dev, T, Hq, d)[3]
+    rc = _lib().gdn_rotary(q.data_ptr(), _ptr(k), q_out.data_ptr(), _ptr(k_out), positions.data_ptr(),
+                           inv_freq.data_ptr(), T, Hq, Hk, d, r, ldq, ldk, ldqo, ldko,
+                           1 if interleaved else 0, 1 if inverse else 0, scale, _DT[dt],
+                           _raw_stream(stream, dev))
+    if rc:
+        _check(rc, "gdn_rotary")
     return q_out, k_out
 
 
@@ -839,72 +879,80 @@ def gdn_rotary_inv_freq(rotary_dim, base=10000.0, scaling="plain", factor=1.0, o
     return f, float(s.value)
 
 
-def _need_rows(x, w, name):
+def _rows(x, w, name):
+    """Checks x [..., C] and w [C]; returns (dtype, device, shape, C, rows)."""
     dt = _dtype(x, name)
-    C = x.shape[-1]
-    _need(x, name, dt)
-    _need(w, "w", torch.float32, (C,))
-    return dt, C, x.numel() // C if C else 0
+    dev, shape = x.get_device(), x.shape
+    C = shape[-1]
+    _want(x, name, dt, shape, dev)
+    _want(w, "w", torch.float32, (C,), dev)
+    return dt, dev, shape, C, x.numel() // C if C else 0
 
 
+def _like(t, name, dtype, shape, dev, make):
+    if t is not None:
+        _want(t, name, dtype, shape, dev)
+    elif make:
+        t = torch.empty(shape, dtype=dtype, device=dev)
+    return t
+
+
+@_on_device
 def gdn_add_rmsnorm(x, residual, w, eps=1e-6, o=None, h=None, stream=None):
     """h = x + residual, o = (1 + w) h / sqrt(mean(h^2) + eps) over the last axis: x, residual
     [..., C] (bf16 or fp32; residual None: h = x and is not written), w [C] fp32.  h may be x or
-    residual.  Returns (o, h)."""
-    dt, C, rows = _need_rows(x, w, "x")
-    _need(residual, "residual", dt, x.shape, optional=True)
-    with _on(x, residual, w, o, h):
-        o = torch.empty_like(x) if o is None else o
-        _need(o, "o", dt, x.shape)
-        if h is None and residual is not None:
-            h = torch.empty_like(x)
-        _need(h, "h", dt, x.shape, optional=True)
-        rc = _lib().gdn_add_rmsnorm(_p(x), _p(residual), _p(w), _p(o), _p(h), rows, C, _DT[dt],
-                                    float(eps), _stream(stream))
-    _check(rc, "gdn_add_rmsnorm")
+    residual, o may be x.  Returns (o, h)."""
+    dt, dev, shape, C, rows = _rows(x, w, "x")
+    if residual is not None:
+        _want(residual, "residual", dt, shape, dev)
+    o = _like(o, "o", dt, shape, dev, True)
+    h = _like(h, "h", dt, shape, dev, residual is not None)
+    rc = _lib().gdn_add_rmsnorm(x.data_ptr(), _ptr(residual), w.data_ptr(), o.data_ptr(), _ptr(h), rows, C,
+                                _DT[dt], eps, _raw_stream(stream, dev))
+    if rc:
+        _check(rc, "gdn_add_rmsnorm")
     return o, x if h is None else h
 
 
+@_on_device
 def gdn_add_rmsnorm_fp8(x, residual, w, eps=1e-6, group=0, o=None, scales=None, h=None,
                         stream=None):
     """gdn_add_rmsnorm with an 8-bit o (float8_e4m3fn) and fp32 scales [..., C / group]: scale =
     max|o| / 448 over each group of columns, group 0 (a whole row) or 128.  Returns (o, scales, h)."""
-    dt, C, rows = _need_rows(x, w, "x")
-    _need(residual, "residual", dt, x.shape, optional=True)
-    group = C if group == 0 else int(group)
+    dt, dev, shape, C, rows = _rows(x, w, "x")
+    if residual is not None:
+        _want(residual, "residual", dt, shape, dev)
+    group = C if group == 0 else group
     if group < 1 or C % group:
         raise ValueError(f"group {group} does not divide {C} columns")
-    with _on(x, residual, w, o, scales, h):
-        if o is None:
-            o = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device)
-        _need(o, "o", torch.float8_e4m3fn, x.shape)
-        sshape = (*x.shape[:-1], C // group)
-        if scales is None:
-            scales = torch.empty(sshape, dtype=torch.float32, device=x.device)
-        _need(scales, "scales", torch.float32, sshape)
-        if h is None and residual is not None:
-            h = torch.empty_like(x)
-        _need(h, "h", dt, x.shape, optional=True)
-        rc = _lib().gdn_add_rmsnorm_fp8(_p(x), _p(residual), _p(w), _p(o), _p(scales), _p(h), rows,
-                                        C, group, _DT[dt], float(eps), _stream(stream))
-    _check(rc, "gdn_add_rmsnorm_fp8")
+    o = _like(o, "o", torch.float8_e4m3fn, shape, dev, True)
+    scales = _like(scales, "scales", torch.float32, (*shape[:-1], C // group), dev, True)
+    h = _like(h, "h", dt, shape, dev, residual is not None)
+    rc = _lib().gdn_add_rmsnorm_fp8(x.data_ptr(), _ptr(residual), w.data_ptr(), o.data_ptr(), scales.data_ptr(),
+                                    _ptr(h), rows, C, group, _DT[dt], eps, _raw_stream(stream, dev))
+    if rc:
+        _check(rc, "gdn_add_rmsnorm_fp8")
     return o, scales, x if h is None else h
 
 
+@functools.lru_cache(maxsize=1024)
+def _norm_ws_bytes(rows, C):
+    return gdn_workspace_bytes(_abi.GDN_OP_ADD_RMSNORM_BACKWARD, 1, rows, 1, C, C) if rows else 0
+
+
+@_on_device
 def gdn_add_rmsnorm_backward(h, w, d_o, d_h=None, eps=1e-6, ws=None, stream=None):
     """Gradients of gdn_add_rmsnorm from the stored h, given d_o and d_h (the gradient of h itself;
     None = 0).  Returns dict dx (like h: the gradient of x and of residual) and dw [C]."""
-    dt, C, rows = _need_rows(h, w, "h")
-    _need(d_o, "d_o", dt, h.shape)
-    _need(d_h, "d_h", dt, h.shape, optional=True)
-    with _on(h, w, d_o, d_h, ws):
-        out = dict(dx=torch.empty_like(h), dw=torch.empty_like(w))
-        wsb = 0
-        if rows:
-            ws, wsb = _workspace(_abi.GDN_OP_ADD_RMSNORM_BACKWARD, h.device, 1, rows, 1, C, C,
-                                 ws=ws)
-        rc = _lib().gdn_add_rmsnorm_backward(_p(h), _p(w), _p(d_o), _p(d_h), _p(out["dx"]),
-                                             _p(out["dw"]), rows, C, _DT[dt], float(eps), _p(ws),
-                                             wsb, _stream(stream))
-    _check(rc, "gdn_add_rmsnorm_backward")
-    return out
+    dt, dev, shape, C, rows = _rows(h, w, "h")
+    _want(d_o, "d_o", dt, shape, dev)
+    if d_h is not None:
+        _want(d_h, "d_h", dt, shape, dev)
+    dx, dw = torch.empty_like(h), torch.empty_like(w)
+    ws, wsp, wsb = _scratch(_norm_ws_bytes(rows, C), ws, dev)
+    rc = _lib().gdn_add_rmsnorm_backward(h.data_ptr(), w.data_ptr(), d_o.data_ptr(), _ptr(d_h), dx.data_ptr(),
+                                         dw.data_ptr(), rows, C, _DT[dt], eps, wsp, wsb,
+                                         _raw_stream(stream, dev))
+    if rc:
+        _check(rc, "gdn_add_rmsnorm_backward")
+    return dict(dx=dx, dw=dw)

@@ -50,6 +50,35 @@ __device__ __forceinline__ void st8(float* p, const float* x) {
     __stcs(reinterpret_cast<float4*>(p), make_float4(x[0], x[1], x[2], x[3]));
     __stcs(reinterpret_cast<float4*>(p) + 1, make_float4(x[4], x[5], x[6], x[7]));
 }
+// 8 values as loaded, unpacked when they are needed (16-bit values take half the registers until then)
+template <typename T>
+struct Raw8 {
+    uint4 u[sizeof(T) / 2];
+    __device__ __forceinline__ void load(const T* p) {
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) u[i] = __ldcs(reinterpret_cast<const uint4*>(p) + i);
+    }
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) u[i] = make_uint4(0, 0, 0, 0);
+    }
+    __device__ __forceinline__ void get(float* x) const {
+        if constexpr (sizeof(T) == 2) {
+            const uint32_t w[4] = {u[0].x, u[0].y, u[0].z, u[0].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                x[2 * j] = __uint_as_float(w[j] << 16);
+                x[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                x[4 * i] = __uint_as_float(u[i].x); x[4 * i + 1] = __uint_as_float(u[i].y);
+                x[4 * i + 2] = __uint_as_float(u[i].z); x[4 * i + 3] = __uint_as_float(u[i].w);
+            }
+        }
+    }
+};
 // the gain's 8 values (read by every row: cached)
 __device__ __forceinline__ void ld_gain(const float* p, float* x) {
     const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
@@ -147,7 +176,7 @@ add_norm_kernel(const T* x, const T* res, const float* __restrict__ w, void* o,
             if ((tid & 31) == 0) s_max[tid >> 5] = top;
             __syncthreads();
             for (int k = 0; k < (int)(blockDim.x >> 5); ++k) top = max_nan(top, s_max[k]);
-            if (tid == 0) scales[row] = top / 448.f;
+            if (tid == 0) scales[row] = top * (1.f / 448.f);
         }
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
@@ -158,20 +187,22 @@ add_norm_kernel(const T* x, const T* res, const float* __restrict__ w, void* o,
                 for (int j = 0; j < 8; ++j) top = max_nan(top, fabsf(v[i][j]));
 #pragma unroll
                 for (int q = 8; q > 0; q >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, q));
-                if (c < nvec && (tid & 15) == 0) scales[row * (C / 128) + c / 16] = top / 448.f;
+                if (c < nvec && (tid & 15) == 0) scales[row * (C / 128) + c / 16] = top * (1.f / 448.f);
             }
             if (c >= nvec) continue;
-            const float scale = top / 448.f;
-            // a group of zeros keeps the scale 0 and gives zeros; one whose scale has no finite
-            // reciprocal is divided
-            const float inv = scale >= FLT_MIN ? 1.f / scale : scale == 0.f ? 0.f : scale;
-            const bool tiny = scale > 0.f && scale < FLT_MIN;
+            float scale = top * (1.f / 448.f);
+            if (scale > 0.f && scale < FLT_MIN) {  // its reciprocal would not be finite
+                scale *= 18446744073709551616.f;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[i][j] *= 18446744073709551616.f;
+            }
+            // a group of zeros keeps the scale 0 and gives zeros
+            const float inv = scale == 0.f ? 0.f : __frcp_rn(scale);
             uint32_t u[2];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const float a = tiny ? v[i][2 * j] / scale : v[i][2 * j] * inv;
-                const float b = tiny ? v[i][2 * j + 1] / scale : v[i][2 * j + 1] * inv;
-                const uint32_t q = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+                const uint32_t q = __nv_cvt_float2_to_fp8x2(make_float2(v[i][2 * j] * inv, v[i][2 * j + 1] * inv),
+                                                            __NV_SATFINITE, __NV_E4M3);
                 u[j / 2] = j % 2 ? u[j / 2] | (q << 16) : q;
             }
             __stcs(reinterpret_cast<uint2*>(static_cast<uint8_t*>(o) + row * C + c * 8), make_uint2(u[0], u[1]));
@@ -194,27 +225,33 @@ add_norm_bwd_kernel(const T* __restrict__ h, const float* __restrict__ w, const 
         for (int j = 0; j < 8; ++j) acc[i][j] = 0.f;
     int turn = 0;
     for (long long row = blockIdx.x; row < rows; row += gridDim.x, turn ^= 1) {
-        float v[NV][8], g[NV][8], s[2] = {0.f, 0.f};
+        // the whole row is asked for before anything waits on it
+        Raw8<T> hv[NV], gv[NV], ev[NV];
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = tid + i * blockDim.x;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[i][j] = g[i][j] = 0.f;
+            hv[i].zero();
+            gv[i].zero();
+            ev[i].zero();
             if (c < nvec) {
-                ld8(h + row * C + c * 8, v[i]);
-                ld8(d_o + row * C + c * 8, g[i]);
+                hv[i].load(h + row * C + c * 8);
+                gv[i].load(d_o + row * C + c * 8);
+                if (d_h) ev[i].load(d_h + row * C + c * 8);
             }
         }
+        float s[2] = {0.f, 0.f};
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = tid + i * blockDim.x;
             if (c >= nvec) continue;
-            float gain[8];
+            float gain[8], v[8], g[8];
             ld_gain(w + c * 8, gain);
+            hv[i].get(v);
+            gv[i].get(g);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                s[0] = fmaf(v[i][j], v[i][j], s[0]);
-                s[1] = fmaf(v[i][j], g[i][j] * gain[j], s[1]);
+                s[0] = fmaf(v[j], v[j], s[0]);
+                s[1] = fmaf(v[j], g[j] * gain[j], s[1]);
             }
         }
         block_sum(s, s_sum[turn]);  // two buffers: the next row's writes need not wait for this one's reads
@@ -224,16 +261,16 @@ add_norm_bwd_kernel(const T* __restrict__ h, const float* __restrict__ w, const 
         for (int i = 0; i < NV; ++i) {
             const int c = tid + i * blockDim.x;
             if (c >= nvec) continue;
-            float gain[8], e[8];
+            float gain[8], v[8], g[8], e[8];
             ld_gain(w + c * 8, gain);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) e[j] = 0.f;
-            if (d_h) ld8(d_h + row * C + c * 8, e);
+            hv[i].get(v);
+            gv[i].get(g);
+            ev[i].get(e);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const float n = v[i][j] * r;
-                acc[i][j] = fmaf(g[i][j], n, acc[i][j]);
-                e[j] = fmaf(r, fmaf(-n, m, g[i][j] * gain[j]), e[j]);
+                const float n = v[j] * r;
+                acc[i][j] = fmaf(g[j], n, acc[i][j]);
+                e[j] = fmaf(r, fmaf(-n, m, g[j] * gain[j]), e[j]);
             }
             st8(dx + row * C + c * 8, e);
         }
@@ -270,8 +307,10 @@ int threads_for(int C, int nv) {
     return (per + 31) / 32 * 32;
 }
 // vectors a thread: as few as keep the block within a warp, else four (a row then needs few warps,
-// and more rows share an SM)
+// and more rows share an SM).  The reverse mode holds three rows and the sums of dw: two, while the block
+// has at most 512 threads.
 int vectors_for(int C) { return C <= 256 ? 1 : C <= 512 ? 2 : kVec; }
+int vectors_for_bwd(int C) { return C <= 256 ? 1 : C <= 8192 ? 2 : kVec; }
 
 template <typename T, int NV>
 cudaError_t launch_fwd(const AddNormArgs& a, cudaStream_t st) {
@@ -312,7 +351,7 @@ cudaError_t launch_bwd(const AddNormArgs& a, cudaStream_t st) {
 }
 template <typename T>
 cudaError_t launch_bwd_type(const AddNormArgs& a, cudaStream_t st) {
-    switch (vectors_for(a.C)) {
+    switch (vectors_for_bwd(a.C)) {
         case 1: return launch_bwd<T, 1>(a, st);
         case 2: return launch_bwd<T, 2>(a, st);
         default: return launch_bwd<T, kVec>(a, st);

@@ -9,83 +9,98 @@ namespace gdn {
 namespace {
 
 // ============================================================================ fp32 kernel
-// One CTA per (segment, head), 256 threads, 64-token chunks on the CUDA cores.  Q^T and K^T (token
-// fastest), V and the state live in shared memory; the products are register tiles: 4 x 4 for
-// the scores, 8 tokens x D/32 columns for the outputs, D/16 x D/16 for the state.
-template <int D>
+// One CTA per (segment, head, VS columns of v), 256 threads, 64-token chunks on the CUDA cores: the columns
+// of the state and of the outputs do not depend on each other, so they are cut over CTAs at the price of
+// computing the scores in each.  Q^T and K^T (token fastest), V and the state's columns live in shared
+// memory; the products are register tiles: 4 x 4 for the scores, 2 tokens x VS/8 columns for the outputs,
+// TK x TV for the state.
+template <int D, int VS>
 struct LaSimt {
     static constexpr int C = kLaChunk;
     static constexpr int LT = C + 4;                 // row stride of the transposed tiles
     static constexpr int QT = 0;                     // [D][LT]
     static constexpr int KT = QT + D * LT;           // [D][LT]
-    static constexpr int V = KT + D * LT;            // [C][D]
-    static constexpr int S = V + C * D;              // [D][D]
-    static constexpr int PT = S + D * D;             // [C][LT]: row j, column i
+    static constexpr int V = KT + D * LT;            // [C][VS]
+    static constexpr int S = V + C * VS;             // [D][VS]
+    static constexpr int PT = S + D * VS;            // [C][LT]: row j, column i
     static constexpr int PW = PT + C * LT;           // e^{g n}, n = 0 .. C
     static constexpr int BYTES = (PW + C + 4) * 4;
+    static constexpr int TK = D == 128 && VS == 64 ? 8 : 4;  // the state's tile of a thread
+    static constexpr int TV = D * VS / 256 / TK;
+    static constexpr int GV = VS / TV;                       // threads across the columns
 };
 
-template <int D, typename T>
+template <int D, int VS>
 __global__ void __launch_bounds__(256)
 la_simt_kernel(const LaParams p) {
-    using M = LaSimt<D>;
+    using M = LaSimt<D, VS>;
     constexpr int C = M::C, LT = M::LT;
     extern __shared__ float sm[];
     float *qt = sm + M::QT, *kt = sm + M::KT, *vs = sm + M::V, *S = sm + M::S, *pt = sm + M::PT,
           *pw = sm + M::PW;
-    const int h = blockIdx.x % p.H, tid = threadIdx.x;
+    const int h = blockIdx.x % p.H, tid = threadIdx.x, c0 = blockIdx.y * VS;
     LaSegment sg;
     if (!la_find_segment(p, blockIdx.x / p.H, &sg)) return;
     if (p.state_only && sg.idx == (p.reverse ? 0 : sg.count - 1)) return;  // nobody starts behind it
     const float g = p.log_decay[h];
     for (int n = tid; n <= C; n += 256) pw[n] = expf(g * (float)n);
 
-    // ---- the state this segment starts from
+    // ---- the state this segment starts from: element e is (k, v column) in memory order
     const size_t DD = (size_t)D * D;
+    auto memory = [&](int e) { return p.state_t ? (c0 + e / D) * D + e % D : e / VS * D + c0 + e % VS; };
+    auto local_at = [&](int e) { return p.state_t ? e % D * VS + e / D : e; };
     if (p.state_only) {
-        for (int e = tid; e < D * D; e += 256) S[e] = 0.f;
+        for (int e = tid; e < D * VS; e += 256) S[e] = 0.f;
     } else {
         const int behind = p.reverse ? sg.count - 1 - sg.idx : sg.idx;
         const float* s_in = p.s_in ? p.s_in + ((size_t)sg.doc * p.H + h) * DD : nullptr;
         const float2 full = la_power2(g, p.L);
         const float2 last = la_power2(g, sg.doc_len - (sg.count - 1) * p.L);
-        for (int e = tid; e < D * D; e += 256) {
-            const int kk = p.state_t ? e % D : e / D, vv = p.state_t ? e / D : e % D;
-            float x = s_in ? s_in[e] : 0.f;
+#pragma unroll 4
+        for (int e = tid; e < D * VS; e += 256) {
+            const int at = memory(e);
+            float x = s_in ? s_in[at] : 0.f;
             for (int b = 0; b < behind; ++b) {
                 const int r = p.reverse ? sg.count - 1 - b : b;
                 const float2 w = r == sg.count - 1 ? last : full;
-                x = fmaf(x, w.x, fmaf(x, w.y, p.local[((size_t)(sg.first_id + r) * p.H + h) * DD + e]));
+                x = fmaf(x, w.x, fmaf(x, w.y, p.local[((size_t)(sg.first_id + r) * p.H + h) * DD + at]));
             }
-            S[kk * D + vv] = x;
+            S[local_at(e)] = x;
         }
     }
-    __syncthreads();
 
     const int nch = (sg.len + C - 1) / C;
-    const T* q = static_cast<const T*>(p.q);
-    const T* k = static_cast<const T*>(p.k);
-    const T* v = static_cast<const T*>(p.v);
+    const float* q = static_cast<const float*>(p.q);
+    const float* k = static_cast<const float*>(p.k);
+    const float* v = static_cast<const float*>(p.v);
     const int Hq = p.H / p.qdiv, Hk = p.H / p.kdiv, Hv = p.H / p.vdiv;
     const int warp = tid >> 5, lane = tid & 31;
     for (int cc = 0; cc < nch; ++cc) {
         const int c = p.reverse ? nch - 1 - cc : cc;
         const int n = min(C, sg.len - c * C);
         const size_t tok = (size_t)sg.t0 + (size_t)c * C;
-        // rows past the end of the document are zero
-        for (int e = tid; e < C * (D / 4); e += 256) {
-            const int i = e / (D / 4), x = (e % (D / 4)) * 4;
-            float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a, w = a;
-            if (i < n) {
-                a = load4(k + ((tok + i) * Hk + h / p.kdiv) * D + x);
-                b = load4(v + ((tok + i) * Hv + h / p.vdiv) * D + x);
-                if (!p.state_only) w = load4(q + ((tok + i) * Hq + h / p.qdiv) * D + x);
+        const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+        __syncthreads();  // the last chunk's tiles are read
+        // rows past the end of the document are zero; a warp takes 8 tokens x 16 columns, so that the
+        // transposed stores fall into different banks
+        {
+            const int i = (warp & 7) * 8 + (lane & 7);
+#pragma unroll
+            for (int x0 = 0; x0 < D; x0 += 16) {
+                const int x = x0 + (lane >> 3) * 4;
+                const float4 a = i < n ? load4(k + ((tok + i) * Hk + h / p.kdiv) * D + x) : zero;
+                kt[(x + 0) * LT + i] = a.x; kt[(x + 1) * LT + i] = a.y;
+                kt[(x + 2) * LT + i] = a.z; kt[(x + 3) * LT + i] = a.w;
+                if (!p.state_only) {
+                    const float4 w = i < n ? load4(q + ((tok + i) * Hq + h / p.qdiv) * D + x) : zero;
+                    qt[(x + 0) * LT + i] = w.x; qt[(x + 1) * LT + i] = w.y;
+                    qt[(x + 2) * LT + i] = w.z; qt[(x + 3) * LT + i] = w.w;
+                }
             }
-            kt[(x + 0) * LT + i] = a.x; kt[(x + 1) * LT + i] = a.y;
-            kt[(x + 2) * LT + i] = a.z; kt[(x + 3) * LT + i] = a.w;
-            qt[(x + 0) * LT + i] = w.x; qt[(x + 1) * LT + i] = w.y;
-            qt[(x + 2) * LT + i] = w.z; qt[(x + 3) * LT + i] = w.w;
-            store4(vs + i * D + x, b);
+        }
+        for (int e = tid; e < C * (VS / 4); e += 256) {
+            const int i = e / (VS / 4), x = (e % (VS / 4)) * 4;
+            store4(vs + i * VS + x, i < n ? load4(v + ((tok + i) * Hv + h / p.vdiv) * D + c0 + x) : zero);
         }
         __syncthreads();
         if (!p.state_only) {
@@ -93,6 +108,7 @@ la_simt_kernel(const LaParams p) {
             {
                 const int j0 = (tid / 16) * 4, i0 = (tid % 16) * 4;
                 float acc[4][4] = {};
+#pragma unroll 8
                 for (int x = 0; x < D; ++x) {
                     const float4 a = load4(kt + x * LT + j0), b = load4(qt + x * LT + i0);
                     const float av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w};
@@ -113,26 +129,30 @@ la_simt_kernel(const LaParams p) {
                 }
             }
             __syncthreads();
-            // ---- outputs: rows 8 warp .. +7, columns lane * D/32 ..
-            constexpr int CPL = D / 32;
-            float acc[8][CPL] = {};
-            const int i0 = warp * 8, c0 = lane * CPL;
+            // ---- outputs: a warp's 8 rows, 2 a thread; VS / 8 columns
+            constexpr int CPL = VS / 8;
+            float acc[2][CPL] = {};
+            const int i0 = warp * 8 + (lane >> 3) * 2, s0 = (lane & 7) * CPL;
             auto product = [&](const float* a, const float* b, int len) {
+#pragma unroll 4
                 for (int x = 0; x < len; ++x) {
-                    const float4 u = load4(a + x * LT + i0), w = load4(a + x * LT + i0 + 4);
-                    const float av[8] = {u.x, u.y, u.z, u.w, w.x, w.y, w.z, w.w};
+                    const float2 u = *reinterpret_cast<const float2*>(a + x * LT + i0);
                     float bv[CPL];
 #pragma unroll
-                    for (int s = 0; s < CPL; ++s) bv[s] = b[x * D + c0 + s];
+                    for (int s = 0; s < CPL; s += 4) {
+                        const float4 w = load4(b + x * VS + s0 + s);
+                        bv[s] = w.x; bv[s + 1] = w.y; bv[s + 2] = w.z; bv[s + 3] = w.w;
+                    }
 #pragma unroll
-                    for (int r = 0; r < 8; ++r)
-#pragma unroll
-                        for (int s = 0; s < CPL; ++s) acc[r][s] = fmaf(av[r], bv[s], acc[r][s]);
+                    for (int s = 0; s < CPL; ++s) {
+                        acc[0][s] = fmaf(u.x, bv[s], acc[0][s]);
+                        acc[1][s] = fmaf(u.y, bv[s], acc[1][s]);
+                    }
                 }
             };
             product(qt, S, D);
 #pragma unroll
-            for (int r = 0; r < 8; ++r) {
+            for (int r = 0; r < 2; ++r) {
                 const int i = i0 + r;
                 const float f = i < n ? pw[p.reverse ? n - 1 - i : i + 1] * p.inter_scale : 0.f;
 #pragma unroll
@@ -140,58 +160,52 @@ la_simt_kernel(const LaParams p) {
             }
             product(pt, vs, C);
 #pragma unroll
-            for (int r = 0; r < 8; ++r) {
-                const int i = i0 + r;
-                if (i >= n) continue;
-                const size_t at = ((tok + i) * p.H + h) * D + c0;
+            for (int r = 0; r < 2; ++r) {
+                if (i0 + r >= n) continue;
+                float* o = static_cast<float*>(p.out) + ((tok + i0 + r) * p.H + h) * D + c0 + s0;
 #pragma unroll
-                for (int s = 0; s < CPL; ++s) {
-                    if (p.out_f32)
-                        static_cast<float*>(p.out)[at + s] = acc[r][s];
-                    else
-                        static_cast<T*>(p.out)[at + s] = from_f32<T>(acc[r][s]);
-                }
+                for (int s = 0; s < CPL; s += 4)
+                    store4(o + s, make_float4(acc[r][s], acc[r][s + 1], acc[r][s + 2], acc[r][s + 3]));
             }
             __syncthreads();  // S is read above
         }
         // ---- state
         {
-            constexpr int R = D / 16;
-            const int k0 = (tid / 16) * R, v0 = (tid % 16) * R;
+            constexpr int TK = M::TK, TV = M::TV;
+            const int k0 = (tid / M::GV) * TK, v0 = (tid % M::GV) * TV;
             const float2 dec = la_power2(g, n);
-            float acc[R][R] = {};
-            for (int j = 0; j < C; j += 4) {
-                float kw[R][4];
+            float acc[TK][TV] = {};
+            for (int j = 0; j < n; j += 4) {  // (rows from n on are zero)
+                float kw[TK][4], f[4];
 #pragma unroll
-                for (int r = 0; r < R; ++r) {
+                for (int u = 0; u < 4; ++u)
+                    f[u] = j + u < n ? pw[p.reverse ? j + u + 1 : n - 1 - j - u] * p.state_scale : 0.f;
+#pragma unroll
+                for (int r = 0; r < TK; ++r) {
                     const float4 a = load4(kt + (k0 + r) * LT + j);
-                    kw[r][0] = a.x; kw[r][1] = a.y; kw[r][2] = a.z; kw[r][3] = a.w;
+                    kw[r][0] = a.x * f[0]; kw[r][1] = a.y * f[1]; kw[r][2] = a.z * f[2]; kw[r][3] = a.w * f[3];
                 }
 #pragma unroll
                 for (int u = 0; u < 4; ++u) {
-                    if (j + u >= n) break;
-                    const float f = pw[p.reverse ? j + u + 1 : n - 1 - j - u] * p.state_scale;
-                    float bv[R];
+                    float bv[TV];
 #pragma unroll
-                    for (int s = 0; s < R; ++s) bv[s] = vs[(j + u) * D + v0 + s];
+                    for (int s = 0; s < TV; ++s) bv[s] = vs[(j + u) * VS + v0 + s];
 #pragma unroll
-                    for (int r = 0; r < R; ++r) {
-                        const float a = kw[r][u] * f;
+                    for (int r = 0; r < TK; ++r)
 #pragma unroll
-                        for (int s = 0; s < R; ++s) acc[r][s] = fmaf(a, bv[s], acc[r][s]);
-                    }
+                        for (int s = 0; s < TV; ++s) acc[r][s] = fmaf(kw[r][u], bv[s], acc[r][s]);
                 }
             }
 #pragma unroll
-            for (int r = 0; r < R; ++r)
+            for (int r = 0; r < TK; ++r)
 #pragma unroll
-                for (int s = 0; s < R; ++s) {
-                    float* x = S + (k0 + r) * D + v0 + s;
+                for (int s = 0; s < TV; ++s) {
+                    float* x = S + (k0 + r) * VS + v0 + s;
                     *x = fmaf(*x, dec.x, fmaf(*x, dec.y, acc[r][s]));
                 }
         }
-        __syncthreads();
     }
+    __syncthreads();
     // ---- what is behind the segment: its local state, or the document's last state
     float* dst = nullptr;
     if (p.state_only)
@@ -199,22 +213,24 @@ la_simt_kernel(const LaParams p) {
     else if (p.s_out && sg.idx == (p.reverse ? 0 : sg.count - 1))
         dst = p.s_out + ((size_t)sg.doc * p.H + h) * DD;
     if (dst)
-        for (int e = tid; e < D * D; e += 256)
-            dst[e] = p.state_t ? S[(e % D) * D + e / D] : S[e];
+        for (int e = tid; e < D * VS; e += 256) dst[memory(e)] = S[local_at(e)];
 }
 
-template <int D, typename T>
+template <int D, int VS>
 cudaError_t launch_simt(const LaParams& p, int nseg, cudaStream_t st) {
-    cudaError_t e = cudaFuncSetAttribute(la_simt_kernel<D, T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         LaSimt<D>::BYTES);
+    cudaError_t e = cudaFuncSetAttribute(la_simt_kernel<D, VS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         LaSimt<D, VS>::BYTES);
     if (e != cudaSuccess) return e;
-    la_simt_kernel<D, T><<<(unsigned)((size_t)nseg * p.H), 256, LaSimt<D>::BYTES, st>>>(p);
+    la_simt_kernel<D, VS><<<dim3((unsigned)((size_t)nseg * p.H), D / VS), 256, LaSimt<D, VS>::BYTES, st>>>(p);
     return cudaGetLastError();
 }
 
 cudaError_t launch_pass(const LaParams& p, int nseg, int d, int dtype, cudaStream_t st) {
     if (dtype == GDN_BF16) return launch_la_tc(p, nseg, d, st);
-    return d == 128 ? launch_simt<128, float>(p, nseg, st) : launch_simt<64, float>(p, nseg, st);
+    // 32 columns a CTA while 64 would leave SMs idle: the scores are then computed once more
+    const bool wide = (long long)nseg * p.H * (d / 64) >= 148;
+    if (d == 128) return wide ? launch_simt<128, 64>(p, nseg, st) : launch_simt<128, 32>(p, nseg, st);
+    return wide ? launch_simt<64, 64>(p, nseg, st) : launch_simt<64, 32>(p, nseg, st);
 }
 
 // ============================================================================ shared heads
@@ -329,14 +345,16 @@ cudaError_t launch_step(const LaStepArgs& a, cudaStream_t st) {
 // ============================================================================ plan
 // One segment per document where the documents alone give every SM work; otherwise segments long
 // enough for their start states (d x d fp32 each) to stay a small part of their tokens.
-LaPlan make_plan(int num_seqs, int T, int H, bool packed) {
+constexpr int kMinSegment[2] = {512, 128};  // bf16, fp32 (whose chunks take about ten times as long)
+
+LaPlan make_plan(int num_seqs, int T, int H, bool packed, int dtype) {
     const long long tokens = packed ? T : (long long)num_seqs * T;
     LaPlan pl;
     pl.L = (T + kLaChunk - 1) / kLaChunk * kLaChunk;
     if ((long long)num_seqs * H < 148) {
         const long long want = (tokens * H + 147) / 148;
         long long L = (want + kLaChunk - 1) / kLaChunk * kLaChunk;
-        if (L < 512) L = 512;
+        if (L < kMinSegment[dtype]) L = kMinSegment[dtype];
         if (L < pl.L) pl.L = (int)L;
     }
     pl.split = pl.L < T;
@@ -349,11 +367,15 @@ size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 }  // namespace
 
 LaLayout la_layout(bool backward, int num_seqs, int T, int H, int Hk, int d, bool packed) {
-    const LaPlan pl = make_plan(num_seqs, T, H, packed);
     const size_t tokens = packed ? (size_t)T : (size_t)num_seqs * T;
     LaLayout l;
     l.off_local = 0;
-    l.off_dk = pl.split ? up256((size_t)pl.nseg * H * d * d * 4) : 0;
+    l.off_dk = 0;
+    for (int dtype : {GDN_BF16, GDN_FP32}) {  // the size serves both types
+        const LaPlan pl = make_plan(num_seqs, T, H, packed, dtype);
+        const size_t n = pl.split ? up256((size_t)pl.nseg * H * d * d * 4) : 0;
+        l.off_dk = n > l.off_dk ? n : l.off_dk;
+    }
     l.off_dv = l.off_dk;
     l.total = l.off_dk;
     if (backward && Hk < H) {
@@ -365,7 +387,7 @@ LaLayout la_layout(bool backward, int num_seqs, int T, int H, int Hk, int d, boo
 
 cudaError_t launch_linear_attn(const LaArgs& a, cudaStream_t st) {
     const bool packed = a.cu_seqlens != nullptr;
-    const LaPlan pl = make_plan(a.num_seqs, a.T, a.H, packed);
+    const LaPlan pl = make_plan(a.num_seqs, a.T, a.H, packed, a.dtype);
     const LaLayout lay = la_layout(a.dy != nullptr, a.num_seqs, a.T, a.H, a.Hk, a.d, packed);
     char* ws = static_cast<char*>(a.ws);
     const int group = a.H / a.Hk;

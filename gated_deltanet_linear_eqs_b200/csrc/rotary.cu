@@ -68,43 +68,64 @@ rotary_kernel(const RotaryArgs p, int tokens, int units) {
     const int hpb = units < kRotThreads ? kRotThreads / units : 1;
     const int hh = units < kRotThreads ? tid / units : 0;
     if (hh >= hpb) return;
-    for (int row = hh; row < nt * heads; row += hpb) {
-        const int t = row / heads;
-        int h = row - t * heads;
-        const RotaryTensor& a = h < p.a[0].heads ? p.a[0] : p.a[1];
-        if (h >= p.a[0].heads) h -= p.a[0].heads;
-        const T* x = static_cast<const T*>(a.x) + (long long)(t0 + t) * a.ldx + (long long)h * p.d;
-        T* y = static_cast<T*>(a.y) + (long long)(t0 + t) * a.ldy + (long long)h * p.d;
-        const float2* w = cs + t * half;
-        for (int u = units < kRotThreads ? tid - hh * units : tid; u < units; u += kRotThreads) {
-            if (u >= turned) {
-                const int at = p.r + (u - turned) * VEC;
-                float v[VEC];
-                rot_load<T, VEC>(x + at, v);
-                rot_store<T, VEC>(y + at, v);
-            } else if constexpr (INTER && VEC > 1) {
-                float v[VEC], o[VEC];
-                rot_load<T, VEC>(x + u * VEC, v);
+    const int u0 = units < kRotThreads ? tid - hh * units : tid;
+    // Two heads a step: both heads' loads are on their way before either is stored.
+    const int rows = nt * heads, step = hpb * (int)gridDim.y;
+    for (int row = hh + hpb * (int)blockIdx.y; row < rows; row += 2 * step) {
+        const T* x[2];
+        T* y[2];
+        const float2* w[2];
+        const bool both = row + step < rows;
 #pragma unroll
-                for (int i = 0; i < VEC / 2; ++i) {
-                    const float2 f = w[u * (VEC / 2) + i];
-                    o[2 * i] = v[2 * i] * f.x - v[2 * i + 1] * f.y;
-                    o[2 * i + 1] = v[2 * i + 1] * f.x + v[2 * i] * f.y;
-                }
-                rot_store<T, VEC>(y + u * VEC, o);
-            } else {
-                const int ia = INTER ? 2 * u : u * VEC, ib = INTER ? 2 * u + 1 : half + u * VEC;
-                float v[VEC], z[VEC], o[VEC], n[VEC];
-                rot_load<T, VEC>(x + ia, v);
-                rot_load<T, VEC>(x + ib, z);
+        for (int b = 0; b < 2; ++b) {
+            const int at = b && both ? row + step : row;
+            const int t = at / heads;
+            int h = at - t * heads;
+            const bool second = h >= p.a[0].heads;
+            if (second) h -= p.a[0].heads;
+            x[b] = static_cast<const T*>(second ? p.a[1].x : p.a[0].x) +
+                   (long long)(t0 + t) * (second ? p.a[1].ldx : p.a[0].ldx) + (long long)h * p.d;
+            y[b] = static_cast<T*>(second ? p.a[1].y : p.a[0].y) +
+                   (long long)(t0 + t) * (second ? p.a[1].ldy : p.a[0].ldy) + (long long)h * p.d;
+            w[b] = cs + t * half;
+        }
+        for (int u = u0; u < units; u += kRotThreads) {
+            const bool turn = u < turned;
+            const int ia = !turn ? p.r + (u - turned) * VEC : INTER ? (VEC > 1 ? u * VEC : 2 * u) : u * VEC;
+            const int ib = INTER ? 2 * u + 1 : half + u * VEC;  // (not of whole interleaved pairs)
+            constexpr bool PAIRS = INTER && VEC > 1;
+            float v[2][VEC], z[2][VEC];
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) {
-                    const float2 f = w[u * VEC + i];
-                    o[i] = v[i] * f.x - z[i] * f.y;
-                    n[i] = z[i] * f.x + v[i] * f.y;
+            for (int b = 0; b < 2; ++b) {
+                if (b && !both) break;
+                rot_load<T, VEC>(x[b] + ia, v[b]);
+                if (!PAIRS && turn) rot_load<T, VEC>(x[b] + ib, z[b]);
+            }
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                if (b && !both) break;
+                if (turn) {
+                    float o[VEC], n[VEC];
+                    if constexpr (PAIRS) {
+#pragma unroll
+                        for (int i = 0; i < VEC / 2; ++i) {
+                            const float2 f = w[b][u * (VEC / 2) + i];
+                            o[2 * i] = v[b][2 * i] * f.x - v[b][2 * i + 1] * f.y;
+                            o[2 * i + 1] = v[b][2 * i + 1] * f.x + v[b][2 * i] * f.y;
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < VEC; ++i) {
+                            const float2 f = w[b][u * VEC + i];
+                            o[i] = v[b][i] * f.x - z[b][i] * f.y;
+                            n[i] = z[b][i] * f.x + v[b][i] * f.y;
+                        }
+                        rot_store<T, VEC>(y[b] + ib, n);
+                    }
+                    rot_store<T, VEC>(y[b] + ia, o);
+                } else {
+                    rot_store<T, VEC>(y[b] + ia, v[b]);
                 }
-                rot_store<T, VEC>(y + ia, o);
-                rot_store<T, VEC>(y + ib, n);
             }
         }
     }
@@ -114,12 +135,17 @@ template <typename T, int VEC, bool INTER>
 cudaError_t launch(const RotaryArgs& a, bool keep, cudaStream_t st) {
     const int turned = INTER && VEC > 1 ? a.r / VEC : a.r / 2 / VEC;
     const int units = turned + (keep ? (a.d - a.r) / VEC : 0);
-    // few tokens: one a block, so that every SM has some; many: kRotTokens
+    // many tokens: kRotTokens a block; few: one, and its heads over several blocks, so that the SMs
+    // share them and a thread has few dependent steps (the angles are computed again in each)
     int tokens = a.T / (148 * 4);
     tokens = tokens < 1 ? 1 : tokens > kRotTokens ? kRotTokens : tokens;
     const unsigned grid = (unsigned)((a.T + tokens - 1) / tokens);
-    rotary_kernel<T, VEC, INTER><<<grid, kRotThreads, (size_t)tokens * (a.r / 2) * sizeof(float2), st>>>(a, tokens,
-                                                                                                     units);
+    const int hpb = units < kRotThreads ? kRotThreads / units : 1;
+    const int steps = (tokens * (a.a[0].heads + a.a[1].heads) + 2 * hpb - 1) / (2 * hpb);
+    int split = 148 * 4 / (int)(grid < 148 * 4 ? grid : 148 * 4);
+    split = split > steps ? steps : split;
+    rotary_kernel<T, VEC, INTER><<<dim3(grid, (unsigned)split), kRotThreads,
+                                   (size_t)tokens * (a.r / 2) * sizeof(float2), st>>>(a, tokens, units);
     return cudaGetLastError();
 }
 
