@@ -108,7 +108,7 @@ la_simt_kernel(const LaParams p) {
             {
                 const int j0 = (tid / 16) * 4, i0 = (tid % 16) * 4;
                 float acc[4][4] = {};
-#pragma unroll 8
+#pragma unroll 16
                 for (int x = 0; x < D; ++x) {
                     const float4 a = load4(kt + x * LT + j0), b = load4(qt + x * LT + i0);
                     const float av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w};
@@ -134,7 +134,7 @@ la_simt_kernel(const LaParams p) {
             float acc[2][CPL] = {};
             const int i0 = warp * 8 + (lane >> 3) * 2, s0 = (lane & 7) * CPL;
             auto product = [&](const float* a, const float* b, int len) {
-#pragma unroll 4
+#pragma unroll 16
                 for (int x = 0; x < len; ++x) {
                     const float2 u = *reinterpret_cast<const float2*>(a + x * LT + i0);
                     float bv[CPL];
@@ -175,6 +175,7 @@ la_simt_kernel(const LaParams p) {
             const int k0 = (tid / M::GV) * TK, v0 = (tid % M::GV) * TV;
             const float2 dec = la_power2(g, n);
             float acc[TK][TV] = {};
+#pragma unroll 2
             for (int j = 0; j < n; j += 4) {  // (rows from n on are zero)
                 float kw[TK][4], f[4];
 #pragma unroll
@@ -345,7 +346,7 @@ cudaError_t launch_step(const LaStepArgs& a, cudaStream_t st) {
 // ============================================================================ plan
 // One segment per document where the documents alone give every SM work; otherwise segments long
 // enough for their start states (d x d fp32 each) to stay a small part of their tokens.
-constexpr int kMinSegment[2] = {512, 128};  // bf16, fp32 (whose chunks take about ten times as long)
+constexpr int kMinSegment[2] = {512, 64};  // bf16, fp32 (whose chunks take about ten times as long)
 
 LaPlan make_plan(int num_seqs, int T, int H, bool packed, int dtype) {
     const long long tokens = packed ? T : (long long)num_seqs * T;

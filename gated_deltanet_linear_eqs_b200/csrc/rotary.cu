@@ -5,20 +5,29 @@
 //     (a, b) -> scale (a cos - b sin, b cos + a sin),
 // and by -p f_i in the inverse form, which is also the gradient.  The other d - r values are kept.
 //
-// The angle is taken in 64 bits (a position of a million times a frequency of one is known to
-// 1e-10 of a turn), reduced to a fraction of a turn there, and its sine and cosine in 32 bits.
-// A block serves a few tokens: it computes their r / 2 (cos, sin) once into shared memory and then
-// turns all heads of q and k with them, so that the trigonometry is shared by the heads and the
-// pass is bound by HBM (x read once, y written once).
+// Angles: f_i / (2 pi) is taken to 64 bits after the point of a turn, so that p f_i / (2 pi) modulo one
+// turn is the low word of an integer product: no error grows with the position beyond the 2^-53 of the
+// frequency itself, and no 64-bit float is touched per token.
+//
+// A warp serves a token at a time.  Its lanes compute the r / 2 (cos, sin) into shared memory (each lane
+// keeps its frequencies), then turn all heads of q and k with them, 16 bytes of both halves of the pairs a
+// lane.  The trigonometry is shared by the heads, warps wait for no other warp, and the pass is bound by
+// HBM (x read once, y written once).
 #include "common.cuh"
 #include "internal.h"
+#include "sm100.cuh"
 
 namespace gdn {
 
 namespace {
 
-constexpr int kRotThreads = 256;
-constexpr int kRotTokens = 8;  // tokens of a block, at most
+using sm100::fma2;
+using sm100::mul2;
+using sm100::pair;
+using sm100::unpair;
+
+constexpr int kRotWarps = 4;    // of a block
+constexpr int kRotFreqs = 2;    // frequencies a lane keeps in registers
 
 template <typename T, int VEC>
 __device__ __forceinline__ void rot_load(const T* p, float* x) {
@@ -26,9 +35,16 @@ __device__ __forceinline__ void rot_load(const T* p, float* x) {
         x[0] = to_f32(*p);
     } else {
         const uint4 u = __ldcs(reinterpret_cast<const uint4*>(p));
-        const T* t = reinterpret_cast<const T*>(&u);
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) x[i] = to_f32(t[i]);
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (VEC == 8) {
+                x[2 * i] = __uint_as_float(w[i] << 16);
+                x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+            } else {
+                x[i] = __uint_as_float(w[i]);
+            }
+        }
     }
 }
 template <typename T, int VEC>
@@ -44,87 +60,97 @@ __device__ __forceinline__ void rot_store(T* p, const float* x) {
     }
 }
 
-// VEC elements a thread and access: 16 bytes where every piece of the layout is a multiple of them,
-// else single elements.  A unit is what a thread turns at once: VEC elements of both halves of the pairs
-// (half layout), VEC / 2 whole pairs (interleaved, VEC > 1), one pair (VEC = 1), or VEC kept elements.
+// f / (2 pi) in units of 2^-64 turns (whole turns drop out)
+__device__ __forceinline__ uint64_t turns_of(float f) {
+    const double t = (double)f * 0.15915494309189535;
+    return (uint64_t)((t - floor(t)) * 18446744073709551616.0);  // below 2^64: t - floor(t) is at most 1 - 2^-53
+}
+
+// VEC elements a lane and access: 16 bytes where every piece of the layout is a multiple of them, else single
+// elements.  A unit is what a lane turns in a head: VEC elements of both halves of the pairs (half
+// layout), VEC / 2 whole pairs (interleaved, VEC > 1), one pair (VEC = 1), or VEC kept elements.
 template <typename T, int VEC, bool INTER>
-__global__ void __launch_bounds__(kRotThreads)
-rotary_kernel(const RotaryArgs p, int tokens, int units) {
-    extern __shared__ float2 cs[];  // [tokens][r / 2]
-    const int half = p.r / 2, tid = threadIdx.x;
-    const int t0 = blockIdx.x * tokens;
-    const int nt = min(tokens, p.T - t0);
-    for (int e = tid; e < nt * half; e += kRotThreads) {
-        const int t = e / half;
-        const double turns = (double)p.positions[t0 + t] * ((double)p.inv_freq[e - t * half] * 0.15915494309189535);
-        float s, c;
-        sincospif(2.f * (float)(turns - rint(turns)), &s, &c);
-        cs[e] = make_float2(c * p.scale, (p.inverse ? -s : s) * p.scale);
-    }
-    __syncthreads();
-    const int heads = p.a[0].heads + p.a[1].heads;
-    const int turned = INTER && VEC > 1 ? p.r / VEC : half / VEC;  // units that turn; the others are kept
-    // a block's threads cover whole heads; a head with more units than threads takes several steps
-    const int hpb = units < kRotThreads ? kRotThreads / units : 1;
-    const int hh = units < kRotThreads ? tid / units : 0;
-    if (hh >= hpb) return;
-    const int u0 = units < kRotThreads ? tid - hh * units : tid;
-    // Two heads a step: both heads' loads are on their way before either is stored.
-    const int rows = nt * heads, step = hpb * (int)gridDim.y;
-    for (int row = hh + hpb * (int)blockIdx.y; row < rows; row += 2 * step) {
-        const T* x[2];
-        T* y[2];
-        const float2* w[2];
-        const bool both = row + step < rows;
+__global__ void __launch_bounds__(kRotWarps * 32)
+rotary_kernel(const RotaryArgs p, int units, int turned, int per_block) {
+    constexpr bool PAIRS = INTER && VEC > 1;
+    extern __shared__ float4 s_cs[];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, half = p.r / 2;
+    const int pad = (half + 3) & ~3;
+    float* cw = reinterpret_cast<float*>(s_cs) + warp * 2 * pad;  // cos; sin behind it
+    float* sw = cw + pad;
+    uint64_t f[kRotFreqs];
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
-            const int at = b && both ? row + step : row;
-            const int t = at / heads;
-            int h = at - t * heads;
-            const bool second = h >= p.a[0].heads;
-            if (second) h -= p.a[0].heads;
-            x[b] = static_cast<const T*>(second ? p.a[1].x : p.a[0].x) +
-                   (long long)(t0 + t) * (second ? p.a[1].ldx : p.a[0].ldx) + (long long)h * p.d;
-            y[b] = static_cast<T*>(second ? p.a[1].y : p.a[0].y) +
-                   (long long)(t0 + t) * (second ? p.a[1].ldy : p.a[0].ldy) + (long long)h * p.d;
-            w[b] = cs + t * half;
+    for (int i = 0; i < kRotFreqs; ++i) f[i] = lane + 32 * i < half ? turns_of(p.inv_freq[lane + 32 * i]) : 0;
+    const int hpw = units < 32 ? 32 / units : 1;  // heads the lanes cover at once
+    const int hh = units < 32 ? lane / units : 0, u0 = units < 32 ? lane - hh * units : lane;
+    const int first = blockIdx.y * per_block, last = min(first + per_block, p.a[0].heads + p.a[1].heads);
+    for (int t = blockIdx.x * kRotWarps + warp; t < p.T; t += gridDim.x * kRotWarps) {
+        const long long pos = p.positions[t];
+        __syncwarp();  // the last token's factors are read
+        for (int i = lane, k = 0; i < half; i += 32, ++k) {
+            const uint64_t fr = k < kRotFreqs ? (k == 0 ? f[0] : f[kRotFreqs - 1]) : turns_of(p.inv_freq[i]);
+            const int turn = (int)(uint32_t)(((uint64_t)pos * fr + 0x80000000ull) >> 32);  // in 2^-32 turns
+            float s, c;
+            sincospif((float)turn * (1.f / 2147483648.f), &s, &c);
+            cw[i] = c * p.scale;
+            sw[i] = (p.inverse ? -s : s) * p.scale;
         }
-        for (int u = u0; u < units; u += kRotThreads) {
-            const bool turn = u < turned;
-            const int ia = !turn ? p.r + (u - turned) * VEC : INTER ? (VEC > 1 ? u * VEC : 2 * u) : u * VEC;
-            const int ib = INTER ? 2 * u + 1 : half + u * VEC;  // (not of whole interleaved pairs)
-            constexpr bool PAIRS = INTER && VEC > 1;
-            float v[2][VEC], z[2][VEC];
+        __syncwarp();
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                if (b && !both) break;
-                rot_load<T, VEC>(x[b] + ia, v[b]);
-                if (!PAIRS && turn) rot_load<T, VEC>(x[b] + ib, z[b]);
-            }
-#pragma unroll
-            for (int b = 0; b < 2; ++b) {
-                if (b && !both) break;
-                if (turn) {
-                    float o[VEC], n[VEC];
-                    if constexpr (PAIRS) {
+        for (int w = 0; w < 2; ++w) {
+            const RotaryTensor& a = p.a[w];
+            const int off = w ? p.a[0].heads : 0;
+            const int h1 = min(last - off, a.heads);
+            if (hh >= hpw) continue;
+            const T* xt = static_cast<const T*>(a.x) + (long long)t * a.ldx;
+            T* yt = static_cast<T*>(a.y) + (long long)t * a.ldy;
+#pragma unroll 2
+            for (int h = max(first - off, 0) + hh; h < h1; h += hpw) {
+                const T* x = xt + h * p.d;
+                T* y = yt + h * p.d;
+                for (int u = u0; u < units; u += 32) {
+                    if (u >= turned) {
+                        const int at = p.r + (u - turned) * VEC;
+                        float v[VEC];
+                        rot_load<T, VEC>(x + at, v);
+                        rot_store<T, VEC>(y + at, v);
+                    } else if constexpr (PAIRS) {
+                        float v[VEC];
+                        rot_load<T, VEC>(x + u * VEC, v);
 #pragma unroll
                         for (int i = 0; i < VEC / 2; ++i) {
-                            const float2 f = w[b][u * (VEC / 2) + i];
-                            o[2 * i] = v[b][2 * i] * f.x - v[b][2 * i + 1] * f.y;
-                            o[2 * i + 1] = v[b][2 * i + 1] * f.x + v[b][2 * i] * f.y;
+                            const float c = cw[u * (VEC / 2) + i], s = sw[u * (VEC / 2) + i];
+                            const uint64_t o = fma2(pair(v[2 * i + 1], v[2 * i]), pair(-s, s),
+                                                    mul2(pair(v[2 * i], v[2 * i + 1]), pair(c, c)));
+                            unpair(o, v[2 * i], v[2 * i + 1]);
                         }
-                    } else {
+                        rot_store<T, VEC>(y + u * VEC, v);
+                    } else if constexpr (VEC > 1) {
+                        float v[VEC], z[VEC];
+                        rot_load<T, VEC>(x + u * VEC, v);
+                        rot_load<T, VEC>(x + half + u * VEC, z);
 #pragma unroll
-                        for (int i = 0; i < VEC; ++i) {
-                            const float2 f = w[b][u * VEC + i];
-                            o[i] = v[b][i] * f.x - z[b][i] * f.y;
-                            n[i] = z[b][i] * f.x + v[b][i] * f.y;
+                        for (int i = 0; i < VEC; i += 4) {
+                            const float4 c = load4(cw + u * VEC + i), s = load4(sw + u * VEC + i);
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const uint64_t c2 = e ? pair(c.z, c.w) : pair(c.x, c.y);
+                                const uint64_t s2 = e ? pair(s.z, s.w) : pair(s.x, s.y);
+                                const uint64_t m2 = e ? pair(-s.z, -s.w) : pair(-s.x, -s.y);
+                                const uint64_t a2 = pair(v[i + 2 * e], v[i + 2 * e + 1]);
+                                const uint64_t b2 = pair(z[i + 2 * e], z[i + 2 * e + 1]);
+                                unpair(fma2(b2, m2, mul2(a2, c2)), v[i + 2 * e], v[i + 2 * e + 1]);
+                                unpair(fma2(a2, s2, mul2(b2, c2)), z[i + 2 * e], z[i + 2 * e + 1]);
+                            }
                         }
-                        rot_store<T, VEC>(y[b] + ib, n);
+                        rot_store<T, VEC>(y + u * VEC, v);
+                        rot_store<T, VEC>(y + half + u * VEC, z);
+                    } else {
+                        const int ia = INTER ? 2 * u : u, ib = INTER ? 2 * u + 1 : half + u;
+                        const float v = to_f32(x[ia]), z = to_f32(x[ib]), c = cw[u], s = sw[u];
+                        y[ia] = from_f32<T>(v * c - z * s);
+                        y[ib] = from_f32<T>(z * c + v * s);
                     }
-                    rot_store<T, VEC>(y[b] + ia, o);
-                } else {
-                    rot_store<T, VEC>(y[b] + ia, v[b]);
                 }
             }
         }
@@ -135,17 +161,18 @@ template <typename T, int VEC, bool INTER>
 cudaError_t launch(const RotaryArgs& a, bool keep, cudaStream_t st) {
     const int turned = INTER && VEC > 1 ? a.r / VEC : a.r / 2 / VEC;
     const int units = turned + (keep ? (a.d - a.r) / VEC : 0);
-    // many tokens: kRotTokens a block; few: one, and its heads over several blocks, so that the SMs
-    // share them and a thread has few dependent steps (the angles are computed again in each)
-    int tokens = a.T / (148 * 4);
-    tokens = tokens < 1 ? 1 : tokens > kRotTokens ? kRotTokens : tokens;
-    const unsigned grid = (unsigned)((a.T + tokens - 1) / tokens);
-    const int hpb = units < kRotThreads ? kRotThreads / units : 1;
-    const int steps = (tokens * (a.a[0].heads + a.a[1].heads) + 2 * hpb - 1) / (2 * hpb);
-    int split = 148 * 4 / (int)(grid < 148 * 4 ? grid : 148 * 4);
-    split = split > steps ? steps : split;
-    rotary_kernel<T, VEC, INTER><<<dim3(grid, (unsigned)split), kRotThreads,
-                                   (size_t)tokens * (a.r / 2) * sizeof(float2), st>>>(a, tokens, units);
+    const int heads = a.a[0].heads + a.a[1].heads;
+    // blocks that fit the SMs at once walk over the tokens; few tokens: the heads go over several blocks,
+    // each of which computes the angles again
+    const int blocks = (a.T + kRotWarps - 1) / kRotWarps, fit = 148 * 12;
+    const int hpw = units < 32 ? 32 / units : 1;
+    int split = fit / blocks;
+    const int most = (heads + hpw - 1) / hpw;
+    split = split < 1 ? 1 : split > most ? most : split;
+    const int per = (heads + split - 1) / split;
+    const size_t smem = (size_t)kRotWarps * 2 * ((a.r / 2 + 3) & ~3) * sizeof(float);
+    rotary_kernel<T, VEC, INTER><<<dim3((unsigned)(blocks < fit ? blocks : fit), (unsigned)((heads + per - 1) / per)),
+                                   kRotWarps * 32, smem, st>>>(a, units, turned, per);
     return cudaGetLastError();
 }
 
