@@ -10,9 +10,11 @@
 //  - The state lives in fp32 registers of the compute warps and is only rounded to bf16 as Ys's
 //    operand.  LOC is a fresh fp32 accumulator each chunk: added into the state by the CUDA cores, its
 //    sums do not suffer from the tensor cores' truncating accumulation over a long sequence.
-//  - The decay weights would cost the products' exactness if they were rounded to bf16 with V.  So a
-//    weighted value is cut into three bf16 pieces (8 bits each: exactly the fp32 value) and LOC is three
-//    products; s_final then has fp32 accuracy.  P is rounded to bf16 once (y is bf16).
+//  - The decay weights would cost the products' exactness if they were rounded to bf16 with V.  So a weight
+//    is cut into three bf16 pieces w1 + w2 + w3 (8 bits each: exactly the fp32 value), and v w into four:
+//    p1 = bf16(v w1), e1 = v w1 - p1 (exact: the product of two 8-bit significands has 16 bits), p2 = bf16(v w2),
+//    and bf16(v w3 + e2) with e2 = v w2 - p2, which is off by 2^-26 of v w.  Five packed bf16 instructions for
+//    two values; LOC is four products and s_final has fp32 accuracy.  P is rounded to bf16 once (y is bf16).
 //  - A operands in TMEM rather than shared memory: the products are bound by shared-memory bandwidth
 //    (an A of 128 x 16 costs as much of it as a B of 128 columns), which V~ and S^T do not touch.
 // Warps 0-7 prepare a chunk (V~, transposed on the way from shared memory to TMEM by ldmatrix, and P; two
@@ -45,25 +47,28 @@ struct TcLayout {
     static constexpr int NT = STATE ? 2 : 3;      // K, V (, Q)
     static constexpr int STAGES = 3;
     static constexpr int STAGE = NT * TILE;
-    static constexpr int P = STAGES * STAGE;      // [j][i] bf16
-    static constexpr int Y = P + 8192;            // outputs on their way to global memory, like a tile
-    static constexpr int TAB = Y + (STATE ? 0 : TILE);  // decay of the scores: [128], zero below 64
-    static constexpr int SW = TAB + 512;          // weights of V~: [64]
-    static constexpr int FI = SW + 256;           // factors of Ys: [64]
+    static constexpr int P = STAGES * STAGE;      // [j][i] bf16, one for each stage
+    static constexpr int Y = P + (STATE ? 0 : STAGES * 8192);  // outputs on their way out: 32 x 32 a back warp
+    static constexpr int TAB = Y + (STATE ? 0 : 8 * 2048);     // decay of the scores by 64 + i - j, two copies
+    static constexpr int SW = TAB + 1024;         // weights of V~, by pairs of tokens: [32][4] (three pieces)
+    static constexpr int FI = SW + 512;           // factors of Ys: [64]
     static constexpr int BAR = FI + 256;
     static constexpr int MISC = BAR + 20 * 8;     // TMEM base, abort flag, zero word
     static constexpr int BYTES = MISC + 16;
-    static constexpr uint32_t T_SC = 0, T_V = 64, T_LOC = 160, T_YI = 288, T_YS = 352, T_S = 416;
+    static constexpr uint32_t T_SC = 0, T_V = 64, T_LOC = 192, T_YI = 320, T_YS = 384, T_S = 448;
 };
-// B_*: arrivals of copies and products; C_*: of the compute warps (8 each)
-enum { B_FULL = 0, B_EMPTY = 3, B_SC = 6, B_LOC, B_Y, C_FIX, C_V, C_P, C_L, C_S, C_Y, B_FIN, B_COUNT = B_FIN + 2 };
+// B_*: arrivals of copies and products; C_*: of the compute warps (8 each).  A wait knows a phase by its
+// parity, so no barrier may complete a phase before every waiter has seen the one before:
+//   SC(c + 1) follows C_P(c), LOC(c + 1) follows C_V(c + 1) and C_L(c), and each of those its waiters' own
+//   arrival behind B_SC(c), B_LOC(c); Ys and Yi(c + 1) follow C_S(c + 1), behind B_Y(c).  The front may
+//   be up to the ring ahead of the warp that issues Yi, so C_P is a barrier a stage, like B_FULL: its
+//   next phase needs the stage loaded again, which needs Yi to have read it.
+enum { B_FULL = 0, B_EMPTY = 3, B_SC = 6, B_LOC, B_Y, C_FIX, C_V, C_P, C_L = C_P + 3, C_S, B_FIN, B_COUNT = B_FIN + 2 };
 
 __device__ __forceinline__ uint32_t pack_rn(float a, float b) {
     const __nv_bfloat162 x = __floats2bfloat162_rn(a, b);
     return *reinterpret_cast<const uint32_t*>(&x);
 }
-constexpr uint64_t kHiMask = 0xffff0000ffff0000ull;  // the bf16 piece of each value of a pair, truncated
-
 template <int D, bool REV, bool STATE>
 __global__ void __launch_bounds__(kTcThreads, 1)
 la_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -93,18 +98,20 @@ la_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
     }
     if (warp == 17) tmem_alloc(tmem_slot, 512);
     float* tab = reinterpret_cast<float*>(sm + L::TAB);
-    float* sw = reinterpret_cast<float*>(sm + L::SW);
     float* fi = reinterpret_cast<float*>(sm + L::FI);
-    for (int e = tid; e < 128; e += kTcThreads) tab[e] = e < 64 ? 0.f : expf(g * (float)(e - 64)) * p.p_scale;
+    if (tid < 256) {  // tab[e] for 64 + i - j = e; the second copy is one entry ahead (pairs then are aligned)
+        const int e = (tid & 127) + (tid >> 7), d = REV ? 64 - e : e - 64;
+        tab[tid] = d >= 0 && d < 64 ? expf(g * (float)d) * p.p_scale : 0.f;
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
 
     auto fail = [&](int bar) {
+        (void)GDN_GUARD(false, p.status, DBG_WAIT, (long)bar * 65536 + warp * 256 + D + STATE * 2 + REV);
         *abort_flag = 1;
         record_status(p.status, GDN_ERR_TIMEOUT);
-        (void)bar;
     };
     auto wwait = [&](int bar, uint32_t parity) {
         const bool ok = mbar_wait_lane(&bars[bar], parity, abort_flag);
@@ -171,7 +178,11 @@ la_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
         int s = 0;             // the chunk's stage
         uint32_t st = s0;      // and its address
         uint32_t full_ph = 0;  // the parity of its arrival
+        int last_s = 0;        // the chunk before
+        uint32_t last_ph = 0;
         auto next_stage = [&]() {
+            last_s = s;
+            last_ph = full_ph;
             st += L::STAGE;
             if (++s == L::STAGES) {
                 s = 0;
@@ -184,7 +195,7 @@ la_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                 const uint32_t ph = cc & 1;
                 // the chunk is in shared memory; its scores' region is free (the last P is stored)
                 ok = wait(B_FULL + s, full_ph) && (place(cc) * C + C <= sg.len || wait(C_FIX, 0)) &&
-                     (STATE || cc == 0 || wait(C_P, ph ^ 1));
+                     (STATE || cc == 0 || wait(C_P + last_s, last_ph));
                 if (!ok) break;
                 tc_fence_after();
                 if (!STATE) {
@@ -206,6 +217,7 @@ la_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                     steps([&](auto kk) { mma_ts<ID_LOC, kk != 0>(tm + L::T_LOC, tm + L::T_V + 8 * kk, k + 128 * kk); });
                     steps([&](auto kk) { mma_ts<ID_LOC, true>(tm + L::T_LOC, tm + L::T_V + 32 + 8 * kk, k + 128 * kk); });
                     steps([&](auto kk) { mma_ts<ID_LOC, true>(tm + L::T_LOC, tm + L::T_V + 64 + 8 * kk, k + 128 * kk); });
+                    steps([&](auto kk) { mma_ts<ID_LOC, true>(tm + L::T_LOC, tm + L::T_V + 96 + 8 * kk, k + 128 * kk); });
                     mma_commit(&bars[B_LOC]);
                     mma_commit(&bars[B_EMPTY + s]);
                 }
@@ -215,7 +227,7 @@ la_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
             for (int cc = 0; cc < nch; ++cc, next_stage()) {
                 const uint32_t ph = cc & 1;
                 // the chunk is in shared memory, the state before it stored, the last outputs read
-                ok = wait(B_FULL + s, full_ph) && wait(C_S, ph) && (cc == 0 || wait(C_Y, ph ^ 1));
+                ok = wait(B_FULL + s, full_ph) && wait(C_S, ph);
                 if (!ok) break;
                 tc_fence_after();
                 if (leader) {
@@ -227,11 +239,11 @@ la_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                         });
                 }
                 __syncwarp();
-                ok = wait(C_P, ph);  // (V's zeroed rows too: the warps that zero them store P afterwards)
+                ok = wait(C_P + s, full_ph);  // (V's zeroed rows too: the warps that zero them store P afterwards)
                 if (!ok) break;
                 tc_fence_after();
                 if (leader) {
-                    const uint32_t v = desc_lo(st + L::TILE, VLBO), pp = desc_lo(s0 + L::P, 8192);
+                    const uint32_t v = desc_lo(st + L::TILE, VLBO), pp = desc_lo(s0 + L::P + s * 8192, 8192);
                     steps([&](auto kk) { mma_ss<ID_YI, kk != 0>(tm + L::T_YI, v + 128 * kk, pp + 128 * kk); });
                     mma_commit(&bars[B_Y]);
                     mma_commit(&bars[B_EMPTY + s]);
@@ -253,92 +265,118 @@ la_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
         // still meet at the named barriers.
         const int quad = warp & 3, half = warp >> 2;
         const uint32_t tl = tmem + (static_cast<uint32_t>(quad * 32) << 16);
-        int cur_n = -1;
+        uint32_t* sw = reinterpret_cast<uint32_t*>(sm + L::SW);
+        uint32_t w1[4], w2[4], w3[4];  // of the tokens 32 half + 8 u + 2 (lane % 4) + 0..1
+        const int j0 = 16 * quad + (lane >> 2), i0 = 32 * half + 2 * (lane & 3);
+        const int k0 = 64 + i0 - j0;  // this lane's first entry of the scores' decay
+        const float2* t0 = reinterpret_cast<const float2*>(tab + (k0 & 1) * 128 + (k0 & ~1));
+        const uint32_t p0 = smem_u32(sm + L::P) + j0 * 128 + 4 * (lane & 3);
+        uint32_t v0[2][2];  // ldmatrix rows of V: 16-row block r, tokens 16 x ..
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const int m = lane >> 3, j = 32 * half + 16 * x + 8 * (m >> 1) + (lane & 7);
+                const int v8 = (4 * quad + 2 * r + (m & 1)) & (D / 8 - 1);
+                v0[r][x] = smem_u32(sm + L::TILE + (v8 >> 3) * 8192) + swz(j, v8 & 7);
+            }
+        int cur_n = -1, s = 0;
+        uint32_t full_ph = 0;
         for (int cc = 0; cc < nch; ++cc) {
             const int n = min(C, sg.len - place(cc) * C);
             const uint32_t ph = cc & 1;
             if (n != cur_n) {  // the weights depend on the chunk's length
                 named_sync(1, 256);
-                if (tid < C)
-                    sw[tid] = REV ? expf(g * (float)(tid + 1)) * p.state_scale
-                                  : tid < n ? expf(g * (float)(n - 1 - tid)) * p.state_scale : 0.f;
+                if (tid < C / 2) {
+                    float w[2];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int j = 2 * tid + e;
+                        w[e] = REV ? expf(g * (float)(j + 1)) * p.state_scale
+                                   : j < n ? expf(g * (float)(n - 1 - j)) * p.state_scale : 0.f;
+                    }
+#pragma unroll
+                    for (int t = 0; t < 3; ++t) {
+                        const uint32_t x = pack_rn(w[0], w[1]);
+                        w[0] -= __uint_as_float(x << 16);
+                        w[1] -= __uint_as_float(x & 0xffff0000u);
+                        sw[4 * tid + t] = x;
+                    }
+                }
                 cur_n = n;
                 named_sync(1, 256);
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const uint4 x = *reinterpret_cast<const uint4*>(sw + 4 * (16 * half + 4 * u + (lane & 3)));
+                    w1[u] = x.x; w2[u] = x.y; w3[u] = x.z;
+                }
             }
-            wwait(B_FULL + cc % L::STAGES, (cc / L::STAGES) & 1);
-            uint8_t* stage = sm + (cc % L::STAGES) * L::STAGE;
+            wwait(B_FULL + s, full_ph);
             if (n < C) {
                 // rows past the document's end hold other documents' tokens (or nothing): K and V are zeroed
                 for (int e = tid; e < (C - n) * 8 * 2 * KB; e += 256) {
                     const int r = n + (e >> 3) / (2 * KB), panel = (e >> 3) % (2 * KB);
-                    *reinterpret_cast<uint4*>(stage + panel * 8192 + r * 128 + (e & 7) * 16) = make_uint4(0, 0, 0, 0);
+                    *reinterpret_cast<uint4*>(sm + s * L::STAGE + panel * 8192 + r * 128 + (e & 7) * 16) =
+                        make_uint4(0, 0, 0, 0);
                 }
                 fence_proxy_async_smem();
                 named_sync(1, 256);
                 if (lane == 0) mbar_arrive(&bars[C_FIX]);
             }
-            // ---- V~: rows v = 32 quad .. +31 (D = 64: twice), tokens 32 half .. +31, in three pieces
+            // ---- V~: rows v = 32 quad .. +31 (D = 64: twice), tokens 32 half .. +31, in four pieces
             {
-                const uint64_t minus = pair(-1.f, -1.f);
-                uint32_t w[3][16];
-                uint64_t f[4];  // of tokens 8 u + 2 (lane % 4) + 0..1
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const float2 x = *reinterpret_cast<const float2*>(sw + 32 * half + 8 * u + 2 * (lane & 3));
-                    f[u] = pair(x.x, x.y);
-                }
+                uint32_t w[4][16];
                 __syncwarp();
 #pragma unroll
                 for (int r = 0; r < 2; ++r)  // 16 rows each
 #pragma unroll
-                    for (int u = 0; u < 4; u += 2) {
-                        const int m = lane >> 3;
-                        const int j = 32 * half + 8 * (u + (m >> 1)) + (lane & 7);
-                        const int v8 = (4 * quad + 2 * r + (m & 1)) & (D / 8 - 1);
-                        uint32_t x[4];
-                        ldsm_x4_t(smem_u32(stage + L::TILE + (v8 >> 3) * 8192) + swz(j, v8 & 7), x[0], x[1], x[2], x[3]);
+                    for (int x = 0; x < 2; ++x) {
+                        uint32_t v[4];
+                        ldsm_x4_t(v0[r][x] + s * L::STAGE, v[0], v[1], v[2], v[3]);
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            const uint64_t y = mul2(pair(__uint_as_float(x[e] << 16), __uint_as_float(x[e] & 0xffff0000u)),
-                                                    f[u + (e >> 1)]);
-                            const uint64_t s1 = fma2(y & kHiMask, minus, y);
-                            const uint64_t s2 = fma2(s1 & kHiMask, minus, s1);
-                            w[0][8 * r + 2 * u + e] = __byte_perm((uint32_t)y, (uint32_t)(y >> 32), 0x7632);
-                            w[1][8 * r + 2 * u + e] = __byte_perm((uint32_t)s1, (uint32_t)(s1 >> 32), 0x7632);
-                            w[2][8 * r + 2 * u + e] = __byte_perm((uint32_t)s2, (uint32_t)(s2 >> 32), 0x7632);
+                            const int u = 2 * x + (e >> 1), at = 8 * r + 4 * x + e;
+                            const uint32_t p1 = mul_bf16x2(v[e], w1[u]), p2 = mul_bf16x2(v[e], w2[u]);
+                            w[0][at] = p1;
+                            w[1][at] = fma_bf16x2(v[e], w1[u], p1 ^ 0x80008000u);
+                            w[2][at] = p2;
+                            w[3][at] = fma_bf16x2(v[e], w3[u], fma_bf16x2(v[e], w2[u], p2 ^ 0x80008000u));
                         }
                     }
                 if (cc > 0) wwait(B_LOC, ph ^ 1);  // the last V~ is read
                 tc_fence_after();
 #pragma unroll
-                for (int t = 0; t < 3; ++t) tmem_st_frag(tl + L::T_V + 32 * t + 16 * half, w[t]);
+                for (int t = 0; t < 4; ++t) tmem_st_frag(tl + L::T_V + 32 * t + 16 * half, w[t]);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bars[C_V]);
             }
-            // ---- P: rows j = 16 quad .. +15, columns i = 32 half .. +31
+            // ---- P: rows j = 16 quad .. +15, columns i = 32 half .. +31.  Its buffer is the stage's own: with
+            // the stage loaded again, the Yi that read the buffer is done.
             if (!STATE) {
                 wwait(B_SC, ph);
-                if (cc > 0) wwait(B_Y, ph ^ 1);  // the last P is read
                 tc_fence_after();
                 float x[16];
                 tmem_ld_frag<4>(tl + L::T_SC + 32 * half, x);
-                const int j0 = 16 * quad + (lane >> 2), i0 = 32 * half + 2 * (lane & 3);
-                const float* t0 = tab + 64 + (REV ? j0 - i0 : i0 - j0);
-                constexpr int dir = REV ? -1 : 1;
 #pragma unroll
-                for (int u = 0; u < 4; ++u)
+                for (int u = 0; u < 4; ++u) {
+                    const uint32_t at = p0 + s * 8192 + (((4 * half + u) ^ (j0 & 7)) << 4);
 #pragma unroll
                     for (int r = 0; r < 2; ++r) {
-                        const float y0 = x[4 * u + 2 * r] * t0[dir * (8 * u - 8 * r)];
-                        const float y1 = x[4 * u + 2 * r + 1] * t0[dir * (8 * u + 1 - 8 * r)];
-                        *reinterpret_cast<uint32_t*>(sm + L::P + swz(j0 + 8 * r, 4 * half + u) + 4 * (lane & 3)) =
-                            pack_rn(y0, y1);
+                        const float2 f = t0[4 * u - 4 * r];
+                        float y0, y1;
+                        unpair(mul2(pair(x[4 * u + 2 * r], x[4 * u + 2 * r + 1]), pair(f.x, f.y)), y0, y1);
+                        asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + 1024 * r), "r"(pack_rn(y0, y1)) : "memory");
                     }
+                }
                 tc_fence_before();
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bars[C_P]);
+                if (lane == 0) mbar_arrive(&bars[C_P + s]);
+            }
+            if (++s == L::STAGES) {
+                s = 0;
+                full_ph ^= 1;
             }
         }
     } else if (warp < 16) {
@@ -385,10 +423,11 @@ la_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                 tmem_st16(tl + L::T_S + half * (NS / 2) + x0, w);
             }
             tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars[C_S]);
         };
         if (!STATE) store_state();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[C_S]);
+        uint8_t* ybuf = sm + L::Y + wb * 2048;  // this warp's 32 tokens x 32 columns, 64-byte rows, swizzled
         float2 dec = make_float2(0.f, 0.f);
         int cur_n = -1;
         bool ok = true;
@@ -432,17 +471,22 @@ la_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
             if (lane == 0) mbar_arrive(&bars[C_L]);
             // ---- outputs: columns v = 32 quad .. +31, tokens 32 half .. +31
             if (!STATE) {
-                if (tb == 0) bulk_wait_read();  // the last chunk's outputs have left the staging tile
                 ok = wwait(B_Y, ph) && ok;  // Ys has read the state, too
                 tc_fence_after();
                 if (cc + 1 < nch) store_state();
-                named_sync(2, 256);
+                if (lane == 0) bulk_wait_read();  // the last chunk's outputs have left the staging tile
+                __syncwarp();
                 const size_t row0 = (size_t)(sg.t0 + c * C), step = (size_t)p.H * D;
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {   // 16 lanes each
                     float y[16], z[16];
                     tmem_ld_frag<4>(tl + (16u * r << 16) + L::T_YI + 32 * half, y);
                     tmem_ld_frag<4>(tl + (16u * r << 16) + L::T_YS + 32 * half, z);
+                    if (r == 1) {  // the state is stored and the outputs are read
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&bars[C_S]);
+                    }
 #pragma unroll
                     for (int u = 0; u < 4; ++u) {
                         const float2 f = *reinterpret_cast<const float2*>(fi + 32 * half + 8 * u + 2 * (lane & 3));
@@ -467,39 +511,35 @@ la_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
 #pragma unroll
                         for (int u = 0; u < 4; u += 2) {
                             const int m = lane >> 3;
-                            const int i = 32 * half + 8 * (u + (m >> 1)) + (lane & 7);
-                            const int v8 = 4 * quad + 2 * r + (m & 1);
-                            stsm_x4_t(smem_u32(sm + L::Y + (v8 >> 3) * 8192) + swz(i, v8 & 7),
+                            const int i = 8 * (u + (m >> 1)) + (lane & 7), v8 = 2 * r + (m & 1);
+                            stsm_x4_t(smem_u32(ybuf) + i * 64 + ((v8 ^ ((i >> 1) & 3)) << 4),
                                       pack_rn(y[4 * u], y[4 * u + 1]), pack_rn(y[4 * u + 2], y[4 * u + 3]),
                                       pack_rn(y[4 * u + 4], y[4 * u + 5]), pack_rn(y[4 * u + 6], y[4 * u + 7]));
                         }
                     }
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bars[C_Y]);
-                if (!p.out_f32) {
+                if (!p.out_f32 && mine) {
                     fence_proxy_async_smem();
-                    named_sync(2, 256);
-                    if (n == C) {
-                        if (tb == 0 && ok) {
-#pragma unroll
-                            for (int b = 0; b < KB; ++b)
-                                tma_store_3d(&tm_y, sm + L::Y + b * 8192, 64 * b, h, (int)row0);
+                    __syncwarp();
+                    if (32 * half + 32 <= n) {
+                        if (lane == 0 && ok) {
+                            tma_store_3d(&tm_y, ybuf, 32 * quad, h, (int)row0 + 32 * half);
                             bulk_commit();
                         }
                     } else if (ok) {  // the document's last rows
-                        __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.out) + row0 * step + (size_t)h * D;
-                        for (int e = tb; e < n * (D / 8); e += 256) {
-                            const int i = e / (D / 8), v8 = e % (D / 8);
-                            *reinterpret_cast<uint4*>(o + (size_t)i * step + 8 * v8) =
-                                *reinterpret_cast<const uint4*>(sm + L::Y + (v8 >> 3) * 8192 + swz(i, v8 & 7));
+                        __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.out) + row0 * step + (size_t)h * D + 32 * quad;
+                        for (int e = lane; e < (n - 32 * half) * 4; e += 32) {
+                            const int i = e >> 2, v8 = e & 3;
+                            *reinterpret_cast<uint4*>(o + (size_t)(32 * half + i) * step + 8 * v8) =
+                                *reinterpret_cast<const uint4*>(ybuf + i * 64 + ((v8 ^ ((i >> 1) & 3)) << 4));
                         }
+                        __syncwarp();
                     }
                 }
             }
         }
-        if (!STATE && tb == 0) bulk_wait_read();
+        if (!STATE && lane == 0) bulk_wait_read();
+        __syncwarp();
         // ---- what is behind the segment
         float* dst = nullptr;
         if (STATE)
@@ -538,15 +578,17 @@ EncodeTiledFn encode_fn() {
     return fn;
 }
 
-// [tokens, heads, d] bf16, boxes of 64 tokens x 1 head x 64 columns; tokens past the end read as zero
-bool make_map(CUtensorMap* m, const void* base, long long tokens, int heads, int d) {
+// [tokens, heads, d] bf16, boxes of `side` tokens x 1 head x `side` columns (64: tiles, 32: a back warp's
+// outputs); tokens past the end read as zero
+bool make_map(CUtensorMap* m, const void* base, long long tokens, int heads, int d, unsigned side = 64) {
     EncodeTiledFn enc = encode_fn();
     if (!enc) return false;
     cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)tokens};
     cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)heads * d * 2};
-    cuuint32_t box[3] = {64, 1, 64}, es[3] = {1, 1, 1};
+    cuuint32_t box[3] = {side, 1, side}, es[3] = {1, 1, 1};
     return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, es,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_INTERLEAVE_NONE,
+               side == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -558,7 +600,7 @@ cudaError_t launch(const LaParams& p, int nseg, cudaStream_t st) {
         !make_map(&mq, p.q, tokens, p.H / p.qdiv, D))
         return cudaErrorInvalidValue;
     my = mq;
-    if (!STATE && !p.out_f32 && !make_map(&my, p.out, tokens, p.H, D)) return cudaErrorInvalidValue;
+    if (!STATE && !p.out_f32 && !make_map(&my, p.out, tokens, p.H, D, 32)) return cudaErrorInvalidValue;
     constexpr int bytes = TcLayout<D, STATE>::BYTES + 1024;
     const cudaError_t e = cudaFuncSetAttribute(la_tc_kernel<D, REV, STATE>,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
