@@ -51,8 +51,8 @@ struct TcLayout {
     static constexpr int Y = P + (STATE ? 0 : STAGES * 8192);  // outputs on their way out: 32 x 32 a back warp
     static constexpr int TAB = Y + (STATE ? 0 : 8 * 2048);     // decay of the scores by 64 + i - j, two copies
     static constexpr int SW = TAB + 1024;         // weights of V~, by pairs of tokens: [32][4] (three pieces)
-    static constexpr int FI = SW + 512;           // factors of Ys: [64]
-    static constexpr int BAR = FI + 256;
+    static constexpr int FI = SW + 2 * 512;       // factors of Ys: [64]; both for full chunks and for the tail
+    static constexpr int BAR = FI + 2 * 256;
     static constexpr int MISC = BAR + 20 * 8;     // TMEM base, abort flag, zero word
     static constexpr int BYTES = MISC + 16;
     static constexpr uint32_t T_SC = 0, T_V = 64, T_LOC = 192, T_YI = 320, T_YS = 384, T_S = 448;
@@ -69,10 +69,34 @@ __device__ __forceinline__ uint32_t pack_rn(float a, float b) {
     const __nv_bfloat162 x = __floats2bfloat162_rn(a, b);
     return *reinterpret_cast<const uint32_t*>(&x);
 }
-template <int D, bool REV, bool STATE>
+// The weights of V~ in pieces, by pairs of tokens; the factor of Ys in token i.
+__device__ __forceinline__ void front_table(uint32_t* sw, int pair_, float g, int n, float scale, bool rev) {
+    float w[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const int j = 2 * pair_ + e;
+        w[e] = rev || j < n ? expf(g * (float)(rev ? j + 1 : n - 1 - j)) * scale : 0.f;
+    }
+#pragma unroll
+    for (int t = 0; t < 3; ++t) {
+        const uint32_t x = pack_rn(w[0], w[1]);
+        w[0] -= __uint_as_float(x << 16);
+        w[1] -= __uint_as_float(x & 0xffff0000u);
+        sw[4 * pair_ + t] = x;
+    }
+}
+__device__ __forceinline__ float back_factor(float g, int i, int n, float scale, bool rev) {
+    return !rev || i < n ? expf(g * (float)(rev ? n - 1 - i : i + 1)) * scale : 0.f;
+}
+
+// MODE: what a pass writes
+enum { M_OUT = 0, M_STATE = 1, M_OUT_F32 = 2 };
+
+template <int D, bool REV, int MODE>
 __global__ void __launch_bounds__(kTcThreads, 1)
 la_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
              const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_y, const LaParams p) {
+    constexpr bool STATE = MODE == M_STATE;
     using L = TcLayout<D, STATE>;
     constexpr int KB = L::KB, C = kLaChunk;
     const int h = blockIdx.x % p.H, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -98,7 +122,13 @@ la_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
     }
     if (warp == 17) tmem_alloc(tmem_slot, 512);
     float* tab = reinterpret_cast<float*>(sm + L::TAB);
-    float* fi = reinterpret_cast<float*>(sm + L::FI);
+    const int tail_n = sg.len - (nch - 1) * C;  // tokens of the document's last chunk, if it is here
+    // tables for full chunks and for one of tail_n tokens, once: the chunks then meet at no barrier
+    if (tid < 64) front_table(reinterpret_cast<uint32_t*>(sm + L::SW) + (tid >> 5) * 128, tid & 31, g,
+                              tid < 32 ? C : tail_n, p.state_scale, REV);
+    if (tid >= 64 && tid < 192)
+        reinterpret_cast<float*>(sm + L::FI)[tid - 64] =
+            back_factor(g, tid & 63, tid < 128 ? C : tail_n, p.inter_scale, REV);
     if (tid < 256) {  // tab[e] for 64 + i - j = e; the second copy is one entry ahead (pairs then are aligned)
         const int e = (tid & 127) + (tid >> 7), d = REV ? 64 - e : e - 64;
         tab[tid] = d >= 0 && d < 64 ? expf(g * (float)d) * p.p_scale : 0.f;
@@ -109,7 +139,7 @@ la_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
     const uint32_t tmem = *tmem_slot;
 
     auto fail = [&](int bar) {
-        (void)GDN_GUARD(false, p.status, DBG_WAIT, (long)bar * 65536 + warp * 256 + D + STATE * 2 + REV);
+        (void)GDN_GUARD(false, p.status, DBG_WAIT, (long)bar * 65536 + warp * 256 + D + MODE * 2 + REV);
         *abort_flag = 1;
         record_status(p.status, GDN_ERR_TIMEOUT);
     };
@@ -265,8 +295,16 @@ la_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
         // still meet at the named barriers.
         const int quad = warp & 3, half = warp >> 2;
         const uint32_t tl = tmem + (static_cast<uint32_t>(quad * 32) << 16);
-        uint32_t* sw = reinterpret_cast<uint32_t*>(sm + L::SW);
         uint32_t w1[4], w2[4], w3[4];  // of the tokens 32 half + 8 u + 2 (lane % 4) + 0..1
+        auto weights = [&](bool tail) {
+            const uint32_t* sw = reinterpret_cast<const uint32_t*>(sm + L::SW) + tail * 128;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const uint4 x = *reinterpret_cast<const uint4*>(sw + 4 * (16 * half + 4 * u + (lane & 3)));
+                w1[u] = x.x; w2[u] = x.y; w3[u] = x.z;
+            }
+        };
+        weights(false);
         const int j0 = 16 * quad + (lane >> 2), i0 = 32 * half + 2 * (lane & 3);
         const int k0 = 64 + i0 - j0;  // this lane's first entry of the scores' decay
         const float2* t0 = reinterpret_cast<const float2*>(tab + (k0 & 1) * 128 + (k0 & ~1));
@@ -280,40 +318,16 @@ la_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                 const int v8 = (4 * quad + 2 * r + (m & 1)) & (D / 8 - 1);
                 v0[r][x] = smem_u32(sm + L::TILE + (v8 >> 3) * 8192) + swz(j, v8 & 7);
             }
-        int cur_n = -1, s = 0;
+        int s = 0;
         uint32_t full_ph = 0;
         for (int cc = 0; cc < nch; ++cc) {
             const int n = min(C, sg.len - place(cc) * C);
             const uint32_t ph = cc & 1;
-            if (n != cur_n) {  // the weights depend on the chunk's length
-                named_sync(1, 256);
-                if (tid < C / 2) {
-                    float w[2];
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int j = 2 * tid + e;
-                        w[e] = REV ? expf(g * (float)(j + 1)) * p.state_scale
-                                   : j < n ? expf(g * (float)(n - 1 - j)) * p.state_scale : 0.f;
-                    }
-#pragma unroll
-                    for (int t = 0; t < 3; ++t) {
-                        const uint32_t x = pack_rn(w[0], w[1]);
-                        w[0] -= __uint_as_float(x << 16);
-                        w[1] -= __uint_as_float(x & 0xffff0000u);
-                        sw[4 * tid + t] = x;
-                    }
-                }
-                cur_n = n;
-                named_sync(1, 256);
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const uint4 x = *reinterpret_cast<const uint4*>(sw + 4 * (16 * half + 4 * u + (lane & 3)));
-                    w1[u] = x.x; w2[u] = x.y; w3[u] = x.z;
-                }
-            }
             wwait(B_FULL + s, full_ph);
             if (n < C) {
                 // rows past the document's end hold other documents' tokens (or nothing): K and V are zeroed
+                weights(true);
+#pragma unroll 1
                 for (int e = tid; e < (C - n) * 8 * 2 * KB; e += 256) {
                     const int r = n + (e >> 3) / (2 * KB), panel = (e >> 3) % (2 * KB);
                     *reinterpret_cast<uint4*>(sm + s * L::STAGE + panel * 8192 + r * 128 + (e & 7) * 16) =
@@ -374,6 +388,7 @@ la_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bars[C_P + s]);
             }
+            if (REV && n < C) weights(false);
             if (++s == L::STAGES) {
                 s = 0;
                 full_ph ^= 1;
@@ -382,7 +397,7 @@ la_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
     } else if (warp < 16) {
         // ---------------------------------------------------------------- back: the state and the outputs
         if constexpr (MOVE) regs_up<kBackRegs>();
-        const int wb = warp - 8, quad = wb & 3, half = wb >> 2, tb = tid - 256;
+        const int wb = warp - 8, quad = wb & 3, half = wb >> 2;
         const int vv = (quad * 32 + lane) & (D - 1);      // the state's row; D = 64: lanes 64.. repeat it
         const bool mine = quad * 32 < D;                  // this warp writes results
         const uint32_t tl = tmem + (static_cast<uint32_t>(quad * 32) << 16);
@@ -428,36 +443,33 @@ la_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars[C_S]);
         uint8_t* ybuf = sm + L::Y + wb * 2048;  // this warp's 32 tokens x 32 columns, 64-byte rows, swizzled
-        float2 dec = make_float2(0.f, 0.f);
-        int cur_n = -1;
+        float2 dec[2];
+#pragma unroll 1
+        for (int e = 1; e >= 0; --e) {
+            dec[1] = dec[0];
+            dec[0] = la_power2(g, e ? tail_n : C);
+        }
         bool ok = true;
         for (int cc = 0; cc < nch; ++cc) {
             const int c = place(cc), n = min(C, sg.len - c * C);
             const uint32_t ph = cc & 1;
-            if (n != cur_n) {  // the factors that depend on the chunk's length
-                if (!STATE) {
-                    named_sync(2, 256);
-                    if (tb < C)
-                        fi[tb] = REV ? (tb < n ? expf(g * (float)(n - 1 - tb)) * p.inter_scale : 0.f)
-                                     : expf(g * (float)(tb + 1)) * p.inter_scale;
-                    named_sync(2, 256);
-                }
-                dec = la_power2(g, n);
-                cur_n = n;
-            }
+            const bool tail = n < C;
+            const float* fi = reinterpret_cast<const float*>(sm + L::FI) + tail * 64;
             // ---- state behind the chunk
             ok = wwait(B_LOC, ph) && ok;
             tc_fence_after();
             {
                 // e^{g n} in one float would be off the same way every time; the rest of it is made up for
                 // every eighth chunk (what entered since then is over-corrected by 8 2^-25 at most)
-                const uint64_t wx = pair(dec.x, dec.x);
+                const float dx = tail ? dec[1].x : dec[0].x;
+                const uint64_t wx = pair(dx, dx);
 #pragma unroll
                 for (int b = 0; b < NS / 2; b += 16) {
                     float x[32];
                     tmem_ld32(tl + L::T_LOC + half * NS + 2 * b, x);
                     if ((cc & 7) == 7) {
-                        const uint64_t wy = pair(8.f * dec.y, 8.f * dec.y);
+                        const float dy = 8.f * (tail ? dec[1].y : dec[0].y);
+                        const uint64_t wy = pair(dy, dy);
 #pragma unroll
                         for (int e = 0; e < 16; ++e)
                             unpair(fma2(S[b + e], wy, pair(x[2 * e], x[2 * e + 1])), x[2 * e], x[2 * e + 1]);
@@ -496,7 +508,7 @@ la_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                             unpair(fma2(f2, pair(z[e], z[e + 1]), pair(y[e], y[e + 1])), y[e], y[e + 1]);
                     }
                     if (!mine) continue;
-                    if (p.out_f32) {
+                    if constexpr (MODE == M_OUT_F32) {
                         float* o = static_cast<float*>(p.out) + row0 * step + (size_t)h * D;
                         if (ok)
 #pragma unroll
@@ -518,7 +530,7 @@ la_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                         }
                     }
                 }
-                if (!p.out_f32 && mine) {
+                if (MODE == M_OUT && mine) {
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (32 * half + 32 <= n) {
@@ -528,6 +540,7 @@ la_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                         }
                     } else if (ok) {  // the document's last rows
                         __nv_bfloat16* o = static_cast<__nv_bfloat16*>(p.out) + row0 * step + (size_t)h * D + 32 * quad;
+#pragma unroll 1
                         for (int e = lane; e < (n - 32 * half) * 4; e += 32) {
                             const int i = e >> 2, v8 = e & 3;
                             *reinterpret_cast<uint4*>(o + (size_t)(32 * half + i) * step + 8 * v8) =
@@ -592,7 +605,7 @@ bool make_map(CUtensorMap* m, const void* base, long long tokens, int heads, int
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, bool REV, bool STATE>
+template <int D, bool REV, int MODE>
 cudaError_t launch(const LaParams& p, int nseg, cudaStream_t st) {
     const long long tokens = p.cu ? p.T : (long long)p.num_seqs * p.T;
     CUtensorMap mq, mk, mv, my;
@@ -600,25 +613,26 @@ cudaError_t launch(const LaParams& p, int nseg, cudaStream_t st) {
         !make_map(&mq, p.q, tokens, p.H / p.qdiv, D))
         return cudaErrorInvalidValue;
     my = mq;
-    if (!STATE && !p.out_f32 && !make_map(&my, p.out, tokens, p.H, D, 32)) return cudaErrorInvalidValue;
-    constexpr int bytes = TcLayout<D, STATE>::BYTES + 1024;
-    const cudaError_t e = cudaFuncSetAttribute(la_tc_kernel<D, REV, STATE>,
+    if (MODE == M_OUT && !make_map(&my, p.out, tokens, p.H, D, 32)) return cudaErrorInvalidValue;
+    constexpr int bytes = TcLayout<D, MODE == M_STATE>::BYTES + 1024;
+    const cudaError_t e = cudaFuncSetAttribute(la_tc_kernel<D, REV, MODE>,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
     if (D == 128) {  // the register shares rest on what the kernel is launched with
         cudaFuncAttributes at;
-        const cudaError_t f = cudaFuncGetAttributes(&at, la_tc_kernel<D, REV, STATE>);
+        const cudaError_t f = cudaFuncGetAttributes(&at, la_tc_kernel<D, REV, MODE>);
         if (f != cudaSuccess) return f;
         if (at.numRegs < kLaunchRegs) return cudaErrorInvalidConfiguration;
     }
-    la_tc_kernel<D, REV, STATE><<<(unsigned)((size_t)nseg * p.H), kTcThreads, bytes, st>>>(mq, mk, mv, my, p);
+    la_tc_kernel<D, REV, MODE><<<(unsigned)((size_t)nseg * p.H), kTcThreads, bytes, st>>>(mq, mk, mv, my, p);
     return cudaGetLastError();
 }
 
 template <int D>
 cudaError_t launch_d(const LaParams& p, int nseg, cudaStream_t st) {
-    if (p.state_only) return p.reverse ? launch<D, true, true>(p, nseg, st) : launch<D, false, true>(p, nseg, st);
-    return p.reverse ? launch<D, true, false>(p, nseg, st) : launch<D, false, false>(p, nseg, st);
+    if (p.state_only) return p.reverse ? launch<D, true, M_STATE>(p, nseg, st) : launch<D, false, M_STATE>(p, nseg, st);
+    if (!p.reverse) return launch<D, false, M_OUT>(p, nseg, st);  // (dq has a head for each state: never in parts)
+    return p.out_f32 ? launch<D, true, M_OUT_F32>(p, nseg, st) : launch<D, true, M_OUT>(p, nseg, st);
 }
 
 }  // namespace
