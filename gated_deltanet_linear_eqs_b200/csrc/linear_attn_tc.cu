@@ -19,7 +19,7 @@
 //    (an A of 128 x 16 costs as much of it as a B of 128 columns), which V~ and S^T do not touch.
 // Warps 0-7 prepare a chunk (V~, transposed on the way from shared memory to TMEM by ldmatrix, and P; two
 // warps a TMEM lane quadrant), warps 8-15 finish it (the state, the outputs), so that one chunk's front
-// runs beside its predecessor's back; warp 16 loads by TMA through a ring of stages, warps 17 and 18 issue the
+// runs beside its predecessor's back; warp 16 loads by TMA through a ring of stages, warps 17 to 19 issue the
 // products.  Full chunks' outputs leave by TMA.  Every wait is bounded; one that gives up records
 // GDN_ERR_TIMEOUT.
 #include <mutex>
@@ -34,7 +34,7 @@ namespace {
 
 using namespace sm100;
 
-constexpr int kTcThreads = 640;  // five warpgroups, the last with an idle warp
+constexpr int kTcThreads = 640;  // five warpgroups
 // Registers a thread: 96 at launch (640 threads), then moved to the back warps, which hold the state.  The
 // shares must not exceed what the block was launched with: 128 (2 x 80 + 2 x 128 + 56) <= 640 x 96.
 constexpr int kLaunchRegs = 96, kFrontRegs = 80, kBackRegs = 128, kIoRegs = 56;
@@ -53,7 +53,7 @@ struct TcLayout {
     static constexpr int SW = TAB + 1024;         // weights of V~, by pairs of tokens: [32][4] (three pieces)
     static constexpr int FI = SW + 2 * 512;       // factors of Ys: [64]; both for full chunks and for the tail
     static constexpr int BAR = FI + 2 * 256;
-    static constexpr int MISC = BAR + 20 * 8;     // TMEM base, abort flag, zero word
+    static constexpr int MISC = BAR + 22 * 8;     // TMEM base, abort flag, zero word
     static constexpr int BYTES = MISC + 16;
     static constexpr uint32_t T_SC = 0, T_V = 64, T_LOC = 192, T_YI = 320, T_YS = 384, T_S = 448;
 };
@@ -62,8 +62,8 @@ struct TcLayout {
 //   SC(c + 1) follows C_P(c), LOC(c + 1) follows C_V(c + 1) and C_L(c), and each of those its waiters' own
 //   arrival behind B_SC(c), B_LOC(c); Ys and Yi(c + 1) follow C_S(c + 1), behind B_Y(c).  The front may
 //   be up to the ring ahead of the warp that issues Yi, so C_P is a barrier a stage, like B_FULL: its
-//   next phase needs the stage loaded again, which needs Yi to have read it.
-enum { B_FULL = 0, B_EMPTY = 3, B_SC = 6, B_LOC, B_Y, C_FIX, C_V, C_P, C_L = C_P + 3, C_S, B_FIN, B_COUNT = B_FIN + 2 };
+//   next phase needs the stage loaded again, which needs SC and Yi to be done with it.
+enum { B_FULL = 0, B_EMPTY = 3, B_SC = 6, B_LOC, B_Y, C_FIX, C_V, C_P, C_L = C_P + 3, C_S, B_FIN, B_COUNT = B_FIN + 3 };
 
 __device__ __forceinline__ uint32_t pack_rn(float a, float b) {
     const __nv_bfloat162 x = __floats2bfloat162_rn(a, b);
@@ -113,9 +113,9 @@ la_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
     volatile int* never = reinterpret_cast<volatile int*>(sm + L::MISC + 8);
     const float g = p.log_decay[h];
     if (tid == 0) {
-        // a stage is free when both issuing warps' products have read it
+        // a stage is free when all issuing warps' products have read it
         for (int b = 0; b < B_COUNT; ++b)
-            mbar_init(&bars[b], b >= C_FIX && b < B_FIN ? 8 : !STATE && b >= B_EMPTY && b < B_SC ? 2 : 1);
+            mbar_init(&bars[b], b >= C_FIX && b < B_FIN ? 8 : !STATE && b >= B_EMPTY && b < B_SC ? 3 : 1);
         *abort_flag = 0;
         *never = 0;
         fence_mbar_init();
@@ -181,10 +181,10 @@ la_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                 mbar_wait(&bars[B_FULL + k % L::STAGES], (k / L::STAGES) & 1, never, 100000000ull);
         }
         __syncwarp();
-    } else if (warp == 17 || (!STATE && warp == 18)) {
+    } else if (warp == 17 || (!STATE && warp > 17)) {
         // ---------------------------------------------------------------- products
-        // Two warps issue, SC and LOC the one, Ys and Yi the other: an issuing warp is held while its products
-        // run, and the waits of one chain then run beside the products of the other.  A whole warp walks and
+        // Three warps issue, LOC the first, Ys and Yi the second, SC the third: an issuing warp is held while its
+        // products run, and the waits of one chain then run beside the products of the others.  A whole warp walks and
         // one lane issues.  (With a single lane walking, every product's descriptors go through vector
         // registers: 110 cycles a product.)
         const bool leader = elect_one();
@@ -223,23 +223,8 @@ la_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
         if (warp == 17) {
             for (int cc = 0; cc < nch; ++cc, next_stage()) {
                 const uint32_t ph = cc & 1;
-                // the chunk is in shared memory; its scores' region is free (the last P is stored)
-                ok = wait(B_FULL + s, full_ph) && (place(cc) * C + C <= sg.len || wait(C_FIX, 0)) &&
-                     (STATE || cc == 0 || wait(C_P + last_s, last_ph));
-                if (!ok) break;
-                tc_fence_after();
-                if (!STATE) {
-                    if (leader) {
-                        const uint32_t k = desc_lo(st, 16), q = k + (2 * L::TILE >> 4);
-                        steps([&](auto kk) { mma_ss<ID_SC, kk != 0>(tm + L::T_SC, k + 2 * kk, q + 2 * kk); });
-                        if constexpr (KB == 2)
-                            steps([&](auto kk) { mma_ss<ID_SC, true>(tm + L::T_SC, k + 512 + 2 * kk, q + 512 + 2 * kk); });
-                        mma_commit(&bars[B_SC]);
-                    }
-                    __syncwarp();
-                }
-                // V~ is stored; the last LOC is read
-                ok = wait(C_V, ph) && (cc == 0 || wait(C_L, ph ^ 1));
+                // the chunk is in shared memory, V~ is stored (K's zeroed rows before it), the last LOC is read
+                ok = wait(B_FULL + s, full_ph) && wait(C_V, ph) && (cc == 0 || wait(C_L, ph ^ 1));
                 if (!ok) break;
                 tc_fence_after();
                 if (leader) {
@@ -249,6 +234,23 @@ la_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                     steps([&](auto kk) { mma_ts<ID_LOC, true>(tm + L::T_LOC, tm + L::T_V + 64 + 8 * kk, k + 128 * kk); });
                     steps([&](auto kk) { mma_ts<ID_LOC, true>(tm + L::T_LOC, tm + L::T_V + 96 + 8 * kk, k + 128 * kk); });
                     mma_commit(&bars[B_LOC]);
+                    mma_commit(&bars[B_EMPTY + s]);
+                }
+                __syncwarp();
+            }
+        } else if (warp == 19) {
+            for (int cc = 0; cc < nch; ++cc, next_stage()) {
+                // the chunk is in shared memory; its scores' region is free (the last P is stored)
+                ok = wait(B_FULL + s, full_ph) && (place(cc) * C + C <= sg.len || wait(C_FIX, 0)) &&
+                     (cc == 0 || wait(C_P + last_s, last_ph));
+                if (!ok) break;
+                tc_fence_after();
+                if (leader) {
+                    const uint32_t k = desc_lo(st, 16), q = k + (2 * L::TILE >> 4);
+                    steps([&](auto kk) { mma_ss<ID_SC, kk != 0>(tm + L::T_SC, k + 2 * kk, q + 2 * kk); });
+                    if constexpr (KB == 2)
+                        steps([&](auto kk) { mma_ss<ID_SC, true>(tm + L::T_SC, k + 512 + 2 * kk, q + 512 + 2 * kk); });
+                    mma_commit(&bars[B_SC]);
                     mma_commit(&bars[B_EMPTY + s]);
                 }
                 __syncwarp();
@@ -359,8 +361,7 @@ la_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                     }
                 if (cc > 0) wwait(B_LOC, ph ^ 1);  // the last V~ is read
                 tc_fence_after();
-#pragma unroll
-                for (int t = 0; t < 4; ++t) tmem_st_frag(tl + L::T_V + 32 * t + 16 * half, w[t]);
+                tmem_st_frag_x4(tl + L::T_V + 16 * half, w);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bars[C_V]);
@@ -492,8 +493,8 @@ la_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {   // 16 lanes each
                     float y[16], z[16];
-                    tmem_ld_frag<4>(tl + (16u * r << 16) + L::T_YI + 32 * half, y);
-                    tmem_ld_frag<4>(tl + (16u * r << 16) + L::T_YS + 32 * half, z);
+                    const uint32_t at = tl + (16u * r << 16) + 32 * half;
+                    tmem_ld_frag4x2(at + L::T_YI, at + L::T_YS, y, z);
                     if (r == 1) {  // the state is stored and the outputs are read
                         tc_fence_before();
                         __syncwarp();

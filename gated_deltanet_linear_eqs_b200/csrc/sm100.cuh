@@ -515,15 +515,34 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* w) {
 
 // 16x128b shape over 32 lanes (two times 16), 16 columns: thread t of the warp gives, for r = 0, 1 and column
 // group g of 4, w[8 r + 2 g] = (lane 16 r + t / 4, column 4 g + t % 4) and w[8 r + 2 g + 1] = (lane
-// 16 r + t / 4 + 8, the same column).  Completed before returning.
-__device__ __forceinline__ void tmem_st_frag(uint32_t taddr, const uint32_t* w) {
+// 16 r + t / 4 + 8, the same column).  Four of them, 32 columns apart, with one wait; completed before
+// returning.
+__device__ __forceinline__ void tmem_st_frag_x4(uint32_t taddr, const uint32_t (*w4)[16]) {
     __syncwarp();
+    const uint32_t *w = w4[0], *x = w4[1], *y = w4[2], *z = w4[3];
+#define GDN_X8(v, i) "r"(v[i]), "r"(v[i + 1]), "r"(v[i + 2]), "r"(v[i + 3]), "r"(v[i + 4]), "r"(v[i + 5]), \
+                     "r"(v[i + 6]), "r"(v[i + 7])
     asm volatile(
+        "{\n\t.reg .b32 a;\n\t"
         "tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%2,%3,%4,%5,%6,%7,%8,%9};\n\t"
         "tcgen05.st.sync.aligned.16x128b.x4.b32 [%1], {%10,%11,%12,%13,%14,%15,%16,%17};\n\t"
-        "tcgen05.wait::st.sync.aligned;" ::"r"(taddr),
-        "r"(taddr + (16u << 16)), GDN_W8(0), GDN_W8(8)
+        "add.u32 a, %0, 32;\n\t"
+        "tcgen05.st.sync.aligned.16x128b.x4.b32 [a], {%18,%19,%20,%21,%22,%23,%24,%25};\n\t"
+        "add.u32 a, %1, 32;\n\t"
+        "tcgen05.st.sync.aligned.16x128b.x4.b32 [a], {%26,%27,%28,%29,%30,%31,%32,%33};\n\t"
+        "add.u32 a, %0, 64;\n\t"
+        "tcgen05.st.sync.aligned.16x128b.x4.b32 [a], {%34,%35,%36,%37,%38,%39,%40,%41};\n\t"
+        "add.u32 a, %1, 64;\n\t"
+        "tcgen05.st.sync.aligned.16x128b.x4.b32 [a], {%42,%43,%44,%45,%46,%47,%48,%49};\n\t"
+        "add.u32 a, %0, 96;\n\t"
+        "tcgen05.st.sync.aligned.16x128b.x4.b32 [a], {%50,%51,%52,%53,%54,%55,%56,%57};\n\t"
+        "add.u32 a, %1, 96;\n\t"
+        "tcgen05.st.sync.aligned.16x128b.x4.b32 [a], {%58,%59,%60,%61,%62,%63,%64,%65};\n\t"
+        "tcgen05.wait::st.sync.aligned;\n\t}\n" ::"r"(taddr),
+        "r"(taddr + (16u << 16)), GDN_X8(w, 0), GDN_X8(w, 8), GDN_X8(x, 0), GDN_X8(x, 8), GDN_X8(y, 0), GDN_X8(y, 8),
+        GDN_X8(z, 0), GDN_X8(z, 8)
         : "memory");
+#undef GDN_X8
 }
 
 // 16x256b shape over 16 lanes from the lane field of taddr, NG = 2 or 4 groups of 8 columns:
@@ -555,6 +574,27 @@ __device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, float* v) {
             : "memory");
 #pragma unroll
         for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+    }
+}
+// Two of tmem_ld_frag<4> (a from ta, b from tb) with one wait.
+__device__ __forceinline__ void tmem_ld_frag4x2(uint32_t ta, uint32_t tb, float* a, float* b) {
+    uint32_t r[16], w[16];
+    __syncwarp();
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%32];\n\t"
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+        "{%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%33];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : GDN_R8(0), GDN_R8(8), "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]),
+          "=r"(w[7]), "=r"(w[8]), "=r"(w[9]), "=r"(w[10]), "=r"(w[11]), "=r"(w[12]), "=r"(w[13]), "=r"(w[14]),
+          "=r"(w[15])
+        : "r"(ta), "r"(tb)
+        : "memory");
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        a[i] = __uint_as_float(r[i]);
+        b[i] = __uint_as_float(w[i]);
     }
 }
 #undef GDN_R8
