@@ -143,8 +143,11 @@ la_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
         *abort_flag = 1;
         record_status(p.status, GDN_ERR_TIMEOUT);
     };
+    // All lanes wait (mbar_wait_warp): a lane that polls alone splits the warp while it is held, and the
+    // warp-collective instructions behind the wait (ldmatrix, whose lanes give each other's addresses) then
+    // fault.
     auto wwait = [&](int bar, uint32_t parity) {
-        const bool ok = mbar_wait_lane(&bars[bar], parity, abort_flag);
+        const bool ok = mbar_wait_warp(&bars[bar], parity, abort_flag);
         if (!ok && lane == 0) fail(bar);
         return ok;
     };
@@ -197,7 +200,7 @@ la_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
         constexpr uint32_t VLBO = D == 128 ? 8192 : 0;
         const uint32_t s0 = smem_u32(sm);
         bool ok = true;
-        auto wait = [&](int bar, uint32_t parity) { return mbar_wait_lane(&bars[bar], parity, abort_flag); };
+        auto wait = [&](int bar, uint32_t parity) { return mbar_wait_warp(&bars[bar], parity, abort_flag); };
         // products over the K steps of 16: A and B advance by constants
         auto steps = [&](auto f) {
             f(std::integral_constant<int, 0>());
@@ -234,7 +237,7 @@ la_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                     steps([&](auto kk) { mma_ts<ID_LOC, true>(tm + L::T_LOC, tm + L::T_V + 64 + 8 * kk, k + 128 * kk); });
                     steps([&](auto kk) { mma_ts<ID_LOC, true>(tm + L::T_LOC, tm + L::T_V + 96 + 8 * kk, k + 128 * kk); });
                     mma_commit(&bars[B_LOC]);
-                    mma_commit(&bars[B_EMPTY + s]);
+                    if (cc + L::STAGES < nch) mma_commit(&bars[B_EMPTY + s]);  // somebody waits
                 }
                 __syncwarp();
             }
@@ -251,7 +254,7 @@ la_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                     if constexpr (KB == 2)
                         steps([&](auto kk) { mma_ss<ID_SC, true>(tm + L::T_SC, k + 512 + 2 * kk, q + 512 + 2 * kk); });
                     mma_commit(&bars[B_SC]);
-                    mma_commit(&bars[B_EMPTY + s]);
+                    if (cc + L::STAGES < nch) mma_commit(&bars[B_EMPTY + s]);  // somebody waits
                 }
                 __syncwarp();
             }
@@ -278,7 +281,7 @@ la_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                     const uint32_t v = desc_lo(st + L::TILE, VLBO), pp = desc_lo(s0 + L::P + s * 8192, 8192);
                     steps([&](auto kk) { mma_ss<ID_YI, kk != 0>(tm + L::T_YI, v + 128 * kk, pp + 128 * kk); });
                     mma_commit(&bars[B_Y]);
-                    mma_commit(&bars[B_EMPTY + s]);
+                    if (cc + L::STAGES < nch) mma_commit(&bars[B_EMPTY + s]);  // somebody waits
                 }
                 __syncwarp();
             }

@@ -102,36 +102,6 @@ __device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity,
     return __all_sync(0xffffffffu, ok);
 }
 
-// mbar_wait_warp with one polling lane: 32 lanes' polls of one barrier are served one after the other (190
-// cycles for a phase that is complete, a few with one lane).  The poll is predicated, and every branch here
-// goes by a vote, so the warp stays converged for the warp-collective instructions that follow.
-__device__ __forceinline__ bool mbar_poll_lane(uint32_t addr, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
-        "mov.u32 %0, 0;\n\t"
-        "setp.eq.u32 q, %3, 0;\n\t"
-        "@q mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "@q selp.u32 %0, 1, 0, p;\n\t}\n"
-        : "=&r"(ok)
-        : "r"(addr), "r"(parity), "r"(threadIdx.x & 31)
-        : "memory");
-    return __any_sync(0xffffffffu, ok);
-}
-__device__ __forceinline__ bool mbar_wait_lane(uint64_t* bar, uint32_t parity, const volatile int* abort,
-                                               uint64_t limit_ns = 2000000000ull) {
-    const uint32_t addr = smem_u32(bar);
-    if (mbar_poll_lane(addr, parity)) return true;
-    const long long c0 = clock64();
-#pragma unroll 1
-    for (uint32_t it = 1;; ++it) {
-        if (mbar_poll_lane(addr, parity)) return true;
-        if ((it & 63) == 0 &&
-            __any_sync(0xffffffffu, *abort != 0 || clock64() - c0 > static_cast<long long>(limit_ns) * 2))
-            return false;
-    }
-}
-
 // Busy-polling form of mbar_wait for latency-critical waits: test_wait never suspends the
 // thread, so the wait ends within a few cycles of the phase completing.  Same limits and result
 // as mbar_wait.
