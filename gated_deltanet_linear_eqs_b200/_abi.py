@@ -105,6 +105,8 @@ class GdnError(RuntimeError):
 def load(path: str = LIB_PATH):
     """Load libgdn.so and declare every entry point; raises if it is missing."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(path):

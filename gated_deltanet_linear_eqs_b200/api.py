@@ -590,15 +590,20 @@ def _on_device(fn):
     @functools.wraps(fn)
     def call(first, *args, **kw):
         dev = first.get_device()
-        if dev < 0 or dev == torch._C._cuda_getDevice():
+        if dev < 0 or dev == _current_device():
             return fn(first, *args, **kw)
         with torch.cuda.device(dev):
             return fn(first, *args, **kw)
     return call
 
 
+_current_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else \
+    lambda dev: torch.cuda.current_stream(dev).cuda_stream
+_current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
+
+
 def _raw_stream(stream, dev):
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    return _current_stream(dev) if stream is None else stream.cuda_stream
 
 
 def _ptr(t):
@@ -801,25 +806,30 @@ def gdn_linear_attn_backward_varlen(q, k, v, log_decay, cu_seqlens, dy, s0=None,
     return dict(dq=dq, dk=dk, dv=dv, ds0=ds0)
 
 
-def _heads(t, name, dtype, dev, tokens=None, heads=None, d=None):
-    """A [T, heads, d] or [B, T, heads, d] tensor whose heads are contiguous and whose tokens are a
-    fixed distance apart; returns (tokens, heads, d, distance)."""
+def _heads(t, name, dtype, dev, tokens, heads, d):
+    """The token distance of a [T, heads, d] or [B, T, heads, d] tensor whose heads are contiguous and whose
+    tokens are evenly spaced (tokens, heads, d: what it must have; heads None: any)."""
     shape, st = t.shape, t.stride()
-    if len(shape) not in (3, 4):
-        raise ValueError(f"{name} must be [T, heads, d] or [B, T, heads, d]")
-    h, hd = shape[-2:]
-    n = shape[0] if len(shape) == 3 else shape[0] * shape[1]
-    ld = st[-3] if shape[-3] > 1 else st[0] if len(shape) == 4 and shape[0] > 1 else h * hd
     if t.dtype != dtype or t.get_device() != dev or dev < 0:
         _need(t, name, dtype)
-        raise ValueError(f"{name} must be {dtype} on the first tensor's device")
+        raise ValueError(f"{name} is on device {t.get_device()}, the first tensor on {dev}")
+    nd = len(shape)
+    if nd != 3 and nd != 4:
+        raise ValueError(f"{name} must be [T, heads, d] or [B, T, heads, d]")
+    h, hd = shape[-2], shape[-1]
+    row = h * hd
+    n = shape[0] if nd == 3 else shape[0] * shape[1]
+    if n != tokens or hd != d or (heads is not None and h != heads):
+        raise ValueError(f"{name} has {n} tokens of {h} heads of {hd}; expected {tokens} of "
+                         f"{'any' if heads is None else heads} heads of {d}")
+    if n <= 1:
+        ld = row
+    else:
+        ld = st[-3] if shape[-3] > 1 else st[0]
     if n and ((hd > 1 and st[-1] != 1) or (h > 1 and st[-2] != hd) or
-              (len(shape) == 4 and shape[0] > 1 and st[0] != shape[1] * ld)):
+              (nd == 4 and shape[0] > 1 and shape[1] > 1 and st[0] != shape[1] * ld)):
         raise ValueError(f"{name}: a token's heads must be contiguous and its tokens evenly spaced")
-    if (tokens is not None and n != tokens) or (heads is not None and h != heads) or \
-            (d is not None and hd != d):
-        raise ValueError(f"{name} has {n} tokens of {h} heads of {hd}; the other tensors do not")
-    return n, h, hd, ld if ld > h * hd or n > 1 else h * hd
+    return ld
 
 
 @_on_device
@@ -832,29 +842,34 @@ def gdn_rotary(q, k, positions, inv_freq, interleaved=False, inverse=False, scal
     per token), inv_freq fp32 on the device.  q_out / k_out may be q / k.  Returns (q_out, k_out)."""
     dt = _dtype(q, "q/k")
     dev = q.get_device()
-    T, Hq, d, ldq = _heads(q, "q", dt, dev)
-    Hk, ldk, ldko = 0, 0, 0
+    if q.dim() < 3:
+        raise ValueError("q must be [T, heads, d] or [B, T, heads, d]")
+    Hq, d = q.shape[-2:]
+    T = q.shape[0] if q.dim() == 3 else q.shape[0] * q.shape[1]
+    ldq = _heads(q, "q", dt, dev, T, None, d)
     _want(positions, "positions", torch.int32, positions.shape, dev)
+    half = inv_freq.numel()
+    _want(inv_freq, "inv_freq", torch.float32, (half,), dev)
     if positions.numel() != T:
         raise ValueError(f"positions must have {T} entries, got {positions.numel()}")
-    r = 2 * inv_freq.numel()
-    _want(inv_freq, "inv_freq", torch.float32, (r // 2,), dev)
     if k is None:
-        k_out = None
+        Hk = ldk = ldko = 0
+        kp = kop = k_out = None
     else:
-        _, Hk, _, ldk = _heads(k, "k", dt, dev, T, None, d)
+        Hk = k.shape[-2]
+        ldk = _heads(k, "k", dt, dev, T, None, d)
         if k_out is None:
-            k_out, ldko = torch.empty(k.shape, dtype=dt, device=k.device), Hk * d
+            k_out, ldko = torch.empty_like(k, memory_format=torch.contiguous_format), Hk * d
         else:
-            ldko = _heads(k_out, "k_out", dt, dev, T, Hk, d)[3]
+            ldko = _heads(k_out, "k_out", dt, dev, T, Hk, d)
+        kp, kop = k.data_ptr(), k_out.data_ptr()
     if q_out is None:
-        q_out, ldqo = torch.empty(q.shape, dtype=dt, device=q.device), Hq * d
+        q_out, ldqo = torch.empty_like(q, memory_format=torch.contiguous_format), Hq * d
     else:
-        ldqo = _heads(q_out, "q_out", dt, dev, T, Hq, d)[3]
-    rc = _lib().gdn_rotary(q.data_ptr(), _ptr(k), q_out.data_ptr(), _ptr(k_out), positions.data_ptr(),
-                           inv_freq.data_ptr(), T, Hq, Hk, d, r, ldq, ldk, ldqo, ldko,
-                           1 if interleaved else 0, 1 if inverse else 0, scale, _DT[dt],
-                           _raw_stream(stream, dev))
+        ldqo = _heads(q_out, "q_out", dt, dev, T, Hq, d)
+    rc = _lib().gdn_rotary(q.data_ptr(), kp, q_out.data_ptr(), kop, positions.data_ptr(), inv_freq.data_ptr(),
+                           T, Hq, Hk, d, 2 * half, ldq, ldk, ldqo, ldko, 1 if interleaved else 0,
+                           1 if inverse else 0, scale, _DT[dt], _raw_stream(stream, dev))
     if rc:
         _check(rc, "gdn_rotary")
     return q_out, k_out
@@ -889,11 +904,12 @@ def _rows(x, w, name):
     return dt, dev, shape, C, x.numel() // C if C else 0
 
 
-def _like(t, name, dtype, shape, dev, make):
+def _like(t, name, x, make):
+    """An optional output like x: checked, or made where it is wanted."""
     if t is not None:
-        _want(t, name, dtype, shape, dev)
+        _want(t, name, x.dtype, x.shape, x.get_device())
     elif make:
-        t = torch.empty(shape, dtype=dtype, device=dev)
+        t = torch.empty_like(x)
     return t
 
 
@@ -905,8 +921,8 @@ def gdn_add_rmsnorm(x, residual, w, eps=1e-6, o=None, h=None, stream=None):
     dt, dev, shape, C, rows = _rows(x, w, "x")
     if residual is not None:
         _want(residual, "residual", dt, shape, dev)
-    o = _like(o, "o", dt, shape, dev, True)
-    h = _like(h, "h", dt, shape, dev, residual is not None)
+    o = _like(o, "o", x, True)
+    h = _like(h, "h", x, residual is not None)
     rc = _lib().gdn_add_rmsnorm(x.data_ptr(), _ptr(residual), w.data_ptr(), o.data_ptr(), _ptr(h), rows, C,
                                 _DT[dt], eps, _raw_stream(stream, dev))
     if rc:
@@ -925,9 +941,12 @@ def gdn_add_rmsnorm_fp8(x, residual, w, eps=1e-6, group=0, o=None, scales=None, 
     group = C if group == 0 else group
     if group < 1 or C % group:
         raise ValueError(f"group {group} does not divide {C} columns")
-    o = _like(o, "o", torch.float8_e4m3fn, shape, dev, True)
-    scales = _like(scales, "scales", torch.float32, (*shape[:-1], C // group), dev, True)
-    h = _like(h, "h", dt, shape, dev, residual is not None)
+    if o is None:
+        o = torch.empty_like(x, dtype=torch.float8_e4m3fn)
+    else:
+        _want(o, "o", torch.float8_e4m3fn, shape, dev)
+    scales = _states(scales, "scales", (*shape[:-1], C // group), dev, True)
+    h = _like(h, "h", x, residual is not None)
     rc = _lib().gdn_add_rmsnorm_fp8(x.data_ptr(), _ptr(residual), w.data_ptr(), o.data_ptr(), scales.data_ptr(),
                                     _ptr(h), rows, C, group, _DT[dt], eps, _raw_stream(stream, dev))
     if rc:

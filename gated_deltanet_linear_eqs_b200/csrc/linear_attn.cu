@@ -24,7 +24,8 @@ struct LaSimt {
     static constexpr int S = V + C * VS;             // [D][VS]
     static constexpr int PT = S + D * VS;            // [C][LT]: row j, column i
     static constexpr int PW = PT + C * LT;           // e^{g n}, n = 0 .. C
-    static constexpr int BYTES = (PW + C + 4) * 4;
+    static constexpr int DEC = PW + C + 4;           // e^{g n} as two floats: of a full chunk, of the last one
+    static constexpr int BYTES = (DEC + 4) * 4;
     static constexpr int TK = D == 128 && VS == 64 ? 8 : 4;  // the state's tile of a thread
     static constexpr int TV = D * VS / 256 / TK;
     static constexpr int GV = VS / TV;                       // threads across the columns
@@ -43,6 +44,11 @@ la_simt_kernel(const LaParams p) {
     if (!la_find_segment(p, blockIdx.x / p.H, &sg)) return;
     if (p.state_only && sg.idx == (p.reverse ? 0 : sg.count - 1)) return;  // nobody starts behind it
     const float g = p.log_decay[h];
+    const int nch = (sg.len + C - 1) / C;
+    float2* dec2 = reinterpret_cast<float2*>(sm + M::DEC);
+    if (tid >= 192) {  // (one warp's worth of threads takes the 64-bit exponentials)
+        if (tid < 194) dec2[tid - 192] = la_power2(g, tid == 192 ? C : sg.len - (nch - 1) * C);
+    }
     for (int n = tid; n <= C; n += 256) pw[n] = expf(g * (float)n);
 
     // ---- the state this segment starts from: element e is (k, v column) in memory order
@@ -54,8 +60,11 @@ la_simt_kernel(const LaParams p) {
     } else {
         const int behind = p.reverse ? sg.count - 1 - sg.idx : sg.idx;
         const float* s_in = p.s_in ? p.s_in + ((size_t)sg.doc * p.H + h) * DD : nullptr;
-        const float2 full = la_power2(g, p.L);
-        const float2 last = la_power2(g, sg.doc_len - (sg.count - 1) * p.L);
+        float2 full = make_float2(0.f, 0.f), last = full;
+        if (behind > 0) {
+            full = la_power2(g, p.L);
+            last = la_power2(g, sg.doc_len - (sg.count - 1) * p.L);
+        }
 #pragma unroll 4
         for (int e = tid; e < D * VS; e += 256) {
             const int at = memory(e);
@@ -69,7 +78,6 @@ la_simt_kernel(const LaParams p) {
         }
     }
 
-    const int nch = (sg.len + C - 1) / C;
     const float* q = static_cast<const float*>(p.q);
     const float* k = static_cast<const float*>(p.k);
     const float* v = static_cast<const float*>(p.v);
@@ -173,7 +181,7 @@ la_simt_kernel(const LaParams p) {
         {
             constexpr int TK = M::TK, TV = M::TV;
             const int k0 = (tid / M::GV) * TK, v0 = (tid % M::GV) * TV;
-            const float2 dec = la_power2(g, n);
+            const float2 dec = dec2[n < C];
             float acc[TK][TV] = {};
 #pragma unroll 2
             for (int j = 0; j < n; j += 4) {  // (rows from n on are zero)
