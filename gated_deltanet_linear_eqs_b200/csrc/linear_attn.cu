@@ -9,212 +9,233 @@ namespace gdn {
 namespace {
 
 // ============================================================================ fp32 kernel
-// One CTA per (segment, head, VS columns of v), 256 threads, 64-token chunks on the CUDA cores: the columns
-// of the state and of the outputs do not depend on each other, so they are cut over CTAs at the price of
-// computing the scores in each.  Q^T and K^T (token fastest), V and the state's columns live in shared
-// memory; the products are register tiles: 4 x 4 for the scores, 2 tokens x VS/8 columns for the outputs,
-// TK x TV for the state.
+// One CTA per (segment, head, VS columns of v), 8 warps, 64-token chunks on warp-level tf32 products.  The
+// columns of the state and of the outputs do not depend on each other, so they are cut over CTAs at the price
+// of computing the scores in each.
+//
+// A product of fp32 values x y is taken as xh yh + xh yl + xl yh, x = xh + xl with xh = x rounded to tf32's 11
+// bits: what is left out is 2^-22 of |x y|, against 2^-24 for a fused multiply-add, and the sums stay fp32.
+// Tiles of a chunk (Q, K, V rows with padded strides, so that fragments are read without bank conflicts) come
+// by asynchronous copies into two buffers, the next chunk's while this one is computed; the state is kept in
+// fragments (registers) and copied to shared memory as the operand of Q S.
 template <int D, int VS>
-struct LaSimt {
+struct LaTf {
     static constexpr int C = kLaChunk;
-    static constexpr int LT = C + 4;                 // row stride of the transposed tiles
-    static constexpr int QT = 0;                     // [D][LT]
-    static constexpr int KT = QT + D * LT;           // [D][LT]
-    static constexpr int V = KT + D * LT;            // [C][VS]
-    static constexpr int S = V + C * VS;             // [D][VS]
-    static constexpr int PT = S + D * VS;            // [C][LT]: row j, column i
-    static constexpr int PW = PT + C * LT;           // e^{g n}, n = 0 .. C
+    static constexpr int LD = D + 4, LV = VS + 8, LP = C + 4;  // row strides in floats
+    static constexpr int Q = 0, K = Q + C * LD, V = K + C * LD, BUF = V + C * LV;
+    static constexpr int S = 2 * BUF;                // [D][LV]
+    static constexpr int P = S + D * LV;             // [i][j]
+    static constexpr int PW = P + C * LP;            // e^{g n}, n = 0 .. C
     static constexpr int DEC = PW + C + 4;           // e^{g n} as two floats: of a full chunk, of the last one
     static constexpr int BYTES = (DEC + 4) * 4;
-    static constexpr int TK = D == 128 && VS == 64 ? 8 : 4;  // the state's tile of a thread
-    static constexpr int TV = D * VS / 256 / TK;
-    static constexpr int GV = VS / TV;                       // threads across the columns
+    static constexpr int SG = D / 16;                // 16-row tiles of the state
+    static constexpr int SN = VS / 8 / (8 / SG);     // its 8-column tiles of a warp (D = 64: two warps a row tile)
+    static constexpr int YN = VS / 16;               // 8-column tiles of the outputs of a warp (4 x 2 warps)
 };
+
+__device__ __forceinline__ void tf_split(float x, uint32_t& hi, uint32_t& lo) {
+    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(hi) : "f"(x));
+    lo = __float_as_uint(x - __uint_as_float(hi));
+}
+__device__ __forceinline__ void tf_mma(float* c, const uint32_t* a, const uint32_t* b) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+// acc[n] += A (16 x k) B (k x 8 N): lane 4 r + c reads a(r, c), a(r + 8, c), a(r, c + 4), a(r + 8, c + 4) of each
+// 8-wide step of A and b(c, r), b(c + 4, r) of each 8-column tile of B.  The tensor cores' sums are truncated,
+// not rounded, so they are kept short: the small products in sums of their own, the large ones 8 steps long,
+// added to acc by the CUDA cores (an error of 3e-7 of y, 1.1e-6 with one long sum).
+template <int N, typename FA, typename FB>
+__device__ __forceinline__ void tf_product(float (*acc)[4], int k, FA a, FB b) {
+#pragma unroll 1
+    for (int k0 = 0; k0 < k; k0 += 64) {
+        float big[N][4] = {}, small[N][4] = {};
+#pragma unroll 2
+        for (int x = k0; x < k0 + 64; x += 8) {
+            uint32_t ah[4], al[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) tf_split(a(8 * (e & 1), x + 4 * (e >> 1)), ah[e], al[e]);
+#pragma unroll
+            for (int n = 0; n < N; ++n) {
+                uint32_t bh[2], bl[2];
+                tf_split(b(x, 8 * n), bh[0], bl[0]);
+                tf_split(b(x + 4, 8 * n), bh[1], bl[1]);
+                tf_mma(small[n], al, bh);
+                tf_mma(big[n], ah, bh);
+                tf_mma(small[n], ah, bl);
+            }
+        }
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[n][e] += big[n][e] + small[n][e];
+    }
+}
+__device__ __forceinline__ void copy16(float* dst, const float* src, bool there) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(sm100::smem_u32(dst)), "l"(src),
+                 "r"(there ? 16 : 0)
+                 : "memory");
+}
 
 template <int D, int VS>
 __global__ void __launch_bounds__(256)
-la_simt_kernel(const LaParams p) {
-    using M = LaSimt<D, VS>;
-    constexpr int C = M::C, LT = M::LT;
-    extern __shared__ float sm[];
-    float *qt = sm + M::QT, *kt = sm + M::KT, *vs = sm + M::V, *S = sm + M::S, *pt = sm + M::PT,
-          *pw = sm + M::PW;
+la_tf_kernel(const LaParams p) {
+    using M = LaTf<D, VS>;
+    constexpr int C = M::C;
+    extern __shared__ float4 sm4[];
+    float* sm = reinterpret_cast<float*>(sm4);
+    float *S = sm + M::S, *P = sm + M::P, *pw = sm + M::PW;
     const int h = blockIdx.x % p.H, tid = threadIdx.x, c0 = blockIdx.y * VS;
+    const int warp = tid >> 5, lane = tid & 31, lr = lane >> 2, lc = lane & 3;
     LaSegment sg;
     if (!la_find_segment(p, blockIdx.x / p.H, &sg)) return;
     if (p.state_only && sg.idx == (p.reverse ? 0 : sg.count - 1)) return;  // nobody starts behind it
-    const float g = p.log_decay[h];
     const int nch = (sg.len + C - 1) / C;
-    float2* dec2 = reinterpret_cast<float2*>(sm + M::DEC);
-    if (tid >= 192) {  // (one warp's worth of threads takes the 64-bit exponentials)
-        if (tid < 194) dec2[tid - 192] = la_power2(g, tid == 192 ? C : sg.len - (nch - 1) * C);
-    }
-    for (int n = tid; n <= C; n += 256) pw[n] = expf(g * (float)n);
-
-    // ---- the state this segment starts from: element e is (k, v column) in memory order
-    const size_t DD = (size_t)D * D;
-    auto memory = [&](int e) { return p.state_t ? (c0 + e / D) * D + e % D : e / VS * D + c0 + e % VS; };
-    auto local_at = [&](int e) { return p.state_t ? e % D * VS + e / D : e; };
-    if (p.state_only) {
-        for (int e = tid; e < D * VS; e += 256) S[e] = 0.f;
-    } else {
-        const int behind = p.reverse ? sg.count - 1 - sg.idx : sg.idx;
-        const float* s_in = p.s_in ? p.s_in + ((size_t)sg.doc * p.H + h) * DD : nullptr;
-        float2 full = make_float2(0.f, 0.f), last = full;
-        if (behind > 0) {
-            full = la_power2(g, p.L);
-            last = la_power2(g, sg.doc_len - (sg.count - 1) * p.L);
-        }
-#pragma unroll 4
-        for (int e = tid; e < D * VS; e += 256) {
-            const int at = memory(e);
-            float x = s_in ? s_in[at] : 0.f;
-            for (int b = 0; b < behind; ++b) {
-                const int r = p.reverse ? sg.count - 1 - b : b;
-                const float2 w = r == sg.count - 1 ? last : full;
-                x = fmaf(x, w.x, fmaf(x, w.y, p.local[((size_t)(sg.first_id + r) * p.H + h) * DD + at]));
-            }
-            S[local_at(e)] = x;
-        }
-    }
-
     const float* q = static_cast<const float*>(p.q);
     const float* k = static_cast<const float*>(p.k);
     const float* v = static_cast<const float*>(p.v);
     const int Hq = p.H / p.qdiv, Hk = p.H / p.kdiv, Hv = p.H / p.vdiv;
-    const int warp = tid >> 5, lane = tid & 31;
-    for (int cc = 0; cc < nch; ++cc) {
-        const int c = p.reverse ? nch - 1 - cc : cc;
-        const int n = min(C, sg.len - c * C);
+    auto place = [&](int cc) { return p.reverse ? nch - 1 - cc : cc; };
+    // rows past the end of the document are zero (and not read)
+    auto fetch = [&](int cc) {
+        float* to = sm + (cc & 1) * M::BUF;
+        const int c = place(cc), n = min(C, sg.len - c * C);
         const size_t tok = (size_t)sg.t0 + (size_t)c * C;
-        const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
-        __syncthreads();  // the last chunk's tiles are read
-        // rows past the end of the document are zero; a warp takes 8 tokens x 16 columns, so that the
-        // transposed stores fall into different banks
-        {
-            const int i = (warp & 7) * 8 + (lane & 7);
-#pragma unroll
-            for (int x0 = 0; x0 < D; x0 += 16) {
-                const int x = x0 + (lane >> 3) * 4;
-                const float4 a = i < n ? load4(k + ((tok + i) * Hk + h / p.kdiv) * D + x) : zero;
-                kt[(x + 0) * LT + i] = a.x; kt[(x + 1) * LT + i] = a.y;
-                kt[(x + 2) * LT + i] = a.z; kt[(x + 3) * LT + i] = a.w;
-                if (!p.state_only) {
-                    const float4 w = i < n ? load4(q + ((tok + i) * Hq + h / p.qdiv) * D + x) : zero;
-                    qt[(x + 0) * LT + i] = w.x; qt[(x + 1) * LT + i] = w.y;
-                    qt[(x + 2) * LT + i] = w.z; qt[(x + 3) * LT + i] = w.w;
-                }
-            }
+        for (int e = tid; e < C * (D / 4); e += 256) {
+            const int i = e / (D / 4), x = (e % (D / 4)) * 4;
+            const size_t at = i < n ? tok + i : tok;
+            copy16(to + M::K + i * M::LD + x, k + (at * Hk + h / p.kdiv) * D + x, i < n);
+            if (!p.state_only) copy16(to + M::Q + i * M::LD + x, q + (at * Hq + h / p.qdiv) * D + x, i < n);
         }
         for (int e = tid; e < C * (VS / 4); e += 256) {
             const int i = e / (VS / 4), x = (e % (VS / 4)) * 4;
-            store4(vs + i * VS + x, i < n ? load4(v + ((tok + i) * Hv + h / p.vdiv) * D + c0 + x) : zero);
+            const size_t at = i < n ? tok + i : tok;
+            copy16(to + M::V + i * M::LV + x, v + (at * Hv + h / p.vdiv) * D + c0 + x, i < n);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    if (nch > 0) fetch(0);
+
+    const float g = p.log_decay[h];
+    float2* dec2 = reinterpret_cast<float2*>(sm + M::DEC);
+    if (tid >= 192 && tid < 194) dec2[tid - 192] = la_power2(g, tid == 192 ? C : sg.len - (nch - 1) * C);
+    for (int n = tid; n <= C; n += 256) pw[n] = expf(g * (float)n);
+
+    // ---- the state: this warp's 16 rows k, SN tiles of 8 columns v, in fragments
+    const int sk = warp % M::SG * 16 + lr, sv = warp / M::SG * M::SN * 8;
+    const size_t DD = (size_t)D * D;
+    auto memory = [&](int n, int e) {  // element e of tile n
+        const int kk = sk + 8 * (e >> 1), vv = c0 + sv + 8 * n + 2 * lc + (e & 1);
+        return p.state_t ? vv * D + kk : kk * D + vv;
+    };
+    float st[M::SN][4];
+    const float* s_in = !p.state_only && p.s_in ? p.s_in + ((size_t)sg.doc * p.H + h) * DD : nullptr;
+#pragma unroll
+    for (int n = 0; n < M::SN; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) st[n][e] = s_in ? s_in[memory(n, e)] : 0.f;
+    const int behind = p.state_only ? 0 : p.reverse ? sg.count - 1 - sg.idx : sg.idx;
+    if (behind > 0) {
+        const float2 full = la_power2(g, p.L), last = la_power2(g, sg.doc_len - (sg.count - 1) * p.L);
+        for (int b = 0; b < behind; ++b) {
+            const int r = p.reverse ? sg.count - 1 - b : b;
+            const float2 w = r == sg.count - 1 ? last : full;
+            const float* loc = p.local + ((size_t)(sg.first_id + r) * p.H + h) * DD;
+#pragma unroll
+            for (int n = 0; n < M::SN; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) st[n][e] = fmaf(st[n][e], w.x, fmaf(st[n][e], w.y, loc[memory(n, e)]));
+        }
+    }
+    auto publish = [&]() {
+#pragma unroll
+        for (int n = 0; n < M::SN; ++n)
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+                *reinterpret_cast<float2*>(S + (sk + 8 * r) * M::LV + sv + 8 * n + 2 * lc) =
+                    make_float2(st[n][2 * r], st[n][2 * r + 1]);
+    };
+    if (!p.state_only) publish();
+
+    const int i0 = warp % 4 * 16, half = warp / 4;  // this warp's tokens and half of the columns
+    for (int cc = 0; cc < nch; ++cc) {
+        const int c = place(cc), n = min(C, sg.len - c * C);
+        const float *qs = sm + (cc & 1) * M::BUF + M::Q, *ks = sm + (cc & 1) * M::BUF + M::K,
+                    *vs = sm + (cc & 1) * M::BUF + M::V;
+        if (cc + 1 < nch) {
+            fetch(cc + 1);
+            asm volatile("cp.async.wait_group 1;" ::: "memory");
+        } else {
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
         }
         __syncthreads();
         if (!p.state_only) {
-            // ---- scores, their decay and mask: pt[j][i]
-            {
-                const int j0 = (tid / 16) * 4, i0 = (tid % 16) * 4;
-                float acc[4][4] = {};
-#pragma unroll 16
-                for (int x = 0; x < D; ++x) {
-                    const float4 a = load4(kt + x * LT + j0), b = load4(qt + x * LT + i0);
-                    const float av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w};
+            // ---- scores of tokens i0 .. +15, keys 32 half .. +31, decayed and masked
+            float acc[4][4] = {};
+            tf_product<4>(acc, D, [&](int r, int x) { return qs[(i0 + lr + r) * M::LD + x + lc]; },
+                          [&](int x, int m) { return ks[(32 * half + m + lr) * M::LD + x + lc]; });
 #pragma unroll
-                    for (int r = 0; r < 4; ++r)
+            for (int m = 0; m < 4; ++m)
 #pragma unroll
-                        for (int s = 0; s < 4; ++s) acc[r][s] = fmaf(av[r], bv[s], acc[r][s]);
-                }
+                for (int r = 0; r < 2; ++r) {
+                    float o[2];
+                    const int i = i0 + lr + 8 * r, j = 32 * half + 8 * m + 2 * lc;
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    float o[4];
-#pragma unroll
-                    for (int s = 0; s < 4; ++s) {
-                        const int d = p.reverse ? j0 + r - (i0 + s) : i0 + s - (j0 + r);
-                        o[s] = d >= 0 ? acc[r][s] * pw[d] * p.p_scale : 0.f;
+                    for (int e = 0; e < 2; ++e) {
+                        const int d = p.reverse ? j + e - i : i - j - e;
+                        o[e] = d >= 0 ? acc[m][2 * r + e] * pw[d] * p.p_scale : 0.f;
                     }
-                    store4(pt + (j0 + r) * LT + i0, make_float4(o[0], o[1], o[2], o[3]));
+                    *reinterpret_cast<float2*>(P + i * M::LP + j) = make_float2(o[0], o[1]);
                 }
-            }
             __syncthreads();
-            // ---- outputs: a warp's 8 rows, 2 a thread; VS / 8 columns
-            constexpr int CPL = VS / 8;
-            float acc[2][CPL] = {};
-            const int i0 = warp * 8 + (lane >> 3) * 2, s0 = (lane & 7) * CPL;
-            auto product = [&](const float* a, const float* b, int len) {
-#pragma unroll 16
-                for (int x = 0; x < len; ++x) {
-                    const float2 u = *reinterpret_cast<const float2*>(a + x * LT + i0);
-                    float bv[CPL];
-#pragma unroll
-                    for (int s = 0; s < CPL; s += 4) {
-                        const float4 w = load4(b + x * VS + s0 + s);
-                        bv[s] = w.x; bv[s + 1] = w.y; bv[s + 2] = w.z; bv[s + 3] = w.w;
-                    }
-#pragma unroll
-                    for (int s = 0; s < CPL; ++s) {
-                        acc[0][s] = fmaf(u.x, bv[s], acc[0][s]);
-                        acc[1][s] = fmaf(u.y, bv[s], acc[1][s]);
-                    }
-                }
-            };
-            product(qt, S, D);
+            // ---- outputs of tokens i0 .. +15, columns VS / 2 half ..
+            float y[M::YN][4] = {};
+            const int v0 = VS / 2 * half;
+            tf_product<M::YN>(y, D, [&](int r, int x) { return qs[(i0 + lr + r) * M::LD + x + lc]; },
+                              [&](int x, int m) { return S[(x + lc) * M::LV + v0 + m + lr]; });
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-                const int i = i0 + r;
+                const int i = i0 + lr + 8 * r;
                 const float f = i < n ? pw[p.reverse ? n - 1 - i : i + 1] * p.inter_scale : 0.f;
 #pragma unroll
-                for (int s = 0; s < CPL; ++s) acc[r][s] *= f;
+                for (int m = 0; m < M::YN; ++m) {
+                    y[m][2 * r] *= f;
+                    y[m][2 * r + 1] *= f;
+                }
             }
-            product(pt, vs, C);
+            tf_product<M::YN>(y, C, [&](int r, int x) { return P[(i0 + lr + r) * M::LP + x + lc]; },
+                              [&](int x, int m) { return vs[(x + lc) * M::LV + v0 + m + lr]; });
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-                if (i0 + r >= n) continue;
-                float* o = static_cast<float*>(p.out) + ((tok + i0 + r) * p.H + h) * D + c0 + s0;
+                const int i = i0 + lr + 8 * r;
+                if (i >= n) continue;
+                float* o = static_cast<float*>(p.out) + (((size_t)sg.t0 + (size_t)c * C + i) * p.H + h) * D + c0 + v0;
 #pragma unroll
-                for (int s = 0; s < CPL; s += 4)
-                    store4(o + s, make_float4(acc[r][s], acc[r][s + 1], acc[r][s + 2], acc[r][s + 3]));
+                for (int m = 0; m < M::YN; ++m)
+                    *reinterpret_cast<float2*>(o + 8 * m + 2 * lc) = make_float2(y[m][2 * r], y[m][2 * r + 1]);
             }
-            __syncthreads();  // S is read above
         }
-        // ---- state
+        // ---- state: the chunk's own sum, weighted in token j, then added to the decayed state
         {
-            constexpr int TK = M::TK, TV = M::TV;
-            const int k0 = (tid / M::GV) * TK, v0 = (tid % M::GV) * TV;
+            float acc[M::SN][4] = {};
+            tf_product<M::SN>(acc, C,
+                              [&](int r, int x) {
+                                  const int j = x + lc;
+                                  const float f = p.reverse ? pw[j + 1] : j < n ? pw[n - 1 - j] : 0.f;
+                                  return ks[j * M::LD + sk + r] * (f * p.state_scale);
+                              },
+                              [&](int x, int m) { return vs[(x + lc) * M::LV + sv + m + lr]; });
             const float2 dec = dec2[n < C];
-            float acc[TK][TV] = {};
-#pragma unroll 2
-            for (int j = 0; j < n; j += 4) {  // (rows from n on are zero)
-                float kw[TK][4], f[4];
 #pragma unroll
-                for (int u = 0; u < 4; ++u)
-                    f[u] = j + u < n ? pw[p.reverse ? j + u + 1 : n - 1 - j - u] * p.state_scale : 0.f;
+            for (int m = 0; m < M::SN; ++m)
 #pragma unroll
-                for (int r = 0; r < TK; ++r) {
-                    const float4 a = load4(kt + (k0 + r) * LT + j);
-                    kw[r][0] = a.x * f[0]; kw[r][1] = a.y * f[1]; kw[r][2] = a.z * f[2]; kw[r][3] = a.w * f[3];
-                }
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    float bv[TV];
-#pragma unroll
-                    for (int s = 0; s < TV; ++s) bv[s] = vs[(j + u) * VS + v0 + s];
-#pragma unroll
-                    for (int r = 0; r < TK; ++r)
-#pragma unroll
-                        for (int s = 0; s < TV; ++s) acc[r][s] = fmaf(kw[r][u], bv[s], acc[r][s]);
-                }
-            }
-#pragma unroll
-            for (int r = 0; r < TK; ++r)
-#pragma unroll
-                for (int s = 0; s < TV; ++s) {
-                    float* x = S + (k0 + r) * VS + v0 + s;
-                    *x = fmaf(*x, dec.x, fmaf(*x, dec.y, acc[r][s]));
-                }
+                for (int e = 0; e < 4; ++e) st[m][e] = fmaf(st[m][e], dec.x, fmaf(st[m][e], dec.y, acc[m][e]));
         }
+        __syncthreads();  // S, P and this chunk's tiles are read
+        if (!p.state_only && cc + 1 < nch) publish();
     }
-    __syncthreads();
     // ---- what is behind the segment: its local state, or the document's last state
     float* dst = nullptr;
     if (p.state_only)
@@ -222,15 +243,18 @@ la_simt_kernel(const LaParams p) {
     else if (p.s_out && sg.idx == (p.reverse ? 0 : sg.count - 1))
         dst = p.s_out + ((size_t)sg.doc * p.H + h) * DD;
     if (dst)
-        for (int e = tid; e < D * VS; e += 256) dst[memory(e)] = S[local_at(e)];
+#pragma unroll
+        for (int n = 0; n < M::SN; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) dst[memory(n, e)] = st[n][e];
 }
 
 template <int D, int VS>
-cudaError_t launch_simt(const LaParams& p, int nseg, cudaStream_t st) {
-    cudaError_t e = cudaFuncSetAttribute(la_simt_kernel<D, VS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         LaSimt<D, VS>::BYTES);
+cudaError_t launch_tf(const LaParams& p, int nseg, cudaStream_t st) {
+    cudaError_t e = cudaFuncSetAttribute(la_tf_kernel<D, VS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         LaTf<D, VS>::BYTES);
     if (e != cudaSuccess) return e;
-    la_simt_kernel<D, VS><<<dim3((unsigned)((size_t)nseg * p.H), D / VS), 256, LaSimt<D, VS>::BYTES, st>>>(p);
+    la_tf_kernel<D, VS><<<dim3((unsigned)((size_t)nseg * p.H), D / VS), 256, LaTf<D, VS>::BYTES, st>>>(p);
     return cudaGetLastError();
 }
 
@@ -238,8 +262,8 @@ cudaError_t launch_pass(const LaParams& p, int nseg, int d, int dtype, cudaStrea
     if (dtype == GDN_BF16) return launch_la_tc(p, nseg, d, st);
     // 32 columns a CTA while 64 would leave SMs idle: the scores are then computed once more
     const bool wide = (long long)nseg * p.H * (d / 64) >= 148;
-    if (d == 128) return wide ? launch_simt<128, 64>(p, nseg, st) : launch_simt<128, 32>(p, nseg, st);
-    return wide ? launch_simt<64, 64>(p, nseg, st) : launch_simt<64, 32>(p, nseg, st);
+    if (d == 128) return wide ? launch_tf<128, 64>(p, nseg, st) : launch_tf<128, 32>(p, nseg, st);
+    return wide ? launch_tf<64, 64>(p, nseg, st) : launch_tf<64, 32>(p, nseg, st);
 }
 
 // ============================================================================ shared heads
