@@ -499,7 +499,7 @@ static int check_attn(const float* log_decay, int H, int Hk, int dk, int dv, int
 static bool ok_tokens(int num_seqs, int T, int H, bool packed) {
     const long long tokens = packed ? T : (long long)num_seqs * T;
     const long long segments = tokens / 64 + num_seqs;
-    return tokens < (1ll << 31) - 64 && segments * H < (1ll << 31);
+    return tokens < (1ll << 31) - 64 && segments * H < (1ll << 31) - 65536;
 }
 
 int gdn_linear_attn_workspace_bytes(int backward, int B, int T, int H, int Hk, int dk, int dv, int num_seqs,

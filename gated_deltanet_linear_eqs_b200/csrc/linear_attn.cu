@@ -258,10 +258,10 @@ cudaError_t launch_tf(const LaParams& p, int nseg, cudaStream_t st) {
     return cudaGetLastError();
 }
 
-cudaError_t launch_pass(const LaParams& p, int nseg, int d, int dtype, cudaStream_t st) {
-    if (dtype == GDN_BF16) return launch_la_tc(p, nseg, d, st);
-    // 32 columns a CTA while 64 would leave SMs idle: the scores are then computed once more
-    const bool wide = (long long)nseg * p.H * (d / 64) >= 148;
+cudaError_t launch_f32(const LaParams& p, int nseg, int d, cudaStream_t st) {
+    // 32 columns a CTA where all those CTAs run at once (the scores are then computed more often): 64 tokens of
+    // 74 heads of 64 take 9.6 us so and 12.1 us with 64 columns, of 100 heads 17.4 and 12.2 us
+    const bool wide = (long long)nseg * p.H * (d / 32) > 148;
     if (d == 128) return wide ? launch_tf<128, 64>(p, nseg, st) : launch_tf<128, 32>(p, nseg, st);
     return wide ? launch_tf<64, 64>(p, nseg, st) : launch_tf<64, 32>(p, nseg, st);
 }
@@ -376,23 +376,31 @@ cudaError_t launch_step(const LaStepArgs& a, cudaStream_t st) {
 }
 
 // ============================================================================ plan
-// One segment per document where the documents alone give every SM work; otherwise segments long
-// enough for their start states (d x d fp32 each) to stay a small part of their tokens.
-constexpr int kMinSegment[2] = {512, 64};  // bf16, fp32 (whose chunks take about ten times as long)
+// Chains are cut where there are fewer of them than SMs.  bf16: equal shares of the CTAs, where la_cut_pays (of packed
+// documents only the sum of the lengths is known here: the kernels decide once more).  fp32: segments of at least
+// one chunk, whose products take several times as long: cut or not, a document of 128 tokens takes 20 or 24 us
+// with 2 heads of 128, 46 or 47 us with 64; of 1024 tokens 28 or 166 us and 293 or 333 us.
 
 LaPlan make_plan(int num_seqs, int T, int H, bool packed, int dtype) {
     const long long tokens = packed ? T : (long long)num_seqs * T;
     LaPlan pl;
     pl.L = (T + kLaChunk - 1) / kLaChunk * kLaChunk;
-    if ((long long)num_seqs * H < 148) {
+    pl.split = (long long)num_seqs * H < kLaCtas && T > kLaChunk;
+    if (dtype == GDN_BF16) {
+        const long long longest = (T + kLaChunk - 1) / kLaChunk;
+        pl.split = pl.split && la_cut_pays(longest, (packed ? 1 : num_seqs) * longest * H);
+    } else if (pl.split) {
         const long long want = (tokens * H + 147) / 148;
-        long long L = (want + kLaChunk - 1) / kLaChunk * kLaChunk;
-        if (L < kMinSegment[dtype]) L = kMinSegment[dtype];
+        const long long L = (want + kLaChunk - 1) / kLaChunk * kLaChunk;
         if (L < pl.L) pl.L = (int)L;
+        pl.split = pl.L < T;
     }
-    pl.split = pl.L < T;
     pl.nseg = packed ? T / pl.L + num_seqs : num_seqs * ((T + pl.L - 1) / pl.L);
     return pl;
+}
+
+size_t local_bytes(const LaPlan& pl, int H, int d, int dtype) {
+    return !pl.split ? 0 : (dtype == GDN_BF16 ? (size_t)kLaCtas : (size_t)pl.nseg * H) * d * d * sizeof(float);
 }
 
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
@@ -405,8 +413,7 @@ LaLayout la_layout(bool backward, int num_seqs, int T, int H, int Hk, int d, boo
     l.off_local = 0;
     l.off_dk = 0;
     for (int dtype : {GDN_BF16, GDN_FP32}) {  // the size serves both types
-        const LaPlan pl = make_plan(num_seqs, T, H, packed, dtype);
-        const size_t n = pl.split ? up256((size_t)pl.nseg * H * d * d * 4) : 0;
+        const size_t n = up256(local_bytes(make_plan(num_seqs, T, H, packed, dtype), H, d, dtype));
         l.off_dk = n > l.off_dk ? n : l.off_dk;
     }
     l.off_dv = l.off_dk;
@@ -432,6 +439,7 @@ cudaError_t launch_linear_attn(const LaArgs& a, cudaStream_t st) {
     p.T = a.T;
     p.H = a.H;
     p.L = pl.L;
+    p.walk = pl.split ? LA_WALK_CUT : packed && a.num_seqs <= kLaDocs ? LA_WALK_SORTED : LA_WALK_TURN;
     p.status = a.status;
     cudaError_t e;
     const auto roles = [&](const void* q, int qdiv, const void* k, int kdiv, const void* v, int vdiv) {
@@ -439,13 +447,21 @@ cudaError_t launch_linear_attn(const LaArgs& a, cudaStream_t st) {
     };
     const auto run = [&](bool state_only) {
         p.state_only = state_only;
-        return launch_pass(p, pl.nseg, a.d, a.dtype, st);
+        return a.dtype == GDN_BF16 ? launch_la_tc(p, a.d, st) : launch_f32(p, pl.nseg, a.d, st);
+    };
+    // the local states, and (bf16) from them the states between the pieces: p's roles are set, s_in not yet used
+    const auto locals = [&](const float* s_in) {
+        p.s_in = nullptr;
+        p.s_out = nullptr;
+        if (cudaError_t f = run(true)) return f;
+        p.s_in = s_in;
+        return a.dtype == GDN_BF16 ? launch_la_scan(p, a.d, st) : cudaSuccess;
     };
     // forward in time: the local states of k, v, then y from s0 (or dq from s0 and dy)
     p.p_scale = p.inter_scale = a.scale;
     p.state_scale = 1.f;
     roles(a.q, 1, a.k, group, a.v, group);
-    if (pl.split && (e = run(true)) != cudaSuccess) return e;
+    if (pl.split && (e = locals(a.s0)) != cudaSuccess) return e;
     p.s_in = a.s0;
     if (a.dy == nullptr) {
         p.out = a.y;
@@ -462,7 +478,7 @@ cudaError_t launch_linear_attn(const LaArgs& a, cudaStream_t st) {
     p.state_scale = a.scale;
     p.state_t = 0;
     roles(a.k, group, a.q, 1, a.dy, 1);
-    if (pl.split && (e = run(true)) != cudaSuccess) return e;
+    if (pl.split && (e = locals(a.ds_final)) != cudaSuccess) return e;
     float* part_k = reinterpret_cast<float*>(ws + lay.off_dk);
     float* part_v = reinterpret_cast<float*>(ws + lay.off_dv);
     p.out_f32 = group > 1;

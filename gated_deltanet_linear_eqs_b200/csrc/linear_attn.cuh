@@ -14,9 +14,11 @@
 // dL/dS before the run.  So one kernel, told the places ("roles") and the direction, runs all of
 // them.
 //
-// Documents are cut into segments of L tokens that run side by side.  A first pass sums every
-// segment's own k v^T ("local" states); the second starts each segment from
-// sum over the segments behind it of e^{g (tokens between)} local + e^{g (..)} s_in.
+// Where the documents and heads are too few for the SMs, a chain (document, head) is cut along time.  A first
+// pass sums every piece's own k v^T ("local" states), and a piece starts from
+// sum over the pieces behind it of e^{g (tokens between)} local + e^{g (..)} s_in.
+// fp32: segments of L tokens, one CTA each (LaSegment).  bf16: the chains' chunks are laid end to end and cut
+// into equal shares, one CTA each, so that a CTA walks the end of one chain and the start of the next (LaPiece).
 #pragma once
 
 #include "common.cuh"
@@ -26,18 +28,24 @@ namespace gdn {
 
 constexpr int kLaChunk = 64;
 
+// How the bf16 kernel's CTAs share the chains: in turn; cut into equal shares; or, packed documents of unlike
+// lengths, longest first, in turn, back and forth (24 documents of 0 to 1200 tokens with 16 heads of 64: 43 us,
+// in plain turn 60 us, left to the hardware a block each 44 us).
+enum { LA_WALK_TURN = 0, LA_WALK_CUT = 1, LA_WALK_SORTED = 2 };
+
 struct LaParams {
     const void *q, *k, *v;  // roles: [T, heads, d] each
     void* out;              // [T, H, d]
     const float* log_decay;
     const float* s_in;      // state the first (reversed: last) segment starts from; NULL = 0
     float* s_out;           // state behind the last (reversed: first) segment; NULL = not written
-    float* local;           // [segments, H, d, d] local states (NULL: one segment per document)
+    float* local;           // fp32: [segments, H, d, d], bf16: [CTAs, d, d] local states (NULL: no chain is cut)
     const int32_t* cu;      // packed documents, or NULL: dense sequences of T tokens
     int num_seqs, T;        // T: tokens per sequence (dense) or of the packed stream
     int H;                  // states (and output heads)
     int qdiv, kdiv, vdiv;   // states per head of the role's tensor
-    int L;                  // segment length, a multiple of kLaChunk
+    int L;                  // fp32: segment length, a multiple of kLaChunk
+    int walk;               // bf16: LA_WALK_*
     float p_scale, inter_scale, state_scale;
     int reverse;
     int state_t;            // states in memory are [v role][k role] rather than [k role][v role]
@@ -124,13 +132,138 @@ __device__ __forceinline__ size_t la_state_index(int kk, int vv, int state_t) {
     return state_t ? (size_t)vv * D + kk : (size_t)kk * D + vv;
 }
 
+// ---- bf16: the shares of the CTAs -------------------------------------------------------------
+// A chain of c chunks counts kLaStart + c units, kLaStart for what its start and end cost; all chains' units are
+// laid end to end (document by document, its heads in turn) and cut into equal shares of at least kLaShare
+// units.  A CTA whose share ends inside a chain leaves that chain's local state in slot [CTA].
+constexpr int kLaStart = 3, kLaShare = 8;
+constexpr int kLaCtas = 148;   // one a SM
+constexpr int kLaDocs = 147;   // documents that are cut (which needs fewer chains than SMs) or sorted at most
+
+// A cut pays where the longest chain takes longer than the two passes over the shares: uncut, a chain takes
+// 7 + 1.5 us a chunk; cut, 31 + 2.8 us a chunk of a share (three launches, the first pass 1.1, the second 1.9;
+// d = 128).  Measured uncut and cut: one document of 2048 tokens 52 and 41 us with 16 heads, 54 and 66 us with 64,
+// 59 and 103 us with 120; of 1024 tokens with 16 heads 29 and 40 us.  d = 64 and the gradients lie close by.
+__host__ __device__ inline bool la_cut_pays(long long longest, long long all) {
+    return longest > 16 + 2 * all / kLaCtas;
+}
+
+struct LaDocs {
+    int cut;                  // LA_WALK_CUT, and the lengths are such that it pays
+    int count;                // pieces of this CTA (cut)
+    int units[kLaDocs + 1];   // cut: units of one head before each document; sorted: the documents by length
+    int t0[kLaDocs], len[kLaDocs];
+};
+struct LaPiece {
+    int doc, h;
+    int t0;            // the document's first token
+    int nch, last;     // its chunks, and the tokens of the last
+    int w0, w1;        // the chunks of this piece, counted in walking order
+    int unused;
+    __device__ bool starts() const { return w0 == 0; }
+    __device__ bool ends() const { return w1 == nch; }
+};
+
+__device__ __forceinline__ void la_document(const LaParams& p, int doc, int* t0, int* len) {
+    if (p.cu == nullptr) {
+        *t0 = doc * p.T;
+        *len = p.T;
+    } else {  // clamped to the stream: a bad value cannot lead outside the tensors
+        *t0 = min(max(p.cu[doc], 0), p.T);
+        *len = min(max(p.cu[doc + 1], *t0), p.T) - *t0;
+    }
+}
+
+// The documents' table, by the whole block (blockDim.x >= 160; ends with a __syncthreads).
+__device__ __forceinline__ void la_make_docs(const LaParams& p, LaDocs* d) {
+    const int tid = threadIdx.x;
+    if (tid < p.num_seqs) {
+        int t0, len;
+        la_document(p, tid, &t0, &len);
+        d->t0[tid] = t0;
+        d->len[tid] = len;
+    }
+    if (tid == 0) d->cut = 0;
+    __syncthreads();
+    if (p.walk == LA_WALK_SORTED) {
+        if (tid < p.num_seqs) {
+            int rank = 0;
+            const int len = d->len[tid];
+            for (int n = 0; n < p.num_seqs; ++n) rank += d->len[n] > len || (d->len[n] == len && n < tid);
+            d->units[rank] = tid;
+        }
+    } else if (tid < 32) {
+        int base = 0, longest = 0;
+        for (int n0 = 0; n0 < p.num_seqs; n0 += 32) {
+            const int n = n0 + tid;
+            const int u = n < p.num_seqs ? kLaStart + (d->len[n] + kLaChunk - 1) / kLaChunk : 0;
+            longest = max(longest, __reduce_max_sync(0xffffffffu, u) - kLaStart);
+            int incl = u;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, incl, o);
+                if (tid >= o) incl += y;
+            }
+            if (n < p.num_seqs) d->units[n] = base + incl - u;
+            base += __shfl_sync(0xffffffffu, incl, 31);
+        }
+        if (tid == 0) {
+            d->units[p.num_seqs] = base;
+            d->cut = la_cut_pays(longest, (long long)p.H * (base - kLaStart * p.num_seqs));
+        }
+    }
+    __syncthreads();
+}
+
+__device__ __forceinline__ int la_shares(int all, int ctas) { return min(ctas, max(1, all / kLaShare)); }
+__device__ __forceinline__ int la_share(int all, int i, int shares) { return (int)((long long)all * i / shares); }
+
+// The pieces of share `share` where chains are cut, in order; returns their number (at most the chains').  One
+// thread.  With `open_only` those that the next share goes on from.
+__device__ __forceinline__ int la_cut_pieces(const LaParams& p, const LaDocs* d, int share, bool open_only,
+                                             LaPiece* out) {
+    const int all = p.H * d->units[p.num_seqs], shares = la_shares(all, kLaCtas);
+    if (share >= shares) return 0;
+    int pos = la_share(all, share, shares), doc = 0, count = 0;
+    const int hi = la_share(all, share + 1, shares);
+    while (p.H * d->units[doc + 1] <= pos) ++doc;
+    int h = (pos - p.H * d->units[doc]) / (d->units[doc + 1] - d->units[doc]);
+    while (pos < hi) {
+        const int u = d->units[doc + 1] - d->units[doc], first = p.H * d->units[doc] + h * u + kLaStart;
+        const int nch = u - kLaStart, w0 = max(pos - first, 0), w1 = min(hi - first, nch);
+        // (an empty chain goes to the share that holds the last of its start's units)
+        if ((nch > 0 ? w1 > w0 : pos < first && first <= hi) && !(open_only && w1 == nch))
+            out[count++] = {doc, h, d->t0[doc], nch, d->len[doc] - (nch - 1) * kLaChunk, w0, w1, 0};
+        pos = first + nch;
+        if (++h == p.H) {
+            h = 0;
+            ++doc;
+        }
+    }
+    return count;
+}
+
+// The chain in place `pos` where none is cut.
+__device__ __forceinline__ void la_chain(const LaParams& p, const LaDocs* d, int pos, LaPiece* out) {
+    const int at = pos / p.H;
+    out->doc = p.walk == LA_WALK_SORTED ? d->units[at] : at;
+    out->h = pos - at * p.H;
+    int len;
+    la_document(p, out->doc, &out->t0, &len);
+    out->nch = out->w1 = (len + kLaChunk - 1) / kLaChunk;
+    out->last = len - (out->nch - 1) * kLaChunk;
+    out->w0 = 0;
+}
+
 // The bf16 passes on the tensor cores (linear_attn_tc.cu).
-cudaError_t launch_la_tc(const LaParams& p, int nseg, int d, cudaStream_t st);
+cudaError_t launch_la_tc(const LaParams& p, int d, cudaStream_t st);
+// Between the two passes: every slot's local state becomes the state at the end of its piece.
+cudaError_t launch_la_scan(const LaParams& p, int d, cudaStream_t st);
 
 struct LaPlan {
-    int L;       // segment length
-    int nseg;    // segments (packed: an upper bound)
-    bool split;  // some document may have more than one segment
+    int L;       // fp32: segment length
+    int nseg;    // fp32: segments (packed: an upper bound)
+    bool split;  // some chain may be cut
 };
 
 }  // namespace gdn

@@ -124,6 +124,43 @@ def test_dense_equals_packed(B, T, H, Hk, d, dtype):
             assert sf is None and out["ds0"] is None
 
 
+@pytest.mark.parametrize("what", ["cut", "cut evenly", "sorted", "as they come", "dense rounds"])
+def test_many_chains(what):
+    """More chains (documents times heads) than the GPU's 148 SMs, or a few that are cut into as many pieces."""
+    rng = np.random.default_rng(len(what))
+    H = {"cut": 1, "cut evenly": 4, "sorted": 4, "as they come": 1, "dense rounds": 1}[what]
+    lens = {"cut": list(rng.integers(0, 9, 90)) + [1211, 0, 64, 777],  # pieces that hold many chains, and parts
+            "cut evenly": [64 * 37, 64],
+            "sorted": list(rng.integers(0, 140, 80)),
+            "as they come": list(rng.integers(0, 90, 200)),
+            "dense rounds": [66] * 300}[what]
+    lens = [int(n) for n in lens]
+    x = make(lens, H, 1, 64, "bf16", seed=3, decay="slow")
+    c = cuda(x)
+    b = lambda t: t.view(len(lens), lens[0], *t.shape[1:])
+    if what == "dense rounds":
+        y, sf = api.gdn_linear_attn(b(c["q"]), b(c["k"]), b(c["v"]), c["log_decay"], s0=c["s0"], scale=0.25)
+        out = api.gdn_linear_attn_backward(b(c["q"]), b(c["k"]), b(c["v"]), c["log_decay"], b(c["dy"]), s0=c["s0"],
+                                           ds_final=c["ds_final"], scale=0.25)
+        y, out = y.flatten(0, 1), {n: t.flatten(0, 1) if n != "ds0" else t for n, t in out.items()}
+    else:
+        y, sf = api.gdn_linear_attn_varlen(c["q"], c["k"], c["v"], c["log_decay"], c["cu_seqlens"], s0=c["s0"],
+                                           scale=0.25)
+        out = api.gdn_linear_attn_backward_varlen(c["q"], c["k"], c["v"], c["log_decay"], c["cu_seqlens"], c["dy"],
+                                                  s0=c["s0"], ds_final=c["ds_final"], scale=0.25)
+    torch.cuda.synchronize()
+    assert api.gdn_read_device_status() == 0
+    ya, sa, ga = mags(x, 0.25)
+    yr, sr = oattn.forward(x["q"], x["k"], x["v"], x["log_decay"], x["cu_seqlens"], s0=x["s0"], scale=0.25)
+    gr = oattn.backward(x["q"], x["k"], x["v"], x["log_decay"], x["cu_seqlens"], x["dy"], s0=x["s0"],
+                        ds_final=x["ds_final"], scale=0.25)
+    close(y, yr, ya, "bf16", "y")
+    close(sf, sr, sa, "fp32", "s_final")
+    for n in ("dq", "dk", "dv"):
+        close(out[n], gr[n], ga[n], "bf16", n)
+    close(out["ds0"], gr["ds0"], ga["ds0"], "fp32", "ds0")
+
+
 def test_gradients_against_differences():
     """fp32, the sum of y dy + s_final ds_final: a central difference along a random direction is exact for a
     function that is linear in each tensor, up to the fp32 rounding of the two losses."""
