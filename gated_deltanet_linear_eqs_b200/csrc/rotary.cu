@@ -27,6 +27,7 @@ using sm100::pair;
 using sm100::unpair;
 
 constexpr int kRotWarps = 4;    // of a block
+constexpr int kRotBlocks = 10;  // on an SM at once
 constexpr int kRotFreqs = 2;    // frequencies a lane keeps in registers
 
 template <typename T, int VEC>
@@ -70,7 +71,7 @@ __device__ __forceinline__ uint64_t turns_of(float f) {
 // elements.  A unit is what a lane turns in a head: VEC elements of both halves of the pairs (half
 // layout), VEC / 2 whole pairs (interleaved, VEC > 1), one pair (VEC = 1), or VEC kept elements.
 template <typename T, int VEC, bool INTER>
-__global__ void __launch_bounds__(kRotWarps * 32)
+__global__ void __launch_bounds__(kRotWarps * 32, kRotBlocks)
 rotary_kernel(const RotaryArgs p, int units, int turned, int per_block) {
     constexpr bool PAIRS = INTER && VEC > 1;
     extern __shared__ float4 s_cs[];
@@ -164,7 +165,7 @@ cudaError_t launch(const RotaryArgs& a, bool keep, cudaStream_t st) {
     const int heads = a.a[0].heads + a.a[1].heads;
     // blocks that fit the SMs at once walk over the tokens; few tokens: the heads go over several blocks,
     // each of which computes the angles again
-    const int blocks = (a.T + kRotWarps - 1) / kRotWarps, fit = 148 * 12;
+    const int blocks = (a.T + kRotWarps - 1) / kRotWarps, fit = 148 * kRotBlocks;
     const int hpw = units < 32 ? 32 / units : 1;
     int split = fit / blocks;
     const int most = (heads + hpw - 1) / hpw;
