@@ -13,10 +13,13 @@
 //    operand.  LOC is a fresh fp32 accumulator each chunk: added into the state by the CUDA cores, its
 //    sums do not suffer from the tensor cores' truncating accumulation over a long sequence.
 //  - The decay weights would cost the products' exactness if they were rounded to bf16 with V.  So a weight
-//    is cut into three bf16 pieces w1 + w2 + w3 (8 bits each: exactly the fp32 value), and v w into four:
-//    p1 = bf16(v w1), e1 = v w1 - p1 (exact: the product of two 8-bit significands has 16 bits), p2 = bf16(v w2),
-//    and bf16(v w3 + e2) with e2 = v w2 - p2, which is off by 2^-26 of v w.  Five packed bf16 instructions for
-//    two values; LOC is four products and s_final has fp32 accuracy.  P is rounded to bf16 once (y is bf16).
+//    is cut into three bf16 pieces w1 + w2 + w3, and v w into three: p1 = bf16(v w1); s = bf16(p2 + e1), where
+//    p2 = bf16(v w2) and e1 = v w1 - p1 (exact: the product of two 8-bit significands has 16 bits); and the rest,
+//    the exact rounding errors of p2 and of the sum (which is exact as s - p2 - e1 since w1 is taken so far below
+//    the weight that |p2| > |e1|) plus v w3, rounded: off by 2^-24 of v w in the root mean square and 2^-21 at most,
+//    about as an fp32 product is.  Nine packed bf16 instructions for two values; LOC is three products and
+//    s_final has fp32 accuracy.  (Four pieces take five instructions, but the tensor cores, which the kernel keeps
+//    busy 70% of its cycles, a sixth longer.)  P is rounded to bf16 once (y is bf16).
 //  - A operands in TMEM rather than shared memory: the products are bound by shared-memory bandwidth
 //    (an A of 128 x 16 costs as much of it as a B of 128 columns), which V~ and S^T do not touch.
 // Warps 0-7 prepare a chunk (V~, transposed on the way from shared memory to TMEM by ldmatrix, and P; two
@@ -41,7 +44,7 @@ constexpr int kTcThreads = 640;  // five warpgroups
 // theirs to the back warps, which hold the state.  The shares must not exceed what the block was launched with:
 // 128 (2 x 96 + 2 x 128 + 32) <= 640 x 96.  (88 for the front and 48 for the issuing warps: the gradients of
 // 8 x 4096 tokens with 32 heads of 128 take 744 us rather than 722 us.)
-constexpr int kLaunchRegs = 96, kFrontRegs = 96, kBackRegs = 128, kIoRegs = 32;
+constexpr int kLaunchRegs = 96, kFrontRegs = 80, kBackRegs = 136, kIoRegs = 48;
 static_assert(128 * (2 * kFrontRegs + 2 * kBackRegs + kIoRegs) <= kTcThreads * kLaunchRegs, "register shares");
 
 template <int D, bool STATE>
@@ -83,7 +86,9 @@ __device__ __forceinline__ uint32_t pack_rn(float a, float b) {
     const __nv_bfloat162 x = __floats2bfloat162_rn(a, b);
     return *reinterpret_cast<const uint32_t*>(&x);
 }
-// The weights of V~ in pieces, by pairs of tokens; the factor of Ys in token i.
+// The weights of V~ in pieces, by pairs of tokens; the factor of Ys in token i.  The first piece is the rounding of
+// a value 2.25 / 256 below the weight: 1.25 to 3.25 parts of 256 are left to the second, more than the rounding
+// errors of products with the first (1 part) and than the first's own.
 __device__ __forceinline__ void front_table(uint32_t* sw, int pair_, float g, int n, float scale, bool rev) {
     float w[2];
 #pragma unroll
@@ -93,7 +98,8 @@ __device__ __forceinline__ void front_table(uint32_t* sw, int pair_, float g, in
     }
 #pragma unroll
     for (int t = 0; t < 3; ++t) {
-        const uint32_t x = pack_rn(w[0], w[1]);
+        const float below = t == 0 ? 1.f - 2.25f / 256.f : 1.f;
+        const uint32_t x = pack_rn(w[0] * below, w[1] * below);
         w[0] -= __uint_as_float(x << 16);
         w[1] -= __uint_as_float(x & 0xffff0000u);
         sw[4 * pair_ + t] = x;
@@ -101,6 +107,26 @@ __device__ __forceinline__ void front_table(uint32_t* sw, int pair_, float g, in
 }
 __device__ __forceinline__ float back_factor(float g, int i, int n, float scale, bool rev) {
     return !rev || i < n ? expf(g * (float)(rev ? n - 1 - i : i + 1)) * scale : 0.f;
+}
+
+// A wait of a whole warp for a phase, bounded: one that gives up leaves the barrier's number + 1 in *abort, which
+// ends the others' waits, too.  All lanes poll together and vote: a lane that polled alone would split the warp
+// while it is held, and the warp-collective instructions behind the wait (ldmatrix, whose lanes give each
+// other's addresses) would then fault.
+__device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, volatile int* abort, int id) {
+    constexpr uint32_t ALL = 0xffffffffu;
+    if (__all_sync(ALL, mbar_try_wait(bar, parity))) return true;
+    const long long c0 = clock64();
+    for (;;) {
+#pragma unroll 1
+        for (int i = 0; i < 64; ++i)
+            if (__all_sync(ALL, mbar_try_wait(bar, parity))) return true;
+        if (__any_sync(ALL, *abort != 0)) return false;
+        if (__any_sync(ALL, clock64() - c0 > 4000000000ll)) {  // two seconds
+            *abort = id + 1;
+            return false;
+        }
+    }
 }
 
 // MODE: what a pass writes
@@ -164,19 +190,7 @@ la_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
         return true;
     };
 
-    auto fail = [&](int bar) {
-        (void)GDN_GUARD(false, p.status, DBG_WAIT, (long)bar * 65536 + warp * 256 + D + MODE * 2 + REV);
-        *abort_flag = 1;
-        record_status(p.status, GDN_ERR_TIMEOUT);
-    };
-    // All lanes wait (mbar_wait_warp): a lane that polls alone splits the warp while it is held, and the
-    // warp-collective instructions behind the wait (ldmatrix, whose lanes give each other's addresses) then
-    // fault.
-    auto wwait = [&](int bar, uint32_t parity) {
-        const bool ok = mbar_wait_warp(&bars[bar], parity, abort_flag);
-        if (!ok && lane == 0) fail(bar);
-        return ok;
-    };
+    auto wait = [&](int bar, uint32_t parity) { return wait_all(&bars[bar], parity, abort_flag, bar); };
     // A piece's chunks are counted down: `left` of them, this one included.  The document's last, the only one
     // that can be short, is the last of a piece that ends, or (reversed) the first of one that starts.
     auto odd = [&](const LaPiece& pc) { return pc.nch > 0 && (REV ? pc.starts() : pc.ends()) ? pc.last : C; };
@@ -199,7 +213,7 @@ la_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                 for (int left = pc.w1 - pc.w0; left > 0; --left, ++it, z += REV ? -C : C) {
                     const int s = it % L::STAGES;
                     if (it >= L::STAGES && !mbar_wait(&bars[B_EMPTY + s], ((it / L::STAGES) - 1) & 1, abort_flag)) {
-                        fail(B_EMPTY + s);
+                        if (!*abort_flag) *abort_flag = B_EMPTY + s + 1;
                         ok = false;
                         break;
                     }
@@ -237,7 +251,6 @@ la_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
         constexpr uint32_t VLBO = D == 128 ? 8192 : 0;
         const uint32_t s0 = smem_u32(sm);
         bool ok = true;
-        auto wait = [&](int bar, uint32_t parity) { return mbar_wait_warp(&bars[bar], parity, abort_flag); };
         // products over the K steps of 16: A and B advance by constants
         auto steps = [&](auto f) {
             f(std::integral_constant<int, 0>());
@@ -276,7 +289,6 @@ la_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                         steps([&](auto kk) { mma_ts<ID_LOC, kk != 0>(d, v + 8 * kk, k + 128 * kk); });
                         steps([&](auto kk) { mma_ts<ID_LOC, true>(d, v + 32 + 8 * kk, k + 128 * kk); });
                         steps([&](auto kk) { mma_ts<ID_LOC, true>(d, v + 64 + 8 * kk, k + 128 * kk); });
-                        steps([&](auto kk) { mma_ts<ID_LOC, true>(d, v + 96 + 8 * kk, k + 128 * kk); });
                         mma_commit(&bars[B_LOC + b]);
                         mma_commit(&bars[B_EMPTY + s]);
                     }
@@ -335,7 +347,6 @@ la_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                     __syncwarp();
                 }
         }
-        if (!ok && lane == 0 && !*abort_flag) fail(B_FIN);
         // no product may still be running when the CTA ends
         if (leader) {
             mma_commit(&bars[B_FIN + warp - 17]);
@@ -391,7 +402,7 @@ la_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
             for (int left = pc.w1 - pc.w0; left > 0; --left, ++it) {
                 const int n = tokens(pc, left, odd_n);
                 const int buf = it % L::NB, use = it / L::NB;
-                wwait(B_FULL + s, full_ph);
+                wait(B_FULL + s, full_ph);
                 if (n < C) {
                     // rows past the document's end hold other documents' tokens (or nothing): K and V are zeroed
                     weights(true);
@@ -405,9 +416,9 @@ la_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                     named_sync(1, 256);
                     if (lane == 0) mbar_arrive(&bars[C_FIX]);
                 }
-                // ---- V~: rows v = 32 quad .. +31 (D = 64: twice), tokens 32 half .. +31, in four pieces
+                // ---- V~: rows v = 32 quad .. +31 (D = 64: twice), tokens 32 half .. +31, in three pieces
                 {
-                    uint32_t w[4][16];
+                    uint32_t w[3][16];
                     __syncwarp();
 #pragma unroll
                     for (int r = 0; r < 2; ++r)  // 16 rows each
@@ -419,15 +430,17 @@ la_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                             for (int e = 0; e < 4; ++e) {
                                 const int u = 2 * x + (e >> 1), at = 8 * r + 4 * x + e;
                                 const uint32_t p1 = mul_bf16x2(v[e], w1[u]), p2 = mul_bf16x2(v[e], w2[u]);
+                                const uint32_t e1 = fma_bf16x2(v[e], w1[u], p1 ^ 0x80008000u);
+                                const uint32_t e2 = fma_bf16x2(v[e], w2[u], p2 ^ 0x80008000u);
+                                const uint32_t sum = add_bf16x2(p2, e1), es = sub_bf16x2(e1, sub_bf16x2(sum, p2));
                                 w[0][at] = p1;
-                                w[1][at] = fma_bf16x2(v[e], w1[u], p1 ^ 0x80008000u);
-                                w[2][at] = p2;
-                                w[3][at] = fma_bf16x2(v[e], w3[u], fma_bf16x2(v[e], w2[u], p2 ^ 0x80008000u));
+                                w[1][at] = sum;
+                                w[2][at] = fma_bf16x2(v[e], w3[u], add_bf16x2(es, e2));
                             }
                         }
-                    if (use > 0) wwait(B_LOC + buf, (use - 1) & 1);  // the last V~ is read
+                    if (use > 0) wait(B_LOC + buf, (use - 1) & 1);  // the last V~ is read
                     tc_fence_after();
-                    tmem_st_frag_x4(tl + L::T_V + 128 * buf + 16 * half, w);
+                    tmem_st_frag_x3(tl + L::T_V + 128 * buf + 16 * half, w);
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&bars[C_V + buf]);
@@ -435,7 +448,7 @@ la_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                 // ---- P: rows j = 16 quad .. +15, columns i = 32 half .. +31.  Its buffer is the stage's own: with
                 // the stage loaded again, the Yi that read the buffer is done.
                 if (!STATE) {
-                    wwait(B_SC, it & 1);
+                    wait(B_SC, it & 1);
                     tc_fence_after();
                     float x[16];
                     tmem_ld_frag<4>(tl + L::T_SC + 32 * half, x);
@@ -528,7 +541,7 @@ la_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                 const float* fi = reinterpret_cast<const float*>(sm + L::FI) + tail * 64;
                 const float2 dec = reinterpret_cast<const float2*>(sm + L::DEC)[tail];
                 // ---- state behind the chunk
-                ok = wwait(B_LOC + buf, use & 1) && ok;
+                ok = wait(B_LOC + buf, use & 1) && ok;
                 tc_fence_after();
                 {
                     // e^{g n} in one float would be off the same way every time; the rest of it is made up for
@@ -553,7 +566,7 @@ la_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
                 if (lane == 0) mbar_arrive(&bars[C_L + buf]);
                 // ---- outputs: columns v = 32 quad .. +31, tokens 32 half .. +31
                 if (!STATE) {
-                    ok = wwait(B_Y, it & 1) && ok;  // Ys has read the state, too
+                    ok = wait(B_Y, it & 1) && ok;  // Ys has read the state, too
                     tc_fence_after();
                     if (left > 1) store_state();
                     if (lane == 0) bulk_wait_read();  // the last chunk's outputs have left the staging tile
@@ -644,6 +657,10 @@ la_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ C
     __syncthreads();
     tc_fence_after();
     if (warp == 17) tmem_dealloc(tmem, 512);
+    if (tid == 0 && *abort_flag) {
+        (void)GDN_GUARD(false, p.status, DBG_WAIT, (long)(*abort_flag - 1) * 65536 + D + MODE * 2 + REV);
+        record_status(p.status, GDN_ERR_TIMEOUT);
+    }
 }
 
 // ============================================================================ between the passes

@@ -485,11 +485,11 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* w) {
 
 // 16x128b shape over 32 lanes (two times 16), 16 columns: thread t of the warp gives, for r = 0, 1 and column
 // group g of 4, w[8 r + 2 g] = (lane 16 r + t / 4, column 4 g + t % 4) and w[8 r + 2 g + 1] = (lane
-// 16 r + t / 4 + 8, the same column).  Four of them, 32 columns apart, with one wait; completed before
+// 16 r + t / 4 + 8, the same column).  Three of them, 32 columns apart, with one wait; completed before
 // returning.
-__device__ __forceinline__ void tmem_st_frag_x4(uint32_t taddr, const uint32_t (*w4)[16]) {
+__device__ __forceinline__ void tmem_st_frag_x3(uint32_t taddr, const uint32_t (*w3)[16]) {
     __syncwarp();
-    const uint32_t *w = w4[0], *x = w4[1], *y = w4[2], *z = w4[3];
+    const uint32_t *w = w3[0], *x = w3[1], *y = w3[2];
 #define GDN_X8(v, i) "r"(v[i]), "r"(v[i + 1]), "r"(v[i + 2]), "r"(v[i + 3]), "r"(v[i + 4]), "r"(v[i + 5]), \
                      "r"(v[i + 6]), "r"(v[i + 7])
     asm volatile(
@@ -504,13 +504,8 @@ __device__ __forceinline__ void tmem_st_frag_x4(uint32_t taddr, const uint32_t (
         "tcgen05.st.sync.aligned.16x128b.x4.b32 [a], {%34,%35,%36,%37,%38,%39,%40,%41};\n\t"
         "add.u32 a, %1, 64;\n\t"
         "tcgen05.st.sync.aligned.16x128b.x4.b32 [a], {%42,%43,%44,%45,%46,%47,%48,%49};\n\t"
-        "add.u32 a, %0, 96;\n\t"
-        "tcgen05.st.sync.aligned.16x128b.x4.b32 [a], {%50,%51,%52,%53,%54,%55,%56,%57};\n\t"
-        "add.u32 a, %1, 96;\n\t"
-        "tcgen05.st.sync.aligned.16x128b.x4.b32 [a], {%58,%59,%60,%61,%62,%63,%64,%65};\n\t"
         "tcgen05.wait::st.sync.aligned;\n\t}\n" ::"r"(taddr),
-        "r"(taddr + (16u << 16)), GDN_X8(w, 0), GDN_X8(w, 8), GDN_X8(x, 0), GDN_X8(x, 8), GDN_X8(y, 0), GDN_X8(y, 8),
-        GDN_X8(z, 0), GDN_X8(z, 8)
+        "r"(taddr + (16u << 16)), GDN_X8(w, 0), GDN_X8(w, 8), GDN_X8(x, 0), GDN_X8(x, 8), GDN_X8(y, 0), GDN_X8(y, 8)
         : "memory");
 #undef GDN_X8
 }
@@ -627,10 +622,27 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
     return r;
 }
 
-// Two bf16 values a register: products and fused multiply-adds, each rounded once to bf16.
+// Two bf16 values a register: products, sums and fused multiply-adds, each rounded once to bf16.
 __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
     uint32_t r;
     asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t add_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t sub_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+// a b - c
+__device__ __forceinline__ uint32_t fms_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t r;
+    asm("{\n\t.reg .b32 n;\n\tneg.bf16x2 n, %3;\n\tfma.rn.bf16x2 %0, %1, %2, n;\n\t}\n"
+        : "=r"(r) : "r"(a), "r"(b), "r"(c));
     return r;
 }
 __device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
