@@ -29,8 +29,8 @@ namespace gdn {
 constexpr int kLaChunk = 64;
 
 // How the bf16 kernel's CTAs share the chains: in turn; cut into equal shares; or, packed documents of unlike
-// lengths, longest first, in turn, back and forth (24 documents of 0 to 1200 tokens with 16 heads of 64: 43 us,
-// in plain turn 60 us, left to the hardware a block each 44 us).
+// lengths, longest first, in turn, back and forth (24 documents of 0 to 1200 tokens with 16 heads of 64: 43 us where
+// plain turns took 60 us).
 enum { LA_WALK_TURN = 0, LA_WALK_CUT = 1, LA_WALK_SORTED = 2 };
 
 struct LaParams {
@@ -127,11 +127,6 @@ __device__ __forceinline__ float2 la_power2(float g, int n) {
     return make_float2(hi, (float)(e - (double)hi));
 }
 
-template <int D>
-__device__ __forceinline__ size_t la_state_index(int kk, int vv, int state_t) {
-    return state_t ? (size_t)vv * D + kk : (size_t)kk * D + vv;
-}
-
 // ---- bf16: the shares of the CTAs -------------------------------------------------------------
 // A chain of c chunks counts kLaStart + c units, kLaStart for what its start and end cost; all chains' units are
 // laid end to end (document by document, its heads in turn) and cut into equal shares of at least kLaShare
@@ -141,9 +136,10 @@ constexpr int kLaCtas = 148;   // one a SM
 constexpr int kLaDocs = 147;   // documents that are cut (which needs fewer chains than SMs) or sorted at most
 
 // A cut pays where the longest chain takes longer than the two passes over the shares: uncut, a chain takes
-// 7 + 1.5 us a chunk; cut, 31 + 2.8 us a chunk of a share (three launches, the first pass 1.1, the second 1.9;
-// d = 128).  Measured uncut and cut: one document of 2048 tokens 52 and 41 us with 16 heads, 54 and 66 us with 64,
-// 59 and 103 us with 120; of 1024 tokens with 16 heads 29 and 40 us.  d = 64 and the gradients lie close by.
+// 6 + 1.4 us a chunk; cut, 31 + 2.4 us a chunk of a share (three launches; the two passes 0.9 and 1.5).  Measured
+// uncut and cut, d = 128: one document of 2048 tokens 50 and 38 us with 16 heads, 54 and 62 us with 64, 58 and 97 us
+// with 120; of 8192 tokens with 64 heads 187 and 160 us; of 1024 tokens with 16 heads 28 and 37 us.  d = 64: 2048
+// tokens 47 and 34 us with 32 heads, 1024 tokens 26 and 33 us.  The gradients lie close by.
 __host__ __device__ inline bool la_cut_pays(long long longest, long long all) {
     return longest > 16 + 2 * all / kLaCtas;
 }
@@ -154,12 +150,11 @@ struct LaDocs {
     int units[kLaDocs + 1];   // cut: units of one head before each document; sorted: the documents by length
     int t0[kLaDocs], len[kLaDocs];
 };
-struct LaPiece {
+struct alignas(16) LaPiece {  // (whole words of 16 bytes: read from shared memory at once)
     int doc, h;
     int t0;            // the document's first token
     int nch, last;     // its chunks, and the tokens of the last
     int w0, w1;        // the chunks of this piece, counted in walking order
-    int unused;
     __device__ bool starts() const { return w0 == 0; }
     __device__ bool ends() const { return w1 == nch; }
 };
@@ -233,7 +228,7 @@ __device__ __forceinline__ int la_cut_pieces(const LaParams& p, const LaDocs* d,
         const int nch = u - kLaStart, w0 = max(pos - first, 0), w1 = min(hi - first, nch);
         // (an empty chain goes to the share that holds the last of its start's units)
         if ((nch > 0 ? w1 > w0 : pos < first && first <= hi) && !(open_only && w1 == nch))
-            out[count++] = {doc, h, d->t0[doc], nch, d->len[doc] - (nch - 1) * kLaChunk, w0, w1, 0};
+            out[count++] = {doc, h, d->t0[doc], nch, d->len[doc] - (nch - 1) * kLaChunk, w0, w1};
         pos = first + nch;
         if (++h == p.H) {
             h = 0;
