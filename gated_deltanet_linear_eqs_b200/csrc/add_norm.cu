@@ -12,7 +12,7 @@
 // share an SM, and their loads hide each other's row sums.  Products and sums are packed, two 32-bit values an
 // instruction: with single ones the SMs issue for half the time and more, and the passes take a fifth longer.
 // Measured, 16 bits: 32768 rows of 2048 with a residual 83 us (6.5 TB/s); 8191 rows of 5120 to 8 bits 50 us
-// (5.9 TB/s); 16384 rows of 4096 in the reverse mode 100 us (5.4 TB/s), 4 us of it the sum of the dw partials.
+// (5.9 TB/s); 16384 rows of 4096 in the reverse mode 97 us (5.5 TB/s).
 #include <cuda_fp8.h>
 #include <float.h>
 
@@ -303,23 +303,20 @@ add_norm_bwd_kernel(const T* __restrict__ h, const float* __restrict__ w, const 
     }
 }
 
-// dw[c] = sum of the partials, in the same order on every run: 8 warps share the blocks of 32 columns.
-__global__ void __launch_bounds__(256)
+// dw[c] = sum of the partials, in the same order on every run: 32 warps share the blocks of 32 columns.
+__global__ void __launch_bounds__(1024)
 add_norm_dw_kernel(const float* __restrict__ part, float* __restrict__ dw, int blocks, int C) {
-    __shared__ float s[8][33];
+    __shared__ float s[32][33];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
     float t = 0.f;
     if (c < C) {
-        const float* at = part + c;
-#pragma unroll 16
-        for (int b = warp; b < blocks; b += 8) t += __ldcs(at + (size_t)b * C);
+#pragma unroll 8
+        for (int b = warp; b < blocks; b += 32) t += __ldcs(part + (size_t)b * C + c);
     }
     s[warp][lane] = t;
     __syncthreads();
-    if (warp == 0 && c < C) {
-        for (int k = 1; k < 8; ++k) t += s[k][lane];
-        dw[c] = t;
-    }
+    t = warp_sum(s[lane][warp]);  // column `warp` of the 32
+    if (lane == 0 && blockIdx.x * 32 + warp < C) dw[blockIdx.x * 32 + warp] = t;
 }
 
 // threads of a block for C columns with NV vectors a thread
@@ -366,7 +363,7 @@ cudaError_t launch_bwd(const AddNormArgs& a, cudaStream_t st) {
         static_cast<T*>(a.dx), part, a.rows, a.C, a.eps);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    add_norm_dw_kernel<<<(unsigned)((a.C + 31) / 32), 256, 0, st>>>(part, a.dw, (int)grid, a.C);
+    add_norm_dw_kernel<<<(unsigned)((a.C + 31) / 32), 1024, 0, st>>>(part, a.dw, (int)grid, a.C);
     return cudaGetLastError();
 }
 template <typename T>
