@@ -495,7 +495,7 @@ static int check_attn(const float* log_decay, int H, int Hk, int dk, int dv, int
     if (!ok_ptr(log_decay) || H < 1 || Hk < 1 || H % Hk != 0) return GDN_ERR_INVALID_ARG;
     return check_dims(dk, dv, dtype);
 }
-// dense sequences: their tokens and the grid's (segment, head) count stay within 31 bits
+// the tokens and the grid's (segment, head) count, with the rounds behind it, stay within 31 bits
 static bool ok_tokens(int num_seqs, int T, int H, bool packed) {
     const long long tokens = packed ? T : (long long)num_seqs * T;
     const long long segments = tokens / 64 + num_seqs;
@@ -522,6 +522,7 @@ static int attn_forward(const void* q, const void* k, const void* v, const float
     if (!ok_ptr(q) || !ok_ptr(k) || !ok_ptr(v) || !ok_ptr(y) || !ok_opt_ptr(s0) || !ok_opt_ptr(s_final))
         return GDN_ERR_INVALID_ARG;
     if (num_seqs < 1 || T < 1 || (packed && cu_seqlens == nullptr)) return GDN_ERR_INVALID_ARG;
+    if (s0 != nullptr && s0 == s_final) return GDN_ERR_INVALID_ARG;  // its end may be written before its start is read
     if (int rc = check_attn(log_decay, H, Hk, dk, dv, dtype)) return rc;
     if (!ok_tokens(num_seqs, T, H, packed)) return GDN_ERR_INVALID_ARG;
     const size_t need = gdn::la_layout(false, num_seqs, T, H, Hk, dk, packed).total;
@@ -543,6 +544,7 @@ static int attn_backward(const void* q, const void* k, const void* v, const floa
         !ok_opt_ptr(s0) || !ok_opt_ptr(ds_final) || !ok_opt_ptr(ds0))
         return GDN_ERR_INVALID_ARG;
     if (num_seqs < 1 || T < 1 || (packed && cu_seqlens == nullptr)) return GDN_ERR_INVALID_ARG;
+    if (ds0 != nullptr && (ds0 == ds_final || ds0 == s0)) return GDN_ERR_INVALID_ARG;
     if (int rc = check_attn(log_decay, H, Hk, dk, dv, dtype)) return rc;
     if (!ok_tokens(num_seqs, T, H, packed)) return GDN_ERR_INVALID_ARG;
     const size_t need = gdn::la_layout(true, num_seqs, T, H, Hk, dk, packed).total;

@@ -402,8 +402,9 @@ int gdn_qsa_indexer(const void* q, const void* k, const float* g, const int32_t*
  *
  * gdn_linear_attn -- B dense sequences of T tokens.  gdn_linear_attn_varlen -- one packed stream
  * ([T, H, dk] tensors) of num_seqs documents; cu_seqlens as in gdn_prefill_varlen (empty documents
- * give s_final = s0).  Computed in 64-token chunks; long sequences are cut into segments that run
- * side by side, each from a start state that a first pass prepares in the workspace.
+ * give s_final = s0).  Computed in 64-token chunks; where sequences and heads are few, long ones are
+ * cut into pieces that run side by side, each from a start state that a first pass prepares in the
+ * workspace.
  * For bf16 the scores and the chunk-start states are rounded to bf16 as operands of the tensor cores;
  * sums and states are fp32 (s_final and ds0 are exact to fp32 rounding), fp32 inputs are computed in
  * fp32 throughout.
@@ -411,7 +412,9 @@ int gdn_qsa_indexer(const void* q, const void* k, const float* g, const int32_t*
  * [N, Hk, dk]; state [N, H, dk, dv] fp32 is read once and updated in place.
  * gdn_linear_attn_backward, _varlen -- gradients of L(y, s_final) given dy and ds_final: dq like q,
  * dk_out and dv_out like k and v (summed over the heads that share them, in fp32 and in a fixed
- * order), ds0 fp32.  dy must not alias an output.
+ * order), ds0 fp32.
+ * No output may overlap an input or another output (s_final == s0, ds0 == ds_final and ds0 == s0 give
+ * GDN_ERR_INVALID_ARG); only the single-token call updates its state in place.
  * gdn_linear_attn_workspace_bytes -- device scratch of the four prompt calls (backward != 0 for the
  * gradients); num_seqs = 0: B dense sequences of T tokens; num_seqs >= 1: packed (B = 1).
  * Two calls that may overlap on the GPU need a workspace each.

@@ -71,6 +71,15 @@ def test_linear_attn_more_refusals(lib):
     assert step(dk=32, dv=32) == SHAPE and step(N=1 << 30) == BAD
 
 
+def test_linear_attn_states_in_place_are_refused(lib):
+    """A long sequence is cut: the CTA that writes its last state may run ahead of the one that reads its first."""
+    for call in (dense, varlen):
+        assert call(lib, s0=A, sf=A) == BAD
+    for call in (back, back_varlen):
+        assert call(lib, dsf=A, ds0=A) == BAD
+        assert call(lib, s0=A, ds0=A) == BAD
+
+
 def test_linear_attn_workspace(lib):
     n = ctypes.c_size_t(0)
     f = lambda *a: lib.gdn_linear_attn_workspace_bytes(*a, ctypes.byref(n))

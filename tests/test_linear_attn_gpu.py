@@ -250,6 +250,71 @@ def test_other_documents_and_heads_are_untouched(dtype):
     assert torch.equal(b1["ds0"][[0, 2]], b0["ds0"][[0, 2]])
 
 
+@pytest.mark.parametrize("lens,bad", [([1500, 90, 0, 65], (1400, 1405)), ([1500, 90, 0, 65], (1590, 1591)),
+                                      ([1500, 90, 0, 65], (64, 65)), ([40, 3] * 40, (43 * 20, 43 * 20 + 40))])
+def test_shared_walks_keep_chains_apart(lens, bad):
+    """CTAs that walk several chains, or parts of them, one after the other (a cut, and 320 chains on 148 SMs): tokens
+    that are not finite reach only their own document and head, forward from (backward: up to) their chunk; rows
+    behind the last document and states of others stay."""
+    H, d, N, T = 4, 64, len(lens), sum(lens)
+    x = make(lens, H, 2, d, "bf16", seed=5, decay="slow")
+    c = cuda(x)
+    cu = [0] + list(np.cumsum(lens))
+    n = next(i for i in range(N) if cu[i] <= bad[0] < cu[i + 1])
+    first = cu[n] + (bad[0] - cu[n]) // 64 * 64
+    z = {k: t.clone() for k, t in c.items()}
+    for k in ("q", "dy"):
+        z[k][bad[0]:bad[1], 2] = float("nan")
+    pad = {k: torch.cat([t, torch.full_like(t[:70], float("nan"))]) if k in ("q", "k", "v", "dy") else t
+           for k, t in z.items()}  # the stream is longer than its documents
+    run = lambda a, y: api.gdn_linear_attn_varlen(a["q"], a["k"], a["v"], a["log_decay"], a["cu_seqlens"],
+                                                  s0=a["s0"], y=y)
+    back = lambda dy: api.gdn_linear_attn_backward_varlen(c["q"], c["k"], c["v"], c["log_decay"], c["cu_seqlens"], dy,
+                                                          s0=c["s0"])
+    buf = torch.full((T + 70, H, d), 7.0, dtype=torch.bfloat16, device="cuda")
+    y0, s0 = run({k: torch.cat([t, torch.zeros_like(t[:70])]) if k in ("q", "k", "v", "dy") else t
+                  for k, t in c.items()}, None)
+    y1, s1 = run(pad, buf)
+    b0, b1 = back(c["dy"]), back(z["dy"])
+    torch.cuda.synchronize()
+    assert api.gdn_read_device_status() == 0
+    keep = torch.ones(T, H, dtype=torch.bool, device="cuda")
+    keep[bad[0]:bad[1], 2] = False
+    assert torch.equal(y1[:T][keep], y0[:T][keep]) and bool((buf[T:] == 7.0).all())  # q reaches its own row alone
+    assert torch.equal(s1, s0)
+    keep[bad[0]:bad[1]] = True
+    keep[first:cu[n + 1], 2] = False  # dq: rows of the chunk on; dk, dv (heads 2, 3 share theirs): up to its end
+    assert torch.equal(b1["dq"][keep], b0["dq"][keep])
+    for k in ("dk", "dv"):
+        keep = torch.ones(T, 2, dtype=torch.bool, device="cuda")
+        keep[cu[n]:first + 64, 1] = False
+        assert torch.equal(b1[k][keep], b0[k][keep])
+    keep = torch.ones(N, H, dtype=torch.bool, device="cuda")
+    keep[n, 2] = False
+    assert torch.equal(b1["ds0"][keep], b0["ds0"][keep])
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_one_long_chain(d):
+    """One head's 20011 tokens over all SMs, with its gradients."""
+    x = make([20011], 1, 1, d, "bf16", seed=d, decay="slow")
+    c = cuda(x)
+    y, sf = api.gdn_linear_attn_varlen(c["q"], c["k"], c["v"], c["log_decay"], c["cu_seqlens"], s0=c["s0"], scale=0.1)
+    out = api.gdn_linear_attn_backward_varlen(c["q"], c["k"], c["v"], c["log_decay"], c["cu_seqlens"], c["dy"],
+                                              s0=c["s0"], ds_final=c["ds_final"], scale=0.1)
+    torch.cuda.synchronize()
+    assert api.gdn_read_device_status() == 0
+    ya, sa, ga = mags(x, 0.1)
+    yr, sr = oattn.forward(x["q"], x["k"], x["v"], x["log_decay"], x["cu_seqlens"], s0=x["s0"], scale=0.1)
+    gr = oattn.backward(x["q"], x["k"], x["v"], x["log_decay"], x["cu_seqlens"], x["dy"], s0=x["s0"],
+                        ds_final=x["ds_final"], scale=0.1)
+    close(y, yr, ya, "bf16", "y")
+    close(sf, sr, sa, "fp32", "s_final")
+    for n in ("dq", "dk", "dv"):
+        close(out[n], gr[n], ga[n], "bf16", n)
+    close(out["ds0"], gr["ds0"], ga["ds0"], "fp32", "ds0")
+
+
 def test_same_result_every_time_and_captured():
     """Runs are bit-equal; a captured graph replays them on new inputs; two streams with a workspace each."""
     x = make([900, 70, 1], 2, 1, 128, "bf16", seed=1, decay="slow")
