@@ -85,8 +85,12 @@ rotary_kernel(const RotaryArgs p, int units, int turned, int per_block) {
     const int hpw = units < 32 ? 32 / units : 1;  // heads the lanes cover at once
     const int hh = units < 32 ? lane / units : 0, u0 = units < 32 ? lane - hh * units : lane;
     const int first = blockIdx.y * per_block, last = min(first + per_block, p.a[0].heads + p.a[1].heads);
-    for (int t = blockIdx.x * kRotWarps + warp; t < p.T; t += gridDim.x * kRotWarps) {
-        const long long pos = p.positions[t];
+    const int step = gridDim.x * kRotWarps;
+    int t = blockIdx.x * kRotWarps + warp;
+    int next = t < p.T ? p.positions[t] : 0;
+    for (; t < p.T; t += step) {
+        const long long pos = next;
+        if (t < p.T - step) next = p.positions[t + step];  // asked for a token ahead
         __syncwarp();  // the last token's factors are read
         for (int i = lane, k = 0; i < half; i += 32, ++k) {
             const uint64_t fr = k < kRotFreqs ? (k == 0 ? f[0] : f[kRotFreqs - 1]) : turns_of(p.inv_freq[i]);
