@@ -34,7 +34,7 @@ struct LaTf {
 };
 
 __device__ __forceinline__ void tf_split(float x, uint32_t& hi, uint32_t& lo) {
-    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(hi) : "f"(x));
+    hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;  // to nearest, ties away (a NaN stays one in lo)
     lo = __float_as_uint(x - __uint_as_float(hi));
 }
 __device__ __forceinline__ void tf_mma(float* c, const uint32_t* a, const uint32_t* b) {

@@ -173,8 +173,8 @@ cudaError_t launch(const RotaryArgs& a, bool keep, cudaStream_t st) {
     split = split < 1 ? 1 : split > most ? most : split;
     const int per = (heads + split - 1) / split;
     const size_t smem = (size_t)kRotWarps * 2 * ((a.r / 2 + 3) & ~3) * sizeof(float);
-    rotary_kernel<T, VEC, INTER><<<dim3((unsigned)(blocks < 3 * fit ? blocks : 3 * fit), (unsigned)((heads + per - 1) / per)),
-                                   kRotWarps * 32, smem, st>>>(a, units, turned, per);
+    const dim3 grid((unsigned)(blocks < 3 * fit ? blocks : 3 * fit), (unsigned)((heads + per - 1) / per));
+    rotary_kernel<T, VEC, INTER><<<grid, kRotWarps * 32, smem, st>>>(a, units, turned, per);
     return cudaGetLastError();
 }
 
