@@ -260,7 +260,7 @@ cudaError_t launch_tf(const LaParams& p, int nseg, cudaStream_t st) {
 
 cudaError_t launch_f32(const LaParams& p, int nseg, int d, cudaStream_t st) {
     // 32 columns a CTA where all those CTAs run at once (the scores are then computed more often): 64 tokens of
-    // 74 heads of 64 take 9.6 us so and 12.1 us with 64 columns, of 100 heads 17.4 and 12.2 us
+    // 74 heads of 64 take 8.9 us so and 11.1 us with 64 columns, of 100 heads 15.8 and 11.2 us
     const bool wide = (long long)nseg * p.H * (d / 32) > 148;
     if (d == 128) return wide ? launch_tf<128, 64>(p, nseg, st) : launch_tf<128, 32>(p, nseg, st);
     return wide ? launch_tf<64, 64>(p, nseg, st) : launch_tf<64, 32>(p, nseg, st);
@@ -376,23 +376,26 @@ cudaError_t launch_step(const LaStepArgs& a, cudaStream_t st) {
 }
 
 // ============================================================================ plan
-// Chains are cut where there are fewer of them than SMs.  bf16: equal shares of the CTAs, where la_cut_pays (of packed
-// documents only the sum of the lengths is known here: the kernels decide once more).  fp32: segments of at least
-// one chunk, whose products take several times as long: cut or not, a document of 128 tokens takes 20 or 24 us
-// with 2 heads of 128, 46 or 47 us with 64; of 1024 tokens 28 or 166 us and 293 or 333 us.
-
-LaPlan make_plan(int num_seqs, int T, int H, bool packed, int dtype) {
-    const long long tokens = packed ? T : (long long)num_seqs * T;
+// Chains are cut where there are fewer of them than SMs and a cut pays.  bf16: equal shares of the CTAs, la_cut_pays
+// (of packed documents only the sum of the lengths is known here: the kernels decide once more).  fp32: segments
+// of at least one chunk, where a CTA for each 32 columns of each chain would leave SMs idle, the more so the
+// longer the chains (of packed documents twice the mean is taken).  Measured in fp32, d = 128, cut and uncut: 128
+// tokens with 2 heads 18 and 21 us, with 24 heads 27 and 22 us; 512 tokens with 24 heads 72 and 76 us, with 32 heads
+// 84 and 75 us; 2048 tokens with 40 heads 333 and 399 us, with 64 heads 517 and 397 us; d = 64: 512 tokens with 48
+// heads 37 and 47 us, with 100 heads 72 and 62 us.
+LaPlan make_plan(int num_seqs, int T, int H, int d, bool packed, int dtype) {
+    const long long tokens = packed ? T : (long long)num_seqs * T, chains = (long long)num_seqs * H;
+    const long long chunks = (T + kLaChunk - 1) / kLaChunk;
     LaPlan pl;
-    pl.L = (T + kLaChunk - 1) / kLaChunk * kLaChunk;
-    pl.split = (long long)num_seqs * H < kLaCtas && T > kLaChunk;
+    pl.L = (int)chunks * kLaChunk;
+    pl.split = chains < kLaCtas && T > kLaChunk;
     if (dtype == GDN_BF16) {
-        const long long longest = (T + kLaChunk - 1) / kLaChunk;
-        pl.split = pl.split && la_cut_pays(longest, (packed ? 1 : num_seqs) * longest * H);
+        pl.split = pl.split && la_cut_pays(chunks, (packed ? 1 : num_seqs) * chunks * H);
     } else if (pl.split) {
-        const long long want = (tokens * H + 147) / 148;
+        const long long mean = 2 * ((chunks + num_seqs - 1) / num_seqs), n = packed && mean < chunks ? mean : chunks;
+        const long long want = (tokens * H + kLaCtas - 1) / kLaCtas;
         const long long L = (want + kLaChunk - 1) / kLaChunk * kLaChunk;
-        if (L < pl.L) pl.L = (int)L;
+        if (L < pl.L && chains * (d / 32) * (n + 6) <= 200 * n) pl.L = (int)L;
         pl.split = pl.L < T;
     }
     pl.nseg = packed ? T / pl.L + num_seqs : num_seqs * ((T + pl.L - 1) / pl.L);
@@ -413,7 +416,7 @@ LaLayout la_layout(bool backward, int num_seqs, int T, int H, int Hk, int d, boo
     l.off_local = 0;
     l.off_dk = 0;
     for (int dtype : {GDN_BF16, GDN_FP32}) {  // the size serves both types
-        const size_t n = up256(local_bytes(make_plan(num_seqs, T, H, packed, dtype), H, d, dtype));
+        const size_t n = up256(local_bytes(make_plan(num_seqs, T, H, d, packed, dtype), H, d, dtype));
         l.off_dk = n > l.off_dk ? n : l.off_dk;
     }
     l.off_dv = l.off_dk;
@@ -427,7 +430,7 @@ LaLayout la_layout(bool backward, int num_seqs, int T, int H, int Hk, int d, boo
 
 cudaError_t launch_linear_attn(const LaArgs& a, cudaStream_t st) {
     const bool packed = a.cu_seqlens != nullptr;
-    const LaPlan pl = make_plan(a.num_seqs, a.T, a.H, packed, a.dtype);
+    const LaPlan pl = make_plan(a.num_seqs, a.T, a.H, a.d, packed, a.dtype);
     const LaLayout lay = la_layout(a.dy != nullptr, a.num_seqs, a.T, a.H, a.Hk, a.d, packed);
     char* ws = static_cast<char*>(a.ws);
     const int group = a.H / a.Hk;
