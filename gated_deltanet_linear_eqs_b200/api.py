@@ -584,22 +584,15 @@ def gdn_qsa_indexer(q, k, g, cu_seqlens, max_doc_len, budget=512, stream=None):
 # The calls below serve decode steps of a few microseconds on the GPU, so their checks are kept short: one
 # comparison a tensor, the reasons looked for only when it fails (_refuse), the stream taken as a raw handle.
 
-def _on_device(fn):
-    """Runs the call with its first tensor's device current: a launch goes to the current device, whatever
-    device its pointers are on."""
-    @functools.wraps(fn)
-    def call(first, *args, **kw):
-        dev = first.get_device()
-        if dev < 0 or dev == _current_device():
-            return fn(first, *args, **kw)
-        with torch.cuda.device(dev):
-            return fn(first, *args, **kw)
-    return call
-
-
 _current_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else \
     lambda dev: torch.cuda.current_stream(dev).cuda_stream
 _current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
+
+
+def _launch(dev, f, a):
+    """f(*a) with device dev current: a launch goes to the current device, whatever device its pointers are on."""
+    with torch.cuda.device(dev):
+        return f(*a)
 
 
 def _raw_stream(stream, dev):
@@ -617,7 +610,7 @@ def _refuse(t, name, dtype, shape, dev):
 
 def _want(t, name, dtype, shape, dev):
     """A contiguous tensor of the given type and shape on device dev."""
-    if t is None or t.dtype != dtype or t.shape != shape or t.get_device() != dev or \
+    if t is None or t.dtype is not dtype or t.shape != shape or t.get_device() != dev or \
             not t.is_contiguous() or dev < 0:
         _refuse(t, name, dtype, shape, dev)
 
@@ -680,7 +673,6 @@ def _states(t, name, shape, dev, make=False):
     return t
 
 
-@_on_device
 def gdn_linear_attn(q, k, v, log_decay, s0=None, scale=1.0, y=None, s_final=None, want_final=True,
                     ws=None, stream=None):
     """Decayed linear attention S_t = e^g S_{t-1} + k_t v_t^T, y_t = scale S_t^T q_t of dense
@@ -694,9 +686,10 @@ def gdn_linear_attn(q, k, v, log_decay, s0=None, scale=1.0, y=None, s_final=None
         _want(y, "y", dt, q.shape, dev)
     s_final = _states(s_final, "s_final", (B, H, d, d), dev, want_final)
     ws, wsp, wsb = _scratch(_attn_ws_bytes(0, B, T, H, Hk, d, d, 0), ws, dev)
-    rc = _lib().gdn_linear_attn(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), _ptr(s0),
-                                y.data_ptr(), _ptr(s_final), B, T, H, Hk, d, d, _DT[dt], scale, wsp,
-                                wsb, _raw_stream(stream, dev))
+    f = _lib().gdn_linear_attn
+    a = (q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), _ptr(s0), y.data_ptr(), _ptr(s_final),
+         B, T, H, Hk, d, d, _DT[dt], scale, wsp, wsb, _raw_stream(stream, dev))
+    rc = f(*a) if dev == _current_device() else _launch(dev, f, a)
     if rc:
         _check(rc, "gdn_linear_attn")
     return y, s_final
@@ -714,7 +707,6 @@ def _documents(B, cu_seqlens, dev):
     return n - 1
 
 
-@_on_device
 def gdn_linear_attn_varlen(q, k, v, log_decay, cu_seqlens, s0=None, scale=1.0, y=None,
                            s_final=None, want_final=True, ws=None, stream=None):
     """gdn_linear_attn of packed documents: q [1,T,H,d] or [T,H,d] (k, v likewise), cu_seqlens
@@ -729,15 +721,15 @@ def gdn_linear_attn_varlen(q, k, v, log_decay, cu_seqlens, s0=None, scale=1.0, y
     s0 = _states(s0, "s0", (N, H, d, d), dev)
     s_final = _states(s_final, "s_final", (N, H, d, d), dev, want_final)
     ws, wsp, wsb = _scratch(_attn_ws_bytes(0, 1, T, H, Hk, d, d, N), ws, dev)
-    rc = _lib().gdn_linear_attn_varlen(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
-                                       cu_seqlens.data_ptr(), N, _ptr(s0), y.data_ptr(), _ptr(s_final), T,
-                                       H, Hk, d, d, _DT[dt], scale, wsp, wsb, _raw_stream(stream, dev))
+    f = _lib().gdn_linear_attn_varlen
+    a = (q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), cu_seqlens.data_ptr(), N, _ptr(s0),
+         y.data_ptr(), _ptr(s_final), T, H, Hk, d, d, _DT[dt], scale, wsp, wsb, _raw_stream(stream, dev))
+    rc = f(*a) if dev == _current_device() else _launch(dev, f, a)
     if rc:
         _check(rc, "gdn_linear_attn_varlen")
     return y, s_final
 
 
-@_on_device
 def gdn_linear_attn_decode_step(q, k, v, log_decay, state, scale=1.0, y=None, stream=None):
     """One token of N sequences: q [N,H,d], k and v [N,Hk,d], state [N,H,d,d] fp32 (updated in
     place).  Returns y [N,H,d]."""
@@ -754,15 +746,15 @@ def gdn_linear_attn_decode_step(q, k, v, log_decay, state, scale=1.0, y=None, st
         y = torch.empty_like(q)
     else:
         _want(y, "y", dt, q.shape, dev)
-    rc = _lib().gdn_linear_attn_decode_step(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
-                                            state.data_ptr(), y.data_ptr(), N, H, Hk, d, d, _DT[dt],
-                                            scale, _raw_stream(stream, dev))
+    f = _lib().gdn_linear_attn_decode_step
+    a = (q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), state.data_ptr(), y.data_ptr(), N, H,
+         Hk, d, d, _DT[dt], scale, _raw_stream(stream, dev))
+    rc = f(*a) if dev == _current_device() else _launch(dev, f, a)
     if rc:
         _check(rc, "gdn_linear_attn_decode_step")
     return y
 
 
-@_on_device
 def gdn_linear_attn_backward(q, k, v, log_decay, dy, s0=None, ds_final=None, scale=1.0,
                              want_ds0=True, ws=None, stream=None):
     """Gradients of gdn_linear_attn's (y, s_final) given dy [B,T,H,d] and ds_final.  Returns dict
@@ -774,16 +766,16 @@ def gdn_linear_attn_backward(q, k, v, log_decay, dy, s0=None, ds_final=None, sca
     dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
     ds0 = _states(None, "ds0", (B, H, d, d), dev, want_ds0)
     ws, wsp, wsb = _scratch(_attn_ws_bytes(1, B, T, H, Hk, d, d, 0), ws, dev)
-    rc = _lib().gdn_linear_attn_backward(q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
-                                         _ptr(s0), dy.data_ptr(), _ptr(ds_final), dq.data_ptr(),
-                                         dk.data_ptr(), dv.data_ptr(), _ptr(ds0), B, T, H, Hk, d, d,
-                                         _DT[dt], scale, wsp, wsb, _raw_stream(stream, dev))
+    f = _lib().gdn_linear_attn_backward
+    a = (q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), _ptr(s0), dy.data_ptr(), _ptr(ds_final),
+         dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _ptr(ds0), B, T, H, Hk, d, d, _DT[dt], scale, wsp, wsb,
+         _raw_stream(stream, dev))
+    rc = f(*a) if dev == _current_device() else _launch(dev, f, a)
     if rc:
         _check(rc, "gdn_linear_attn_backward")
     return dict(dq=dq, dk=dk, dv=dv, ds0=ds0)
 
 
-@_on_device
 def gdn_linear_attn_backward_varlen(q, k, v, log_decay, cu_seqlens, dy, s0=None, ds_final=None,
                                     scale=1.0, want_ds0=True, ws=None, stream=None):
     """Gradients of gdn_linear_attn_varlen given dy (like q) and ds_final [N,H,d,d].  Returns
@@ -797,10 +789,11 @@ def gdn_linear_attn_backward_varlen(q, k, v, log_decay, cu_seqlens, dy, s0=None,
     ds_final = _states(ds_final, "ds_final", (N, H, d, d), dev)
     ds0 = _states(None, "ds0", (N, H, d, d), dev, want_ds0)
     ws, wsp, wsb = _scratch(_attn_ws_bytes(1, 1, T, H, Hk, d, d, N), ws, dev)
-    rc = _lib().gdn_linear_attn_backward_varlen(
-        q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), cu_seqlens.data_ptr(), N, _ptr(s0),
-        dy.data_ptr(), _ptr(ds_final), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _ptr(ds0), T, H, Hk, d, d,
-        _DT[dt], scale, wsp, wsb, _raw_stream(stream, dev))
+    f = _lib().gdn_linear_attn_backward_varlen
+    a = (q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), cu_seqlens.data_ptr(), N, _ptr(s0),
+         dy.data_ptr(), _ptr(ds_final), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _ptr(ds0), T, H, Hk, d, d,
+         _DT[dt], scale, wsp, wsb, _raw_stream(stream, dev))
+    rc = f(*a) if dev == _current_device() else _launch(dev, f, a)
     if rc:
         _check(rc, "gdn_linear_attn_backward_varlen")
     return dict(dq=dq, dk=dk, dv=dv, ds0=ds0)
@@ -809,11 +802,14 @@ def gdn_linear_attn_backward_varlen(q, k, v, log_decay, cu_seqlens, dy, s0=None,
 def _heads(t, name, dtype, dev, tokens, heads, d):
     """The token distance of a [T, heads, d] or [B, T, heads, d] tensor whose heads are contiguous and whose
     tokens are evenly spaced (tokens, heads, d: what it must have; heads None: any)."""
-    shape, st = t.shape, t.stride()
-    if t.dtype != dtype or t.get_device() != dev or dev < 0:
+    shape = t.shape
+    if t.dtype is not dtype or t.get_device() != dev or dev < 0:
         _need(t, name, dtype)
         raise ValueError(f"{name} is on device {t.get_device()}, the first tensor on {dev}")
     nd = len(shape)
+    if nd == 3 and t.is_contiguous() and shape[0] == tokens and shape[2] == d and (heads is None or shape[1] == heads):
+        return shape[1] * d
+    st = t.stride()
     if nd != 3 and nd != 4:
         raise ValueError(f"{name} must be [T, heads, d] or [B, T, heads, d]")
     h, hd = shape[-2], shape[-1]
@@ -832,7 +828,6 @@ def _heads(t, name, dtype, dev, tokens, heads, d):
     return ld
 
 
-@_on_device
 def gdn_rotary(q, k, positions, inv_freq, interleaved=False, inverse=False, scale=1.0, q_out=None,
                k_out=None, stream=None):
     """Rotary positions of q [T,Hq,d] and k [T,Hk,d] (or [B,T,..]; k may be None): the first
@@ -867,9 +862,11 @@ def gdn_rotary(q, k, positions, inv_freq, interleaved=False, inverse=False, scal
         q_out, ldqo = torch.empty_like(q, memory_format=torch.contiguous_format), Hq * d
     else:
         ldqo = _heads(q_out, "q_out", dt, dev, T, Hq, d)
-    rc = _lib().gdn_rotary(q.data_ptr(), kp, q_out.data_ptr(), kop, positions.data_ptr(), inv_freq.data_ptr(),
-                           T, Hq, Hk, d, 2 * half, ldq, ldk, ldqo, ldko, 1 if interleaved else 0,
-                           1 if inverse else 0, scale, _DT[dt], _raw_stream(stream, dev))
+    f = _lib().gdn_rotary
+    a = (q.data_ptr(), kp, q_out.data_ptr(), kop, positions.data_ptr(), inv_freq.data_ptr(), T, Hq, Hk, d,
+         2 * half, ldq, ldk, ldqo, ldko, 1 if interleaved else 0, 1 if inverse else 0, scale, _DT[dt],
+         _raw_stream(stream, dev))
+    rc = f(*a) if dev == _current_device() else _launch(dev, f, a)
     if rc:
         _check(rc, "gdn_rotary")
     return q_out, k_out
@@ -913,7 +910,6 @@ def _like(t, name, x, make):
     return t
 
 
-@_on_device
 def gdn_add_rmsnorm(x, residual, w, eps=1e-6, o=None, h=None, stream=None):
     """h = x + residual, o = (1 + w) h / sqrt(mean(h^2) + eps) over the last axis: x, residual
     [..., C] (bf16 or fp32; residual None: h = x and is not written), w [C] fp32.  h may be x or
@@ -923,14 +919,15 @@ def gdn_add_rmsnorm(x, residual, w, eps=1e-6, o=None, h=None, stream=None):
         _want(residual, "residual", dt, shape, dev)
     o = _like(o, "o", x, True)
     h = _like(h, "h", x, residual is not None)
-    rc = _lib().gdn_add_rmsnorm(x.data_ptr(), _ptr(residual), w.data_ptr(), o.data_ptr(), _ptr(h), rows, C,
-                                _DT[dt], eps, _raw_stream(stream, dev))
+    f = _lib().gdn_add_rmsnorm
+    a = (x.data_ptr(), _ptr(residual), w.data_ptr(), o.data_ptr(), _ptr(h), rows, C, _DT[dt], eps,
+         _raw_stream(stream, dev))
+    rc = f(*a) if dev == _current_device() else _launch(dev, f, a)
     if rc:
         _check(rc, "gdn_add_rmsnorm")
     return o, x if h is None else h
 
 
-@_on_device
 def gdn_add_rmsnorm_fp8(x, residual, w, eps=1e-6, group=0, o=None, scales=None, h=None,
                         stream=None):
     """gdn_add_rmsnorm with an 8-bit o (float8_e4m3fn) and fp32 scales [..., C / group]: scale =
@@ -947,8 +944,10 @@ def gdn_add_rmsnorm_fp8(x, residual, w, eps=1e-6, group=0, o=None, scales=None, 
         _want(o, "o", torch.float8_e4m3fn, shape, dev)
     scales = _states(scales, "scales", (*shape[:-1], C // group), dev, True)
     h = _like(h, "h", x, residual is not None)
-    rc = _lib().gdn_add_rmsnorm_fp8(x.data_ptr(), _ptr(residual), w.data_ptr(), o.data_ptr(), scales.data_ptr(),
-                                    _ptr(h), rows, C, group, _DT[dt], eps, _raw_stream(stream, dev))
+    f = _lib().gdn_add_rmsnorm_fp8
+    a = (x.data_ptr(), _ptr(residual), w.data_ptr(), o.data_ptr(), scales.data_ptr(), _ptr(h), rows, C, group,
+         _DT[dt], eps, _raw_stream(stream, dev))
+    rc = f(*a) if dev == _current_device() else _launch(dev, f, a)
     if rc:
         _check(rc, "gdn_add_rmsnorm_fp8")
     return o, scales, x if h is None else h
@@ -959,7 +958,6 @@ def _norm_ws_bytes(rows, C):
     return gdn_workspace_bytes(_abi.GDN_OP_ADD_RMSNORM_BACKWARD, 1, rows, 1, C, C) if rows else 0
 
 
-@_on_device
 def gdn_add_rmsnorm_backward(h, w, d_o, d_h=None, eps=1e-6, ws=None, stream=None):
     """Gradients of gdn_add_rmsnorm from the stored h, given d_o and d_h (the gradient of h itself;
     None = 0).  Returns dict dx (like h: the gradient of x and of residual) and dw [C]."""
@@ -969,9 +967,10 @@ def gdn_add_rmsnorm_backward(h, w, d_o, d_h=None, eps=1e-6, ws=None, stream=None
         _want(d_h, "d_h", dt, shape, dev)
     dx, dw = torch.empty_like(h), torch.empty_like(w)
     ws, wsp, wsb = _scratch(_norm_ws_bytes(rows, C), ws, dev)
-    rc = _lib().gdn_add_rmsnorm_backward(h.data_ptr(), w.data_ptr(), d_o.data_ptr(), _ptr(d_h), dx.data_ptr(),
-                                         dw.data_ptr(), rows, C, _DT[dt], eps, wsp, wsb,
-                                         _raw_stream(stream, dev))
+    f = _lib().gdn_add_rmsnorm_backward
+    a = (h.data_ptr(), w.data_ptr(), d_o.data_ptr(), _ptr(d_h), dx.data_ptr(), dw.data_ptr(), rows, C, _DT[dt],
+         eps, wsp, wsb, _raw_stream(stream, dev))
+    rc = f(*a) if dev == _current_device() else _launch(dev, f, a)
     if rc:
         _check(rc, "gdn_add_rmsnorm_backward")
     return dict(dx=dx, dw=dw)
