@@ -4,6 +4,10 @@ Argument marshalling only: every function checks that the torch tensors are CUDA
 contiguous and of the expected dtype, allocates the outputs (and workspace) it is not
 given, and calls the C entry point on the current CUDA stream.  Every arithmetic step
 runs in the library's kernels; a non-OK status raises ``GdnError``.
+
+``stream`` (every call's last argument) runs the call on that stream instead, and takes what
+the call allocates from it.  As with torch's own operators, the caller orders the streams: the
+tensors given must be ready on that stream, and must be kept until it has used them.
 """
 from __future__ import annotations
 
@@ -22,9 +26,28 @@ def _lib():
     return _abi.load()
 
 
-def _stream(stream):
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+def _stream():
+    return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+
+
+def _on(stream, f, args):
+    """f(**args) with `stream` the current one.  The workspace and the outputs then come from that stream's
+    memory: a block of the caller's current stream could still be in use by its earlier work, and
+    the workspace, dropped when the call returns, could be handed to its next allocation while the
+    kernels run.  Outputs may be used on the caller's current stream, too (after waiting for `stream`)."""
+    t = next((a for a in args.values() if isinstance(a, torch.Tensor) and a.is_cuda), None)
+    if not isinstance(stream, torch.cuda.Stream):  # another library's stream object
+        stream = torch.cuda.ExternalStream(stream.cuda_stream, device=None if t is None else t.device)
+    if t is not None and stream.device != t.device:
+        raise ValueError(f"stream is of {stream.device}, the first tensor on {t.device}")
+    here = torch.cuda.current_stream(stream.device)
+    with torch.cuda.stream(stream):
+        out = f(**{**args, "stream": None})
+    if stream != here:
+        for o in out.values() if isinstance(out, dict) else out if isinstance(out, tuple) else (out,):
+            if isinstance(o, torch.Tensor):
+                o.record_stream(here)
+    return out
 
 
 def _p(t):
@@ -71,6 +94,8 @@ def gdn_prefill(q, k, v, alpha, beta, s0=None, scale=1.0, l2norm_qk=True, y=None
                 s_final=None, want_final=True, ws=None, stream=None):
     """q,k [B,T,H,dk], v [B,T,H,dv] (bf16 or fp32), alpha,beta [B,T,H] fp32,
     s0 [B,H,dk,dv] fp32 or None.  Returns (y, s_final)."""
+    if stream is not None:
+        return _on(stream, gdn_prefill, locals())
     B, T, H, dk = q.shape
     dv = v.shape[-1]
     dt = q.dtype
@@ -91,7 +116,7 @@ def gdn_prefill(q, k, v, alpha, beta, s0=None, scale=1.0, l2norm_qk=True, y=None
     ws, wsb = _workspace(_abi.GDN_OP_PREFILL, q.device, B, T, H, dk, dv, ws=ws)
     rc = _lib().gdn_prefill(_p(q), _p(k), _p(v), _p(alpha), _p(beta), _p(s0), _p(y),
                             _p(s_final), B, T, H, dk, dv, _DT[dt], float(scale),
-                            int(bool(l2norm_qk)), _p(ws), wsb, _stream(stream))
+                            int(bool(l2norm_qk)), _p(ws), wsb, _stream())
     _check(rc, "gdn_prefill")
     return y, s_final
 
@@ -102,6 +127,8 @@ def gdn_prefill_segmented(q, k, v, alpha, beta, s0=None, num_segments=1, scale=1
     """gdn_prefill with every sequence cut into ``num_segments`` segments that run side by side
     (affine state maps, a scan, and a pass from every segment's start state).  Same tensors as
     gdn_prefill.  Returns (y, s_final)."""
+    if stream is not None:
+        return _on(stream, gdn_prefill_segmented, locals())
     B, T, H, dk = q.shape
     dv = v.shape[-1]
     dt = q.dtype
@@ -124,7 +151,7 @@ def gdn_prefill_segmented(q, k, v, alpha, beta, s0=None, num_segments=1, scale=1
     rc = _lib().gdn_prefill_segmented(_p(q), _p(k), _p(v), _p(alpha), _p(beta), _p(s0), _p(y),
                                       _p(s_final), B, T, H, dk, dv, _DT[dt], float(scale),
                                       int(bool(l2norm_qk)), int(num_segments), _p(ws), wsb,
-                                      _stream(stream))
+                                      _stream())
     _check(rc, "gdn_prefill_segmented")
     return y, s_final
 
@@ -133,6 +160,8 @@ def gdn_prefill_varlen(q, k, v, alpha, beta, cu_seqlens, s0=None, scale=1.0, l2n
                        y=None, s_final=None, ws=None, stream=None):
     """Packed documents: q,k [1,T,H,dk] (or [T,H,dk]), v likewise, alpha,beta [1,T,H],
     cu_seqlens int32 [N+1] on the device, s0 [N,H,dk,dv] or None.  Returns (y, s_final)."""
+    if stream is not None:
+        return _on(stream, gdn_prefill_varlen, locals())
     if q.dim() == 3:
         q, k, v, alpha, beta = (x.unsqueeze(0) for x in (q, k, v, alpha, beta))
     _, T, H, dk = q.shape
@@ -158,7 +187,7 @@ def gdn_prefill_varlen(q, k, v, alpha, beta, cu_seqlens, s0=None, scale=1.0, l2n
     rc = _lib().gdn_prefill_varlen(_p(q), _p(k), _p(v), _p(alpha), _p(beta), _p(cu_seqlens), N,
                                    _p(s0), _p(y), _p(s_final), T, H, dk, dv, _DT[dt],
                                    float(scale), int(bool(l2norm_qk)), _p(ws), wsb,
-                                   _stream(stream))
+                                   _stream())
     _check(rc, "gdn_prefill_varlen")
     return y, s_final
 
@@ -167,6 +196,8 @@ def gdn_prefill_varlen_prepare(q, k, v, alpha, beta, cu_seqlens, ws, scale=1.0,
                                l2norm_qk=True, stream=None):
     """First phase of gdn_prefill_varlen (bf16): the state-independent chunk work, into ``ws``
     (a uint8 device tensor of gdn_workspace_bytes(GDN_OP_PREFILL_VARLEN, ...) bytes)."""
+    if stream is not None:
+        return _on(stream, gdn_prefill_varlen_prepare, locals())
     if q.dim() == 3:
         q, k, v, alpha, beta = (x.unsqueeze(0) for x in (q, k, v, alpha, beta))
     _, T, H, dk = q.shape
@@ -181,7 +212,7 @@ def gdn_prefill_varlen_prepare(q, k, v, alpha, beta, cu_seqlens, ws, scale=1.0,
     rc = _lib().gdn_prefill_varlen_prepare(_p(q), _p(k), _p(v), _p(alpha), _p(beta),
                                            _p(cu_seqlens), N, T, H, dk, dv, _DT[torch.bfloat16],
                                            float(scale), int(bool(l2norm_qk)), _p(ws),
-                                           ws.numel() * ws.element_size(), _stream(stream))
+                                           ws.numel() * ws.element_size(), _stream())
     _check(rc, "gdn_prefill_varlen_prepare")
 
 
@@ -189,6 +220,8 @@ def gdn_prefill_varlen_finish(q, k, cu_seqlens, ws, s0=None, y=None, s_final=Non
                               stream=None):
     """Second phase of gdn_prefill_varlen (bf16): the sequential chunk pass from s0 over the
     records gdn_prefill_varlen_prepare wrote into ``ws``.  Returns (y, s_final)."""
+    if stream is not None:
+        return _on(stream, gdn_prefill_varlen_finish, locals())
     if q.dim() == 3:
         q, k = q.unsqueeze(0), k.unsqueeze(0)
     _, T, H, dk = q.shape
@@ -206,7 +239,7 @@ def gdn_prefill_varlen_finish(q, k, cu_seqlens, ws, s0=None, y=None, s_final=Non
     _need(s_final, "s_final", torch.float32, (N, H, dk, dv))
     rc = _lib().gdn_prefill_varlen_finish(_p(q), _p(k), _p(cu_seqlens), N, _p(s0), _p(y),
                                           _p(s_final), T, H, dk, dv, _DT[torch.bfloat16], _p(ws),
-                                          ws.numel() * ws.element_size(), _stream(stream))
+                                          ws.numel() * ws.element_size(), _stream())
     _check(rc, "gdn_prefill_varlen_finish")
     return y, s_final
 
@@ -215,6 +248,8 @@ def gdn_decode_step(q, k, v, alpha, beta, state, scale=1.0, l2norm_qk=True, y=No
                     stream=None):
     """q,k [N,H,dk], v [N,H,dv], alpha,beta [N,H], state [N,H,dk,dv] fp32 (updated in
     place).  Returns y [N,H,dv]."""
+    if stream is not None:
+        return _on(stream, gdn_decode_step, locals())
     N, H, dk = q.shape
     dv = v.shape[-1]
     dt = q.dtype
@@ -231,7 +266,7 @@ def gdn_decode_step(q, k, v, alpha, beta, state, scale=1.0, l2norm_qk=True, y=No
     _need(y, "y", dt, (N, H, dv))
     rc = _lib().gdn_decode_step(_p(q), _p(k), _p(v), _p(alpha), _p(beta), _p(state), _p(y), N, H,
                                 dk, dv, _DT[dt], float(scale), int(bool(l2norm_qk)),
-                                _stream(stream))
+                                _stream())
     _check(rc, "gdn_decode_step")
     return y
 
@@ -240,6 +275,8 @@ def gdn_backward(q, k, v, alpha, beta, dy, s0=None, ds_final=None, scale=1.0, l2
                  want_ds0=True, ws=None, stream=None):
     """Gradients of (y, s_final) w.r.t. (q, k, v, alpha, beta, s0) given dy and ds_final.
     Returns dict dq, dk, dv, dalpha, dbeta, ds0."""
+    if stream is not None:
+        return _on(stream, gdn_backward, locals())
     B, T, H, dk = q.shape
     dv = v.shape[-1]
     dt = q.dtype
@@ -262,7 +299,7 @@ def gdn_backward(q, k, v, alpha, beta, dy, s0=None, ds_final=None, scale=1.0, l2
                              _p(ds_final), _p(out["dq"]), _p(out["dk"]), _p(out["dv"]),
                              _p(out["dalpha"]), _p(out["dbeta"]), _p(out["ds0"]), B, T, H, dk,
                              dv, _DT[dt], float(scale), int(bool(l2norm_qk)), _p(ws), wsb,
-                             _stream(stream))
+                             _stream())
     _check(rc, "gdn_backward")
     return out
 
@@ -273,6 +310,8 @@ def gdn_backward_noalloc(q, k, v, alpha, beta, dy, s0=None, ds_final=None, scale
     library allocates nothing.  ``out`` may supply preallocated gradient tensors (a dict with
     the keys of gdn_backward's result), so that a caller without an allocator can pass its
     own buffers.  Returns the gradient dict."""
+    if stream is not None:
+        return _on(stream, gdn_backward_noalloc, locals())
     B, T, H, dk = q.shape
     dv = v.shape[-1]
     dt = q.dtype
@@ -295,7 +334,7 @@ def gdn_backward_noalloc(q, k, v, alpha, beta, dy, s0=None, ds_final=None, scale
                                      _p(ds_final), _p(out["dq"]), _p(out["dk"]), _p(out["dv"]),
                                      _p(out["dalpha"]), _p(out["dbeta"]), _p(out.get("ds0")), B,
                                      T, H, dk, dv, _DT[dt], float(scale), int(bool(l2norm_qk)),
-                                     _stream(stream))
+                                     _stream())
     _check(rc, "gdn_backward_noalloc")
     return out
 
@@ -315,6 +354,8 @@ def gdn_prefill_gated(q, k, v, a, b, A_log, b_alpha, s0=None, scale=1.0, l2norm_
                       y=None, s_final=None, want_final=True, ws=None, stream=None):
     """gdn_prefill with alpha and beta given by eqs. (9)-(10): a = W_alpha x, b = W_beta x
     [B,T,H] fp32, A_log and b_alpha [H] fp32.  Returns (y, s_final)."""
+    if stream is not None:
+        return _on(stream, gdn_prefill_gated, locals())
     B, T, H, dk = q.shape
     dv = v.shape[-1]
     dt = q.dtype
@@ -335,7 +376,7 @@ def gdn_prefill_gated(q, k, v, a, b, A_log, b_alpha, s0=None, scale=1.0, l2norm_
     rc = _lib().gdn_prefill_gated(_p(q), _p(k), _p(v), _p(a), _p(b), _p(A_log), _p(b_alpha),
                                   _p(s0), _p(y), _p(s_final), B, T, H, dk, dv, _DT[dt],
                                   float(scale), int(bool(l2norm_qk)), _p(ws), wsb,
-                                  _stream(stream))
+                                  _stream())
     _check(rc, "gdn_prefill_gated")
     return y, s_final
 
@@ -344,6 +385,8 @@ def gdn_prefill_varlen_gated(q, k, v, a, b, A_log, b_alpha, cu_seqlens, s0=None,
                              l2norm_qk=True, y=None, s_final=None, ws=None, stream=None):
     """gdn_prefill_varlen with alpha and beta given by eqs. (9)-(10) (a, b [1,T,H] or [T,H]
     fp32; A_log, b_alpha [H]).  Returns (y, s_final)."""
+    if stream is not None:
+        return _on(stream, gdn_prefill_varlen_gated, locals())
     if q.dim() == 3:
         q, k, v, a, b = (x.unsqueeze(0) for x in (q, k, v, a, b))
     _, T, H, dk = q.shape
@@ -368,7 +411,7 @@ def gdn_prefill_varlen_gated(q, k, v, a, b, A_log, b_alpha, cu_seqlens, s0=None,
     rc = _lib().gdn_prefill_varlen_gated(_p(q), _p(k), _p(v), _p(a), _p(b), _p(A_log),
                                          _p(b_alpha), _p(cu_seqlens), N, _p(s0), _p(y),
                                          _p(s_final), T, H, dk, dv, _DT[dt], float(scale),
-                                         int(bool(l2norm_qk)), _p(ws), wsb, _stream(stream))
+                                         int(bool(l2norm_qk)), _p(ws), wsb, _stream())
     _check(rc, "gdn_prefill_varlen_gated")
     return y, s_final
 
@@ -377,6 +420,8 @@ def gdn_decode_step_gated(q, k, v, a, b, A_log, b_alpha, state, scale=1.0, l2nor
                           y=None, stream=None):
     """gdn_decode_step with alpha and beta given by eqs. (9)-(10) (a, b [N,H] fp32; A_log,
     b_alpha [H]).  The state is updated in place.  Returns y [N,H,dv]."""
+    if stream is not None:
+        return _on(stream, gdn_decode_step_gated, locals())
     N, H, dk = q.shape
     dv = v.shape[-1]
     dt = q.dtype
@@ -392,7 +437,7 @@ def gdn_decode_step_gated(q, k, v, a, b, A_log, b_alpha, state, scale=1.0, l2nor
     _need(y, "y", dt, (N, H, dv))
     rc = _lib().gdn_decode_step_gated(_p(q), _p(k), _p(v), _p(a), _p(b), _p(A_log), _p(b_alpha),
                                       _p(state), _p(y), N, H, dk, dv, _DT[dt], float(scale),
-                                      int(bool(l2norm_qk)), _stream(stream))
+                                      int(bool(l2norm_qk)), _stream())
     _check(rc, "gdn_decode_step_gated")
     return y
 
@@ -401,6 +446,8 @@ def gdn_backward_gated(q, k, v, a, b, A_log, b_alpha, dy, s0=None, ds_final=None
                        l2norm_qk=True, want_ds0=True, ws=None, stream=None):
     """Gradients of (y, s_final) for the gated form.  Returns dict dq, dk, dv, da, db,
     dA_log, db_alpha, ds0."""
+    if stream is not None:
+        return _on(stream, gdn_backward_gated, locals())
     B, T, H, dk = q.shape
     dv = v.shape[-1]
     dt = q.dtype
@@ -424,7 +471,7 @@ def gdn_backward_gated(q, k, v, a, b, A_log, b_alpha, dy, s0=None, ds_final=None
                                    _p(out["dv"]), _p(out["da"]), _p(out["db"]),
                                    _p(out["dA_log"]), _p(out["db_alpha"]), _p(out["ds0"]), B, T,
                                    H, dk, dv, _DT[dt], float(scale), int(bool(l2norm_qk)), _p(ws),
-                                   wsb, _stream(stream))
+                                   wsb, _stream())
     _check(rc, "gdn_backward_gated")
     return out
 
@@ -432,6 +479,8 @@ def gdn_backward_gated(q, k, v, a, b, A_log, b_alpha, dy, s0=None, ds_final=None
 def gdn_gated_rmsnorm(y, z, w, eps=1e-6, o=None, stream=None):
     """The bracket of eq. (11): sigmoid(z) * (1 + w) * y / sqrt(mean(y^2) + eps) over the last
     axis.  y, z [..., dv] (bf16 or fp32, same dtype), w [dv] fp32.  Returns o like y."""
+    if stream is not None:
+        return _on(stream, gdn_gated_rmsnorm, locals())
     dt = y.dtype
     if dt not in _DT:
         raise ValueError("y/z must be bf16 or fp32")
@@ -444,13 +493,15 @@ def gdn_gated_rmsnorm(y, z, w, eps=1e-6, o=None, stream=None):
     _need(o, "o", dt, y.shape)
     rows = y.numel() // dv if dv else 0
     rc = _lib().gdn_gated_rmsnorm(_p(y), _p(z), _p(w), _p(o), rows, dv, _DT[dt], float(eps),
-                                  _stream(stream))
+                                  _stream())
     _check(rc, "gdn_gated_rmsnorm")
     return o
 
 
 def gdn_gated_rmsnorm_backward(y, z, w, d_o, eps=1e-6, stream=None):
     """Gradients of gdn_gated_rmsnorm given d_o.  Returns dict dy, dz (like y) and dw [dv]."""
+    if stream is not None:
+        return _on(stream, gdn_gated_rmsnorm_backward, locals())
     dt = y.dtype
     if dt not in _DT:
         raise ValueError("y/z must be bf16 or fp32")
@@ -463,7 +514,7 @@ def gdn_gated_rmsnorm_backward(y, z, w, d_o, eps=1e-6, stream=None):
     rows = y.numel() // dv if dv else 0
     rc = _lib().gdn_gated_rmsnorm_backward(_p(y), _p(z), _p(w), _p(d_o), _p(out["dy"]),
                                            _p(out["dz"]), _p(out["dw"]), rows, dv, _DT[dt],
-                                           float(eps), _stream(stream))
+                                           float(eps), _stream())
     _check(rc, "gdn_gated_rmsnorm_backward")
     return out
 
@@ -478,7 +529,9 @@ def gdn_read_device_status(reset=True):
 def gdn_selftest_wait_timeout(limit_ns=1_000_000, stream=None):
     """Launch the kernel whose bounded wait runs out (see include/gdn.h); afterwards
     gdn_read_device_status() reports GDN_ERR_TIMEOUT."""
-    _check(_lib().gdn_selftest_wait_timeout(int(limit_ns), _stream(stream)),
+    if stream is not None:
+        return _on(stream, gdn_selftest_wait_timeout, locals())
+    _check(_lib().gdn_selftest_wait_timeout(int(limit_ns), _stream()),
            "gdn_selftest_wait_timeout")
 
 
@@ -490,6 +543,8 @@ def gdn_short_conv_varlen(x, w, cu_seqlens, conv_state=None, activation="none",
     """Short causal convolution of packed documents: x [T, C] (bf16 or fp32, C % 8 == 0),
     w [C, W] fp32, cu_seqlens [N+1] int32 (CUDA), conv_state [N, W-1, C] like x or None (zero).
     Returns (y [T, C], final conv state [N, W-1, C] or None)."""
+    if stream is not None:
+        return _on(stream, gdn_short_conv_varlen, locals())
     dt = x.dtype
     if dt not in _DT:
         raise ValueError("x must be bf16 or fp32")
@@ -507,7 +562,7 @@ def gdn_short_conv_varlen(x, w, cu_seqlens, conv_state=None, activation="none",
     _need(y, "y", dt, (T, C))
     sf = torch.empty((N, W - 1, C), dtype=dt, device=x.device) if return_state else None
     rc = _lib().gdn_short_conv_varlen(_p(x), _p(w), _p(cu_seqlens), N, _p(conv_state), _p(sf),
-                                      _p(y), T, C, W, _DT[dt], _ACT[activation], _stream(stream))
+                                      _p(y), T, C, W, _DT[dt], _ACT[activation], _stream())
     _check(rc, "gdn_short_conv_varlen")
     return y, sf
 
@@ -515,6 +570,8 @@ def gdn_short_conv_varlen(x, w, cu_seqlens, conv_state=None, activation="none",
 def gdn_short_conv_step(x, w, conv_state, activation="none", y=None, stream=None):
     """One decode token per sequence: x [N, C], w [C, W] fp32, conv_state [N, W-1, C] like x,
     updated in place.  Returns y [N, C]."""
+    if stream is not None:
+        return _on(stream, gdn_short_conv_step, locals())
     dt = x.dtype
     if dt not in _DT:
         raise ValueError("x must be bf16 or fp32")
@@ -527,7 +584,7 @@ def gdn_short_conv_step(x, w, conv_state, activation="none", y=None, stream=None
         y = torch.empty_like(x)
     _need(y, "y", dt, (N, C))
     rc = _lib().gdn_short_conv_step(_p(x), _p(w), _p(conv_state), _p(y), N, C, W, _DT[dt],
-                                    _ACT[activation], _stream(stream))
+                                    _ACT[activation], _stream())
     _check(rc, "gdn_short_conv_step")
     return y
 
@@ -541,6 +598,8 @@ def gdn_qsa_block_scores(q, k, g, cu_seqlens, max_doc_len, stream=None):
     fp32, cu_seqlens [N+1] int32 (CUDA), every document at most max_doc_len tokens.  Returns
     (k_hat [T//4, 128] bf16, block_base [N+1] int32, scores [T, ld] fp32); row t of scores holds
     its visible blocks' scores (document-local block order), the rest is not written."""
+    if stream is not None:
+        return _on(stream, gdn_qsa_block_scores, locals())
     T = q.shape[0]
     _need(q, "q", torch.bfloat16, (T, 4, 128))
     _need(k, "k", torch.bfloat16, (T, 128))
@@ -556,13 +615,15 @@ def gdn_qsa_block_scores(q, k, g, cu_seqlens, max_doc_len, stream=None):
                      dtype=torch.uint8, device=dev)
     rc = _lib().gdn_qsa_block_scores(_p(q), _p(k), _p(g), _p(cu_seqlens), N, T, int(max_doc_len),
                                      _p(k_hat), _p(base), _p(scores), ld, _p(ws), ws.numel(),
-                                     _stream(stream))
+                                     _stream())
     _check(rc, "gdn_qsa_block_scores")
     return k_hat, base, scores
 
 
 def gdn_qsa_select_blocks(scores, cu_seqlens, budget=512, sel=None, stream=None):
     """Top-budget block selection from gdn_qsa_block_scores' scores: sel [T, budget] int32."""
+    if stream is not None:
+        return _on(stream, gdn_qsa_select_blocks, locals())
     _need(scores, "scores", torch.float32)
     _need(cu_seqlens, "cu_seqlens", torch.int32)
     T, ld = scores.shape
@@ -570,15 +631,17 @@ def gdn_qsa_select_blocks(scores, cu_seqlens, budget=512, sel=None, stream=None)
         sel = torch.empty((T, budget), dtype=torch.int32, device=scores.device)
     _need(sel, "sel", torch.int32, (T, budget))
     rc = _lib().gdn_qsa_select_blocks(_p(scores), ld, _p(cu_seqlens), cu_seqlens.numel() - 1, T,
-                                      int(budget), _p(sel), _stream(stream))
+                                      int(budget), _p(sel), _stream())
     _check(rc, "gdn_qsa_select_blocks")
     return sel
 
 
 def gdn_qsa_indexer(q, k, g, cu_seqlens, max_doc_len, budget=512, stream=None):
     """Both steps: returns (sel [T, budget] int32, k_hat, block_base, scores)."""
-    k_hat, base, scores = gdn_qsa_block_scores(q, k, g, cu_seqlens, max_doc_len, stream)
-    return gdn_qsa_select_blocks(scores, cu_seqlens, budget, stream=stream), k_hat, base, scores
+    if stream is not None:
+        return _on(stream, gdn_qsa_indexer, locals())
+    k_hat, base, scores = gdn_qsa_block_scores(q, k, g, cu_seqlens, max_doc_len)
+    return gdn_qsa_select_blocks(scores, cu_seqlens, budget), k_hat, base, scores
 
 
 # The calls below serve decode steps of a few microseconds on the GPU, so their checks are kept short: one
@@ -593,10 +656,6 @@ def _launch(dev, f, a):
     """f(*a) with device dev current: a launch goes to the current device, whatever device its pointers are on."""
     with torch.cuda.device(dev):
         return f(*a)
-
-
-def _raw_stream(stream, dev):
-    return _current_stream(dev) if stream is None else stream.cuda_stream
 
 
 def _ptr(t):
@@ -678,6 +737,8 @@ def gdn_linear_attn(q, k, v, log_decay, s0=None, scale=1.0, y=None, s_final=None
     """Decayed linear attention S_t = e^g S_{t-1} + k_t v_t^T, y_t = scale S_t^T q_t of dense
     sequences: q [B,T,H,d], k and v [B,T,Hk,d] (bf16 or fp32; Hk divides H), log_decay [H] fp32
     (g <= 0, a constant), s0 [B,H,d,d] fp32 or None.  Returns (y, s_final)."""
+    if stream is not None:
+        return _on(stream, gdn_linear_attn, locals())
     dt, dev, B, T, H, Hk, d = _attn_shapes(q, k, v, log_decay)
     s0 = _states(s0, "s0", (B, H, d, d), dev)
     if y is None:
@@ -688,7 +749,7 @@ def gdn_linear_attn(q, k, v, log_decay, s0=None, scale=1.0, y=None, s_final=None
     ws, wsp, wsb = _scratch(_attn_ws_bytes(0, B, T, H, Hk, d, d, 0), ws, dev)
     f = _lib().gdn_linear_attn
     a = (q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), _ptr(s0), y.data_ptr(), _ptr(s_final),
-         B, T, H, Hk, d, d, _DT[dt], scale, wsp, wsb, _raw_stream(stream, dev))
+         B, T, H, Hk, d, d, _DT[dt], scale, wsp, wsb, _current_stream(dev))
     rc = f(*a) if dev == _current_device() else _launch(dev, f, a)
     if rc:
         _check(rc, "gdn_linear_attn")
@@ -711,6 +772,8 @@ def gdn_linear_attn_varlen(q, k, v, log_decay, cu_seqlens, s0=None, scale=1.0, y
                            s_final=None, want_final=True, ws=None, stream=None):
     """gdn_linear_attn of packed documents: q [1,T,H,d] or [T,H,d] (k, v likewise), cu_seqlens
     int32 [N+1] on the device, s0 [N,H,d,d] fp32 or None.  Returns (y like q, s_final)."""
+    if stream is not None:
+        return _on(stream, gdn_linear_attn_varlen, locals())
     if y is None:
         y = torch.empty_like(q)
     else:
@@ -723,7 +786,7 @@ def gdn_linear_attn_varlen(q, k, v, log_decay, cu_seqlens, s0=None, scale=1.0, y
     ws, wsp, wsb = _scratch(_attn_ws_bytes(0, 1, T, H, Hk, d, d, N), ws, dev)
     f = _lib().gdn_linear_attn_varlen
     a = (q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), cu_seqlens.data_ptr(), N, _ptr(s0),
-         y.data_ptr(), _ptr(s_final), T, H, Hk, d, d, _DT[dt], scale, wsp, wsb, _raw_stream(stream, dev))
+         y.data_ptr(), _ptr(s_final), T, H, Hk, d, d, _DT[dt], scale, wsp, wsb, _current_stream(dev))
     rc = f(*a) if dev == _current_device() else _launch(dev, f, a)
     if rc:
         _check(rc, "gdn_linear_attn_varlen")
@@ -733,6 +796,8 @@ def gdn_linear_attn_varlen(q, k, v, log_decay, cu_seqlens, s0=None, scale=1.0, y
 def gdn_linear_attn_decode_step(q, k, v, log_decay, state, scale=1.0, y=None, stream=None):
     """One token of N sequences: q [N,H,d], k and v [N,Hk,d], state [N,H,d,d] fp32 (updated in
     place).  Returns y [N,H,d]."""
+    if stream is not None:
+        return _on(stream, gdn_linear_attn_decode_step, locals())
     dt = _dtype(q, "q/k/v")
     N, H, d = q.shape
     Hk = k.shape[1]
@@ -748,7 +813,7 @@ def gdn_linear_attn_decode_step(q, k, v, log_decay, state, scale=1.0, y=None, st
         _want(y, "y", dt, q.shape, dev)
     f = _lib().gdn_linear_attn_decode_step
     a = (q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), state.data_ptr(), y.data_ptr(), N, H,
-         Hk, d, d, _DT[dt], scale, _raw_stream(stream, dev))
+         Hk, d, d, _DT[dt], scale, _current_stream(dev))
     rc = f(*a) if dev == _current_device() else _launch(dev, f, a)
     if rc:
         _check(rc, "gdn_linear_attn_decode_step")
@@ -759,6 +824,8 @@ def gdn_linear_attn_backward(q, k, v, log_decay, dy, s0=None, ds_final=None, sca
                              want_ds0=True, ws=None, stream=None):
     """Gradients of gdn_linear_attn's (y, s_final) given dy [B,T,H,d] and ds_final.  Returns dict
     dq, dk, dv (like q, k, v) and ds0 [B,H,d,d] (None unless want_ds0)."""
+    if stream is not None:
+        return _on(stream, gdn_linear_attn_backward, locals())
     dt, dev, B, T, H, Hk, d = _attn_shapes(q, k, v, log_decay)
     _want(dy, "dy", dt, q.shape, dev)
     s0 = _states(s0, "s0", (B, H, d, d), dev)
@@ -769,7 +836,7 @@ def gdn_linear_attn_backward(q, k, v, log_decay, dy, s0=None, ds_final=None, sca
     f = _lib().gdn_linear_attn_backward
     a = (q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), _ptr(s0), dy.data_ptr(), _ptr(ds_final),
          dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _ptr(ds0), B, T, H, Hk, d, d, _DT[dt], scale, wsp, wsb,
-         _raw_stream(stream, dev))
+         _current_stream(dev))
     rc = f(*a) if dev == _current_device() else _launch(dev, f, a)
     if rc:
         _check(rc, "gdn_linear_attn_backward")
@@ -780,6 +847,8 @@ def gdn_linear_attn_backward_varlen(q, k, v, log_decay, cu_seqlens, dy, s0=None,
                                     scale=1.0, want_ds0=True, ws=None, stream=None):
     """Gradients of gdn_linear_attn_varlen given dy (like q) and ds_final [N,H,d,d].  Returns
     dict dq, dk, dv (like q, k, v) and ds0 [N,H,d,d] (None unless want_ds0)."""
+    if stream is not None:
+        return _on(stream, gdn_linear_attn_backward_varlen, locals())
     _want(dy, "dy", q.dtype, q.shape, q.get_device())
     dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
     q, k, v = _packed(q, k, v)
@@ -792,7 +861,7 @@ def gdn_linear_attn_backward_varlen(q, k, v, log_decay, cu_seqlens, dy, s0=None,
     f = _lib().gdn_linear_attn_backward_varlen
     a = (q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(), cu_seqlens.data_ptr(), N, _ptr(s0),
          dy.data_ptr(), _ptr(ds_final), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _ptr(ds0), T, H, Hk, d, d,
-         _DT[dt], scale, wsp, wsb, _raw_stream(stream, dev))
+         _DT[dt], scale, wsp, wsb, _current_stream(dev))
     rc = f(*a) if dev == _current_device() else _launch(dev, f, a)
     if rc:
         _check(rc, "gdn_linear_attn_backward_varlen")
@@ -835,6 +904,8 @@ def gdn_rotary(q, k, positions, inv_freq, interleaved=False, inverse=False, scal
     by positions[t] * inv_freq[i] and are scaled; inverse turns back (the gradient).  q and k may be
     views into one projection (contiguous heads, evenly spaced tokens).  positions int32 (one
     per token), inv_freq fp32 on the device.  q_out / k_out may be q / k.  Returns (q_out, k_out)."""
+    if stream is not None:
+        return _on(stream, gdn_rotary, locals())
     dt = _dtype(q, "q/k")
     dev = q.get_device()
     if q.dim() < 3:
@@ -865,7 +936,7 @@ def gdn_rotary(q, k, positions, inv_freq, interleaved=False, inverse=False, scal
     f = _lib().gdn_rotary
     a = (q.data_ptr(), kp, q_out.data_ptr(), kop, positions.data_ptr(), inv_freq.data_ptr(), T, Hq, Hk, d,
          2 * half, ldq, ldk, ldqo, ldko, 1 if interleaved else 0, 1 if inverse else 0, scale, _DT[dt],
-         _raw_stream(stream, dev))
+         _current_stream(dev))
     rc = f(*a) if dev == _current_device() else _launch(dev, f, a)
     if rc:
         _check(rc, "gdn_rotary")
@@ -914,6 +985,8 @@ def gdn_add_rmsnorm(x, residual, w, eps=1e-6, o=None, h=None, stream=None):
     """h = x + residual, o = (1 + w) h / sqrt(mean(h^2) + eps) over the last axis: x, residual
     [..., C] (bf16 or fp32; residual None: h = x and is not written), w [C] fp32.  h may be x or
     residual, o may be x.  Returns (o, h)."""
+    if stream is not None:
+        return _on(stream, gdn_add_rmsnorm, locals())
     dt, dev, shape, C, rows = _rows(x, w, "x")
     if residual is not None:
         _want(residual, "residual", dt, shape, dev)
@@ -921,7 +994,7 @@ def gdn_add_rmsnorm(x, residual, w, eps=1e-6, o=None, h=None, stream=None):
     h = _like(h, "h", x, residual is not None)
     f = _lib().gdn_add_rmsnorm
     a = (x.data_ptr(), _ptr(residual), w.data_ptr(), o.data_ptr(), _ptr(h), rows, C, _DT[dt], eps,
-         _raw_stream(stream, dev))
+         _current_stream(dev))
     rc = f(*a) if dev == _current_device() else _launch(dev, f, a)
     if rc:
         _check(rc, "gdn_add_rmsnorm")
@@ -932,6 +1005,8 @@ def gdn_add_rmsnorm_fp8(x, residual, w, eps=1e-6, group=0, o=None, scales=None, 
                         stream=None):
     """gdn_add_rmsnorm with an 8-bit o (float8_e4m3fn) and fp32 scales [..., C / group]: scale =
     max|o| / 448 over each group of columns, group 0 (a whole row) or 128.  Returns (o, scales, h)."""
+    if stream is not None:
+        return _on(stream, gdn_add_rmsnorm_fp8, locals())
     dt, dev, shape, C, rows = _rows(x, w, "x")
     if residual is not None:
         _want(residual, "residual", dt, shape, dev)
@@ -946,7 +1021,7 @@ def gdn_add_rmsnorm_fp8(x, residual, w, eps=1e-6, group=0, o=None, scales=None, 
     h = _like(h, "h", x, residual is not None)
     f = _lib().gdn_add_rmsnorm_fp8
     a = (x.data_ptr(), _ptr(residual), w.data_ptr(), o.data_ptr(), scales.data_ptr(), _ptr(h), rows, C, group,
-         _DT[dt], eps, _raw_stream(stream, dev))
+         _DT[dt], eps, _current_stream(dev))
     rc = f(*a) if dev == _current_device() else _launch(dev, f, a)
     if rc:
         _check(rc, "gdn_add_rmsnorm_fp8")
@@ -961,6 +1036,8 @@ def _norm_ws_bytes(rows, C):
 def gdn_add_rmsnorm_backward(h, w, d_o, d_h=None, eps=1e-6, ws=None, stream=None):
     """Gradients of gdn_add_rmsnorm from the stored h, given d_o and d_h (the gradient of h itself;
     None = 0).  Returns dict dx (like h: the gradient of x and of residual) and dw [C]."""
+    if stream is not None:
+        return _on(stream, gdn_add_rmsnorm_backward, locals())
     dt, dev, shape, C, rows = _rows(h, w, "h")
     _want(d_o, "d_o", dt, shape, dev)
     if d_h is not None:
@@ -969,7 +1046,7 @@ def gdn_add_rmsnorm_backward(h, w, d_o, d_h=None, eps=1e-6, ws=None, stream=None
     ws, wsp, wsb = _scratch(_norm_ws_bytes(rows, C), ws, dev)
     f = _lib().gdn_add_rmsnorm_backward
     a = (h.data_ptr(), w.data_ptr(), d_o.data_ptr(), _ptr(d_h), dx.data_ptr(), dw.data_ptr(), rows, C, _DT[dt],
-         eps, wsp, wsb, _raw_stream(stream, dev))
+         eps, wsp, wsb, _current_stream(dev))
     rc = f(*a) if dev == _current_device() else _launch(dev, f, a)
     if rc:
         _check(rc, "gdn_add_rmsnorm_backward")
