@@ -85,7 +85,9 @@ rotary_kernel(const RotaryArgs p, int units, int turned, int per_block) {
     const int hpw = units < 32 ? 32 / units : 1;  // heads the lanes cover at once
     const int hh = units < 32 ? lane / units : 0, u0 = units < 32 ? lane - hh * units : lane;
     const int first = blockIdx.y * per_block, last = min(first + per_block, p.a[0].heads + p.a[1].heads);
-    for (int t = blockIdx.x * kRotWarps + warp; t < p.T; t += gridDim.x * kRotWarps) {
+    // (counted down: a step past the last token may not fit 31 bits)
+    for (int left = p.T - (int)(blockIdx.x * kRotWarps + warp); left > 0; left -= gridDim.x * kRotWarps) {
+        const int t = p.T - left;
         const long long pos = p.positions[t];
         __syncwarp();  // the last token's factors are read
         for (int i = lane, k = 0; i < half; i += 32, ++k) {
@@ -166,7 +168,7 @@ cudaError_t launch(const RotaryArgs& a, bool keep, cudaStream_t st) {
     // three times the blocks that fit the SMs at once walk over the tokens (32768 tokens of 18 heads of 128: 54.1 us;
     // once 55.3 us, six times 55.2 us, a warp a token 56 us); few tokens: the heads go over several blocks, each of
     // which computes the angles again
-    const int blocks = (a.T + kRotWarps - 1) / kRotWarps, fit = 148 * kRotBlocks;
+    const int blocks = a.T / kRotWarps + (a.T % kRotWarps != 0), fit = 148 * kRotBlocks;
     const int hpw = units < 32 ? 32 / units : 1;
     int split = fit / blocks;
     const int most = (heads + hpw - 1) / hpw;

@@ -100,3 +100,23 @@ def test_no_tokens_and_graph():
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(got, want)
+
+
+def test_token_counts_up_to_31_bits():
+    """2^31 - 1 tokens, in place (a step of the grid past the last token does not fit 31 bits): every token is turned
+    once, those of position 0 keep their values."""
+    T = 2 ** 31 - 1
+    f = api.gdn_rotary_inv_freq(8)[0]
+    x = torch.ones(T, 1, 8, dtype=torch.bfloat16, device="cuda")
+    pos = torch.zeros(T, dtype=torch.int32, device="cuda")
+    at = torch.tensor([0, 1, 17759, 17760, 2 ** 28, 2 ** 30 + 1, T - 17761, T - 17760, T - 4, T - 3, T - 2, T - 1])
+    pos[at.cuda()] = torch.arange(1, len(at) + 1, dtype=torch.int32, device="cuda")
+    api.gdn_rotary(x, None, pos, f.cuda(), q_out=x)
+    torch.cuda.synchronize()
+    check(x[at.cuda()], torch.ones(len(at), 1, 8, dtype=torch.bfloat16), torch.arange(1, len(at) + 1, dtype=torch.int32), f,
+          "bf16", False, False, 1.0)
+    x[at.cuda()] = 1
+    for i in range(0, T, 2 ** 28):
+        assert bool((x[i:i + 2 ** 28] == 1).all())
+    del x, pos
+    torch.cuda.empty_cache()
