@@ -674,6 +674,13 @@ def _want(t, name, dtype, shape, dev):
         _refuse(t, name, dtype, shape, dev)
 
 
+_INT_MAX = 2 ** 31 - 1  # of the sizes that the library takes as ints: a larger one would arrive as its low 32 bits
+
+
+def _too_large(what, n):
+    raise ValueError(f"{what} must be below 2^31, got {n}")
+
+
 def _dtype(t, name):
     dt = t.dtype
     if dt not in _DT:
@@ -764,6 +771,8 @@ def _documents(B, cu_seqlens, dev):
     if B != 1:
         raise ValueError("packed documents are one stream: q must be [1, T, H, d] or [T, H, d]")
     n = cu_seqlens.numel()
+    if n > _INT_MAX:
+        _too_large("cu_seqlens' length", n)
     _want(cu_seqlens, "cu_seqlens", torch.int32, (n,), dev)
     return n - 1
 
@@ -912,6 +921,8 @@ def gdn_rotary(q, k, positions, inv_freq, interleaved=False, inverse=False, scal
         raise ValueError("q must be [T, heads, d] or [B, T, heads, d]")
     Hq, d = q.shape[-2:]
     T = q.shape[0] if q.dim() == 3 else q.shape[0] * q.shape[1]
+    if T > _INT_MAX or Hq * d > _INT_MAX:
+        _too_large("q's tokens, and a token's row,", (T, Hq * d))
     ldq = _heads(q, "q", dt, dev, T, None, d)
     _want(positions, "positions", torch.int32, positions.shape, dev)
     half = inv_freq.numel()
@@ -923,6 +934,8 @@ def gdn_rotary(q, k, positions, inv_freq, interleaved=False, inverse=False, scal
         kp = kop = k_out = None
     else:
         Hk = k.shape[-2]
+        if Hk * d > _INT_MAX:
+            _too_large("a token's row of k", Hk * d)
         ldk = _heads(k, "k", dt, dev, T, None, d)
         if k_out is None:
             k_out, ldko = torch.empty_like(k, memory_format=torch.contiguous_format), Hk * d
@@ -967,6 +980,8 @@ def _rows(x, w, name):
     dt = _dtype(x, name)
     dev, shape = x.get_device(), x.shape
     C = shape[-1]
+    if C > _INT_MAX:
+        _too_large("the last axis", C)
     _want(x, name, dt, shape, dev)
     _want(w, "w", torch.float32, (C,), dev)
     return dt, dev, shape, C, x.numel() // C if C else 0

@@ -613,6 +613,7 @@ int gdn_rotary(const void* q, const void* k, void* q_out, void* k_out, const int
     const auto ok = [T, d](const void* x, const void* y, int heads, int64_t ldx, int64_t ldy) {
         if (heads == 0) return true;
         const int64_t row = (int64_t)heads * d;
+        if (row >= (1ll << 31)) return false;  // places within a row are kept in 32 bits
         if (ldx < row || ldy < row || ldx % 8 != 0 || ldy % 8 != 0) return false;
         if (x == y && ldx != ldy) return false;  // in place: the same rows
         return T == 0 ? aligned16(x) && aligned16(y) : ok_ptr(x) && ok_ptr(y);

@@ -180,3 +180,29 @@ def test_bindings_refuse_host_tensors_and_shapes():
         api.gdn_add_rmsnorm(t[0, :, 0], None, torch.zeros(64))
     with pytest.raises(ValueError, match="CUDA"):
         api.gdn_add_rmsnorm_backward(t[0, :, 0], torch.zeros(64), t[0, :, 0])
+
+
+def test_rotary_rows_of_31_bits_are_refused(lib):
+    """Places within a token's row are kept in 32 bits."""
+    def call(Hq, Hk, d):
+        lq, lk = Hq * d, max(Hk, 1) * d
+        return lib.gdn_rotary(A, A, A, A, A, A, 1, Hq, Hk, d, 8, lq, lk, lq, lk, 0, 0, 1.0, 0, None)
+    assert call(1 << 21, 0, 1024) == BAD and call(1, 1 << 28, 8) == BAD and call(1 << 28, 1 << 28, 8) == BAD
+
+
+def test_bindings_refuse_sizes_past_31_bits():
+    """The library takes them as ints, and ctypes hands over the low 32 bits without a word."""
+    big = torch.zeros(1, dtype=torch.bfloat16).expand((1 << 32) + 8)
+    pos, f, w = torch.zeros(8, dtype=torch.int32), torch.zeros(4), torch.zeros(8)
+    with pytest.raises(ValueError, match="2\\^31"):
+        api.gdn_rotary(big[:, None, None].expand(-1, 1, 8), None, pos, f)
+    with pytest.raises(ValueError, match="2\\^31"):
+        api.gdn_rotary(big[None, :, None].expand(1, -1, 8), None, pos, f)
+    with pytest.raises(ValueError, match="2\\^31"):
+        api.gdn_add_rmsnorm(big[None], None, w)
+    with pytest.raises(ValueError, match="2\\^31"):
+        api.gdn_add_rmsnorm_fp8(big[None], None, w)
+    with pytest.raises(ValueError, match="2\\^31"):
+        api.gdn_add_rmsnorm_backward(big[None], w, big[None])
+    with pytest.raises(ValueError, match="2\\^31"):
+        api._documents(1, torch.zeros(1, dtype=torch.int32).expand((1 << 32) + 2), 0)
