@@ -495,11 +495,11 @@ static int check_attn(const float* log_decay, int H, int Hk, int dk, int dv, int
     if (!ok_ptr(log_decay) || H < 1 || Hk < 1 || H % Hk != 0) return GDN_ERR_INVALID_ARG;
     return check_dims(dk, dv, dtype);
 }
-// the tokens and the grid's (segment, head) count, with the rounds behind it, stay within 31 bits
+// the tokens, the grid's (segment, head) count and a CTA's next (document, head) place stay within 31 bits
 static bool ok_tokens(int num_seqs, int T, int H, bool packed) {
     const long long tokens = packed ? T : (long long)num_seqs * T;
     const long long segments = tokens / 64 + num_seqs;
-    return tokens < (1ll << 31) - 64 && segments * H < (1ll << 31) - 65536;
+    return tokens < (1ll << 31) - 64 && segments * H < (1ll << 31) - 65536 && (long long)num_seqs * H < (1ll << 30);
 }
 
 int gdn_linear_attn_workspace_bytes(int backward, int B, int T, int H, int Hk, int dk, int dv, int num_seqs,

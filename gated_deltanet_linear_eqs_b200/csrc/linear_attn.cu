@@ -398,7 +398,7 @@ LaPlan make_plan(int num_seqs, int T, int H, int d, bool packed, int dtype) {
         if (L < pl.L && chains * (d / 32) * (n + 6) <= 200 * n) pl.L = (int)L;
         pl.split = pl.L < T;
     }
-    pl.nseg = packed ? T / pl.L + num_seqs : num_seqs * ((T + pl.L - 1) / pl.L);
+    pl.nseg = packed ? T / pl.L + num_seqs : num_seqs * ((T - 1) / pl.L + 1);
     return pl;
 }
 

@@ -66,7 +66,7 @@ struct LaSegment {
 // cu_seqlens are clamped to the stream, so that a bad value cannot lead outside the tensors.
 __device__ __forceinline__ bool la_find_segment(const LaParams& p, int id, LaSegment* out) {
     if (p.cu == nullptr) {
-        const int per = (p.T + p.L - 1) / p.L;
+        const int per = (p.T - 1) / p.L + 1;
         const int doc = id / per;
         if (doc >= p.num_seqs) return false;
         out->doc = doc;
@@ -88,7 +88,7 @@ __device__ __forceinline__ bool la_find_segment(const LaParams& p, int id, LaSeg
         if (tid < 256 && n < p.num_seqs) {
             t0 = min(max(p.cu[n], 0), p.T);
             len = min(max(p.cu[n + 1], t0), p.T) - t0;
-            cnt = max(1, (len + p.L - 1) / p.L);
+            cnt = (max(len, 1) - 1) / p.L + 1;
         }
         int incl = cnt;
 #pragma unroll

@@ -418,8 +418,9 @@ int gdn_qsa_indexer(const void* q, const void* k, const float* g, const int32_t*
  * gdn_linear_attn_workspace_bytes -- device scratch of the four prompt calls (backward != 0 for the
  * gradients); num_seqs = 0: B dense sequences of T tokens; num_seqs >= 1: packed (B = 1).
  * Two calls that may overlap on the GPU need a workspace each.
- * Errors: GDN_ERR_INVALID_ARG (null or misaligned pointer, bad size, Hk not a divisor of H, 2^31 or
- * more tokens or (segment, head) pairs), GDN_ERR_UNSUPPORTED_SHAPE, GDN_ERR_WORKSPACE.
+ * Errors: GDN_ERR_INVALID_ARG (null or misaligned pointer, bad size, Hk not a divisor of H, about 2^31
+ * tokens or (64-token segment, head) pairs, 2^30 (document, head) pairs), GDN_ERR_UNSUPPORTED_SHAPE,
+ * GDN_ERR_WORKSPACE.
  */
 int gdn_linear_attn_workspace_bytes(int backward, int B, int T, int H, int Hk, int dk, int dv,
                                     int num_seqs, size_t* bytes);

@@ -206,3 +206,19 @@ def test_bindings_refuse_sizes_past_31_bits():
         api.gdn_add_rmsnorm_backward(big[None], w, big[None])
     with pytest.raises(ValueError, match="2\\^31"):
         api._documents(1, torch.zeros(1, dtype=torch.int32).expand((1 << 32) + 2), 0)
+
+
+def test_linear_attn_counts_up_to_31_bits(lib):
+    """2^30 (document, head) pairs and more are refused (a CTA's next pair is counted in 32 bits); sizes right below
+    the tokens' limit are formed without an overflow."""
+    n = ctypes.c_size_t(0)
+    f = lambda *a: lib.gdn_linear_attn_workspace_bytes(*a, ctypes.byref(n))
+    for call in (varlen, back_varlen):
+        assert call(lib, T=1, H=1 << 10, Hk=1, n=1 << 20) == BAD
+    for call in (dense, back):
+        assert call(lib, T=1, H=1 << 10, Hk=1, B=1 << 20) == BAD
+    assert f(0, 1, 1, 1 << 10, 1, 64, 64, 1 << 20) == BAD and f(0, 1, 1, 1 << 10, 1, 64, 64, (1 << 20) - 1) == 0
+    # one chain in as many pieces as the GPU has SMs
+    assert f(0, 1, 2 ** 31 - 65, 1, 1, 64, 64, 0) == 0 and n.value == 148 * 64 * 64 * 4
+    # 148 chains: none is cut
+    assert f(0, 1, 2 ** 23, 148, 148, 64, 64, 0) == 0 and n.value == 0
