@@ -141,6 +141,8 @@ la_tf_kernel(const LaParams p) {
         const float2 full = la_power2(g, p.L), last = la_power2(g, sg.doc_len - (sg.count - 1) * p.L);
         for (int b = 0; b < behind; ++b) {
             const int r = p.reverse ? sg.count - 1 - b : b;
+            // (offsets that fall and rise again make more segments than the grid: those have no local state)
+            if (sg.first_id + r >= (int)(gridDim.x / p.H)) continue;
             const float2 w = r == sg.count - 1 ? last : full;
             const float* loc = p.local + ((size_t)(sg.first_id + r) * p.H + h) * DD;
 #pragma unroll

@@ -351,3 +351,24 @@ def test_same_result_every_time_and_captured():
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(o1, ref)) and all(torch.equal(a, b) for a, b in zip(o2, ref2))
     assert api.gdn_read_device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_falling_offsets_stay_inside(dtype):
+    """Offsets that fall and rise again are not allowed (their results mean nothing) but lead nowhere outside the
+    tensors: three documents, the first and the last over the whole stream, have more segments than the stream's
+    length and the documents' number make room for.  The workspace is NaN where no pass has written it."""
+    T, H, d = 512, 1, 64
+    x = make([T], H, H, d, dtype, seed=11, decay="slow")
+    c = cuda(x)
+    cu = torch.tensor([0, T, 0, T], dtype=torch.int32, device="cuda")
+    s0, dsf = c["s0"].repeat(3, 1, 1, 1), c["ds_final"].repeat(3, 1, 1, 1)
+    n = api.gdn_linear_attn_workspace_bytes(1, T, H, H, d, d, 3, backward=True)
+    ws = torch.full((n // 4,), float("nan"), device="cuda")
+    y, sf = api.gdn_linear_attn_varlen(c["q"], c["k"], c["v"], c["log_decay"], cu, s0=s0, ws=ws)
+    ws.fill_(float("nan"))
+    g = api.gdn_linear_attn_backward_varlen(c["q"], c["k"], c["v"], c["log_decay"], cu, c["dy"], s0=s0, ds_final=dsf, ws=ws)
+    torch.cuda.synchronize()
+    assert api.gdn_read_device_status() == 0
+    for t in (y, *g.values()):
+        assert bool(torch.isfinite(t).all())
