@@ -57,6 +57,7 @@ int current_device_info(DeviceInfo* out) {
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool ok_ptr(const void* p) { return p != nullptr && aligned16(p); }
 bool ok_opt_ptr(const void* p) { return p == nullptr || aligned16(p); }
+bool ok_int_ptr(const int32_t* p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 int check_dims(int dk, int dv, int dtype) {
     if (dtype != GDN_BF16 && dtype != GDN_FP32) return GDN_ERR_INVALID_ARG;
@@ -521,7 +522,7 @@ static int attn_forward(const void* q, const void* k, const void* v, const float
                         int Hk, int dk, int dv, int dtype, float scale, void* ws, size_t ws_bytes, void* stream) {
     if (!ok_ptr(q) || !ok_ptr(k) || !ok_ptr(v) || !ok_ptr(y) || !ok_opt_ptr(s0) || !ok_opt_ptr(s_final))
         return GDN_ERR_INVALID_ARG;
-    if (num_seqs < 1 || T < 1 || (packed && cu_seqlens == nullptr)) return GDN_ERR_INVALID_ARG;
+    if (num_seqs < 1 || T < 1 || (packed && !ok_int_ptr(cu_seqlens))) return GDN_ERR_INVALID_ARG;
     if (s0 != nullptr && s0 == s_final) return GDN_ERR_INVALID_ARG;  // its end may be written before its start is read
     if (int rc = check_attn(log_decay, H, Hk, dk, dv, dtype)) return rc;
     if (!ok_tokens(num_seqs, T, H, packed)) return GDN_ERR_INVALID_ARG;
@@ -543,7 +544,7 @@ static int attn_backward(const void* q, const void* k, const void* v, const floa
     if (!ok_ptr(q) || !ok_ptr(k) || !ok_ptr(v) || !ok_ptr(dy) || !ok_ptr(dq) || !ok_ptr(dk_out) || !ok_ptr(dv_out) ||
         !ok_opt_ptr(s0) || !ok_opt_ptr(ds_final) || !ok_opt_ptr(ds0))
         return GDN_ERR_INVALID_ARG;
-    if (num_seqs < 1 || T < 1 || (packed && cu_seqlens == nullptr)) return GDN_ERR_INVALID_ARG;
+    if (num_seqs < 1 || T < 1 || (packed && !ok_int_ptr(cu_seqlens))) return GDN_ERR_INVALID_ARG;
     if (ds0 != nullptr && (ds0 == ds_final || ds0 == s0)) return GDN_ERR_INVALID_ARG;
     if (int rc = check_attn(log_decay, H, Hk, dk, dv, dtype)) return rc;
     if (!ok_tokens(num_seqs, T, H, packed)) return GDN_ERR_INVALID_ARG;
@@ -619,8 +620,7 @@ int gdn_rotary(const void* q, const void* k, void* q_out, void* k_out, const int
         return T == 0 ? aligned16(x) && aligned16(y) : ok_ptr(x) && ok_ptr(y);
     };
     if (!ok(q, q_out, Hq, ld_q, ld_q_out) || !ok(k, k_out, Hk, ld_k, ld_k_out)) return GDN_ERR_INVALID_ARG;
-    if (!ok_ptr(inv_freq) || (T > 0 && (positions == nullptr || (reinterpret_cast<uintptr_t>(positions) & 3u))))
-        return GDN_ERR_INVALID_ARG;
+    if (!ok_ptr(inv_freq) || (T > 0 && !ok_int_ptr(positions))) return GDN_ERR_INVALID_ARG;
     DeviceInfo dev;
     if (int rc = current_device_info(&dev)) return rc;
     gdn::RotaryArgs a{};

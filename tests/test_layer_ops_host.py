@@ -222,3 +222,8 @@ def test_linear_attn_counts_up_to_31_bits(lib):
     assert f(0, 1, 2 ** 31 - 65, 1, 1, 64, 64, 0) == 0 and n.value == 148 * 64 * 64 * 4
     # 148 chains: none is cut
     assert f(0, 1, 2 ** 23, 148, 148, 64, 64, 0) == 0 and n.value == 0
+
+
+def test_linear_attn_offsets_must_be_aligned(lib):
+    for call in (varlen, back_varlen):
+        assert call(lib, cu=A + 2) == BAD and call(lib, cu=A + 1) == BAD
