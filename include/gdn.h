@@ -404,7 +404,8 @@ int gdn_qsa_indexer(const void* q, const void* k, const float* g, const int32_t*
  * ([T, H, dk] tensors) of num_seqs documents; cu_seqlens as in gdn_prefill_varlen (empty documents
  * give s_final = s0).  Computed in 64-token chunks; where sequences and heads are few, long ones are
  * cut into pieces that run side by side, each from a start state that a first pass prepares in the
- * workspace.
+ * workspace.  Equal calls give equal bits.  Where the cuts fall depends on all lengths of a call, and
+ * with them a document's last bits; uncut bf16 documents do not depend on the others in any bit.
  * For bf16 the scores and the chunk-start states are rounded to bf16 as operands of the tensor cores;
  * sums and states are fp32 (s_final and ds0 are exact to fp32 rounding), fp32 inputs are computed in
  * fp32 throughout.

@@ -227,3 +227,26 @@ def test_linear_attn_counts_up_to_31_bits(lib):
 def test_linear_attn_offsets_must_be_aligned(lib):
     for call in (varlen, back_varlen):
         assert call(lib, cu=A + 2) == BAD and call(lib, cu=A + 1) == BAD
+
+
+def test_decay_factors_that_take_turns():
+    """The bf16 kernel's factors of a state, restated: over any run of chunks their product is within one step of the
+    exact power (2^-23, and the second order of many steps), where one float's drifts away."""
+    rng = np.random.default_rng(0)
+    g = np.concatenate([-np.exp2(rng.uniform(-22, -8, 200)), [-1e-9, -2.0 ** -30, 0.0, -0.5, -1.25]]).astype(np.float32)
+    left = np.arange(2048, 0, -1)
+    worst = drift = 0.0
+    for x in g:
+        e = np.exp(64.0 * np.float64(x))
+        hi = np.float32(e)
+        lo = np.float32(e - np.float64(hi))
+        nxt = (hi.view(np.int32) + np.int32(-1 if lo < 0 else 1)).view(np.float32)
+        rho = np.float32(lo / (nxt - hi)) * np.float32(-1 if lo < 0 else 1)
+        steps = np.rint(left.astype(np.float32) * rho).astype(np.int32) - np.rint((left - 1).astype(np.float32) * rho).astype(
+            np.int32)
+        f = (hi.view(np.int32) + steps).view(np.float32).astype(np.float64)
+        off = np.concatenate([[0.0], np.cumsum(np.log(f) - 64.0 * np.float64(x))])  # of the products, relative
+        worst = max(worst, off.max() - off.min())
+        drift = max(drift, 2048 * abs(np.log(np.float64(hi)) - 64.0 * np.float64(x)))
+    assert worst <= 2.0 ** -23 * 1.01, worst
+    assert drift >= 2.0 ** -15, drift

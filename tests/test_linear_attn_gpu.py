@@ -372,3 +372,83 @@ def test_falling_offsets_stay_inside(dtype):
     assert api.gdn_read_device_status() == 0
     for t in (y, *g.values()):
         assert bool(torch.isfinite(t).all())
+
+
+def far_decays(H):
+    """Decays of about 2^-14 a token whose e^{64 g} lies nearly half a step from its nearest float: in one float they
+    would be off by H 2^-25 and more after H chunks."""
+    g = []
+    for h in range(H):
+        x = np.float32(-(2.0 ** -14) * (1 + h / 3))
+        while True:
+            e = np.exp(64.0 * np.float64(x))
+            off = (e - np.float64(np.float32(e))) / np.spacing(np.float32(e))
+            if abs(off) > 0.45 and (off > 0) == (h % 2 == 0):
+                break
+            x = np.nextafter(x, np.float32(-1))
+        g.append(x)
+    return torch.tensor(np.array(g))
+
+
+def relative(got, ref):
+    return float(np.linalg.norm(got.double().cpu().numpy() - ref) / np.linalg.norm(ref))
+
+
+# What fp32 states and outputs may be off by, relative, as 2-norms.  In each of about 256 chunks that a state with this
+# decay remembers one rounding of it, 2^-24 / sqrt(3) in the root mean square: sixteen of them, 2^-20.8, where all are of
+# a value just above a power of two (2^-21.3 as they come); the chunk's own sums 2^-22 (products in parts, sums in the
+# tensor cores that are cut off below 2^-23).  A decay in one float, off by 0.45 2^-24 a chunk, would be off by 100 and
+# more chunks' worth: 2^-18.5.
+STATE_TOL = 2.0 ** -20
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 64), ("bf16", 128), ("fp32", 64)])
+@pytest.mark.parametrize("walk", ["cut", "in turn"])
+def test_states_keep_fp32_accuracy(dtype, d, walk):
+    """Long chains with weak decays, the last chunk short: cut into pieces, and uncut (more chains than SMs, so that
+    some start where their CTA has walked another one)."""
+    H, T, B = 3, 16411, 1 if walk == "cut" else 50
+    g = torch.Generator(device="cuda").manual_seed(d)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda")
+    q, k, v, dy = (r(B, T, H, d).to(DT[dtype]) for _ in range(4))
+    s0, dsf, ld = 8 * r(B, H, d, d), 8 * r(B, H, d, d), far_decays(H)
+    y, sf = api.gdn_linear_attn(q, k, v, ld.cuda(), s0=s0, scale=0.1)
+    out = api.gdn_linear_attn_backward(q, k, v, ld.cuda(), dy, s0=s0, ds_final=dsf, scale=0.1)
+    torch.cuda.synchronize()
+    assert api.gdn_read_device_status() == 0
+    for b in sorted({0, B // 2, B - 1}):
+        x = [t[b].cpu() for t in (q, k, v)]
+        yr, sr = oattn.forward(*x, ld, [0, T], s0=s0[b:b + 1].cpu(), scale=0.1)
+        gr = oattn.backward(*x, ld, [0, T], dy[b].cpu(), s0=s0[b:b + 1].cpu(), ds_final=dsf[b:b + 1].cpu(), scale=0.1)
+        err = {"s_final": relative(sf[b], sr[0]), "ds0": relative(out["ds0"][b], gr["ds0"][0])}
+        if dtype == "fp32":
+            err.update(y=relative(y[b], yr), **{n: relative(out[n][b], gr[n]) for n in ("dq", "dk", "dv")})
+        print(walk, dtype, d, b, err)
+        assert max(err.values()) <= STATE_TOL, err
+
+
+def test_documents_do_not_depend_on_each_other():
+    """bf16, uncut: a document gives the same bits alone and among 79 others, wherever its CTA stood before."""
+    rng = np.random.default_rng(4)
+    H, d = 4, 64
+    lens = [int(n) for n in rng.integers(0, 1000, 80)]
+    x = make(lens, H, 2, d, "bf16", seed=7, decay="slow")
+    x["log_decay"] = far_decays(H) * 16
+    c = cuda(x)
+    y, sf = api.gdn_linear_attn_varlen(c["q"], c["k"], c["v"], c["log_decay"], c["cu_seqlens"], s0=c["s0"], scale=0.25)
+    out = api.gdn_linear_attn_backward_varlen(c["q"], c["k"], c["v"], c["log_decay"], c["cu_seqlens"], c["dy"],
+                                              s0=c["s0"], ds_final=c["ds_final"], scale=0.25)
+    at = 0
+    for i, n in enumerate(lens):
+        if n == 0:
+            continue
+        one = {m: c[m][at:at + n].contiguous()[None] for m in ("q", "k", "v", "dy")}
+        s0, dsf = c["s0"][i:i + 1], c["ds_final"][i:i + 1]
+        y1, s1 = api.gdn_linear_attn(one["q"], one["k"], one["v"], c["log_decay"], s0=s0, scale=0.25)
+        o1 = api.gdn_linear_attn_backward(one["q"], one["k"], one["v"], c["log_decay"], one["dy"], s0=s0, ds_final=dsf,
+                                          scale=0.25)
+        assert torch.equal(y1[0], y[at:at + n]) and torch.equal(s1[0], sf[i]), (i, n)
+        assert all(torch.equal(o1[m][0], out[m][at:at + n]) for m in ("dq", "dk", "dv")), (i, n)
+        assert torch.equal(o1["ds0"][0], out["ds0"][i]), (i, n)
+        at += n
+    assert api.gdn_read_device_status() == 0
