@@ -780,7 +780,8 @@ def _documents(B, cu_seqlens, dev):
 def gdn_linear_attn_varlen(q, k, v, log_decay, cu_seqlens, s0=None, scale=1.0, y=None,
                            s_final=None, want_final=True, ws=None, stream=None):
     """gdn_linear_attn of packed documents: q [1,T,H,d] or [T,H,d] (k, v likewise), cu_seqlens
-    int32 [N+1] on the device, s0 [N,H,d,d] fp32 or None.  Returns (y like q, s_final)."""
+    int32 [N+1] on the device, s0 [N,H,d,d] fp32 or None.  Rows outside the documents are not written.
+    Returns (y like q, s_final)."""
     if stream is not None:
         return _on(stream, gdn_linear_attn_varlen, locals())
     if y is None:
@@ -855,7 +856,8 @@ def gdn_linear_attn_backward(q, k, v, log_decay, dy, s0=None, ds_final=None, sca
 def gdn_linear_attn_backward_varlen(q, k, v, log_decay, cu_seqlens, dy, s0=None, ds_final=None,
                                     scale=1.0, want_ds0=True, ws=None, stream=None):
     """Gradients of gdn_linear_attn_varlen given dy (like q) and ds_final [N,H,d,d].  Returns
-    dict dq, dk, dv (like q, k, v) and ds0 [N,H,d,d] (None unless want_ds0)."""
+    dict dq, dk, dv (like q, k, v; rows outside the documents are not written) and ds0 [N,H,d,d]
+    (None unless want_ds0)."""
     if stream is not None:
         return _on(stream, gdn_linear_attn_backward_varlen, locals())
     _want(dy, "dy", q.dtype, q.shape, q.get_device())

@@ -270,11 +270,18 @@ cudaError_t launch_f32(const LaParams& p, int nseg, int d, cudaStream_t st) {
 
 // ============================================================================ shared heads
 // dk and dv of a k / v head shared by `group` heads: the sum of the heads' parts, in fp32 and in
-// head order.  part [T, H, d] fp32 -> out [T, H / group, d].
+// head order.  part [T, H, d] fp32 -> out [T, H / group, d]; rows outside the documents have no parts and are left.
 template <typename T>
 __global__ void __launch_bounds__(256)
-la_group_sum_kernel(const float* __restrict__ part, T* __restrict__ out, size_t n4, int d4, int group) {
-    for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < n4; i += (size_t)gridDim.x * 256) {
+la_group_sum_kernel(const float* __restrict__ part, T* __restrict__ out, int tokens, int Hk, int d4, int group,
+                    const int32_t* __restrict__ cu, int num_seqs) {
+    int first = 0, last = tokens;
+    if (cu != nullptr) {
+        first = min(max(cu[0], 0), tokens);
+        last = min(max(cu[num_seqs], first), tokens);
+    }
+    const size_t n4 = (size_t)last * Hk * d4;
+    for (size_t i = (size_t)first * Hk * d4 + (size_t)blockIdx.x * 256 + threadIdx.x; i < n4; i += (size_t)gridDim.x * 256) {
         const size_t head = i / d4;
         const int x = (int)(i % d4);
         float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -286,14 +293,16 @@ la_group_sum_kernel(const float* __restrict__ part, T* __restrict__ out, size_t 
     }
 }
 
-cudaError_t launch_group_sum(const float* part, void* out, size_t tokens, int Hk, int d, int group, int dtype,
-                             cudaStream_t st) {
-    const size_t n4 = tokens * Hk * (d / 4);
+cudaError_t launch_group_sum(const float* part, void* out, const LaArgs& a, cudaStream_t st) {
+    const int tokens = a.cu_seqlens ? a.T : a.num_seqs * a.T, group = a.H / a.Hk, d4 = a.d / 4;
+    const size_t n4 = (size_t)tokens * a.Hk * d4;
     const unsigned grid = (unsigned)min((n4 + 255) / 256, (size_t)148 * 16);
-    if (dtype == GDN_BF16)
-        la_group_sum_kernel<<<grid, 256, 0, st>>>(part, static_cast<__nv_bfloat16*>(out), n4, d / 4, group);
+    if (a.dtype == GDN_BF16)
+        la_group_sum_kernel<<<grid, 256, 0, st>>>(part, static_cast<__nv_bfloat16*>(out), tokens, a.Hk, d4, group,
+                                                  a.cu_seqlens, a.num_seqs);
     else
-        la_group_sum_kernel<<<grid, 256, 0, st>>>(part, static_cast<float*>(out), n4, d / 4, group);
+        la_group_sum_kernel<<<grid, 256, 0, st>>>(part, static_cast<float*>(out), tokens, a.Hk, d4, group, a.cu_seqlens,
+                                                  a.num_seqs);
     return cudaGetLastError();
 }
 
@@ -497,9 +506,8 @@ cudaError_t launch_linear_attn(const LaArgs& a, cudaStream_t st) {
     p.state_t = 1;
     if ((e = run(false)) != cudaSuccess) return e;
     if (group > 1) {
-        const size_t tokens = packed ? (size_t)a.T : (size_t)a.num_seqs * a.T;
-        if ((e = launch_group_sum(part_k, a.dk_out, tokens, a.Hk, a.d, group, a.dtype, st)) != cudaSuccess) return e;
-        return launch_group_sum(part_v, a.dv_out, tokens, a.Hk, a.d, group, a.dtype, st);
+        if ((e = launch_group_sum(part_k, a.dk_out, a, st)) != cudaSuccess) return e;
+        return launch_group_sum(part_v, a.dv_out, a, st);
     }
     return cudaSuccess;
 }

@@ -402,7 +402,8 @@ int gdn_qsa_indexer(const void* q, const void* k, const float* g, const int32_t*
  *
  * gdn_linear_attn -- B dense sequences of T tokens.  gdn_linear_attn_varlen -- one packed stream
  * ([T, H, dk] tensors) of num_seqs documents; cu_seqlens as in gdn_prefill_varlen (empty documents
- * give s_final = s0).  Computed in 64-token chunks; where sequences and heads are few, long ones are
+ * give s_final = s0), but the last document may end before T: rows outside the documents are neither
+ * used nor written, in any of the packed calls.  Computed in 64-token chunks; where sequences and heads are few, long ones are
  * cut into pieces that run side by side, each from a start state that a first pass prepares in the
  * workspace.  Equal calls give equal bits.  Where the cuts fall depends on all lengths of a call, and
  * with them a document's last bits; uncut bf16 documents do not depend on the others in any bit.

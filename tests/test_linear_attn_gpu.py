@@ -15,7 +15,7 @@ import pytest
 import torch
 
 import oracle.linear_attn as oattn
-from gated_deltanet_linear_eqs_b200 import api
+from gated_deltanet_linear_eqs_b200 import _abi, api
 from gated_deltanet_linear_eqs_b200.inputs import cu_seqlens_from
 
 pytestmark = pytest.mark.gpu
@@ -452,3 +452,38 @@ def test_documents_do_not_depend_on_each_other():
         assert torch.equal(o1["ds0"][0], out["ds0"][i]), (i, n)
         at += n
     assert api.gdn_read_device_status() == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("H,Hk", [(4, 1), (4, 2), (2, 2)])
+@pytest.mark.parametrize("lens", [[70, 0, 100], [1500, 65]], ids=["short", "long"])
+def test_rows_outside_the_documents_are_left(lens, H, Hk, dtype):
+    """A stream that is longer than its documents (a padded batch, its rows NaN): outputs and gradients behind the last
+    document keep what they held, shared heads or not, and the others are those of the stream without them."""
+    d, T, more = 64, sum(lens), 77
+    x = make(lens, H, Hk, d, dtype, seed=T + Hk, decay="slow")
+    c = cuda(x)
+    N = len(lens)
+    want = [api.gdn_linear_attn_varlen(c["q"], c["k"], c["v"], c["log_decay"], c["cu_seqlens"], s0=c["s0"])[0]]
+    g = api.gdn_linear_attn_backward_varlen(c["q"], c["k"], c["v"], c["log_decay"], c["cu_seqlens"], c["dy"], s0=c["s0"])
+    want += [g["dq"], g["dk"], g["dv"]]
+    p = {n: torch.cat([c[n], torch.full_like(c[n][:more], float("nan"))]) for n in ("q", "k", "v", "dy")}
+    out = [torch.full((T + more, h, d), 7.0, dtype=DT[dtype], device="cuda") for h in (H, H, Hk, Hk)]
+    ds0 = torch.empty_like(c["s0"])
+    n = api.gdn_linear_attn_workspace_bytes(1, T + more, H, Hk, d, d, N, backward=True)
+    ws = torch.full((n // 4 + 4,), float("nan"), device="cuda")
+    api.gdn_linear_attn_varlen(p["q"], p["k"], p["v"], c["log_decay"], c["cu_seqlens"], s0=c["s0"], y=out[0], ws=ws)
+    rc = _abi.load().gdn_linear_attn_backward_varlen(
+        *(p[n].data_ptr() for n in "qkv"), c["log_decay"].data_ptr(), c["cu_seqlens"].data_ptr(), N, c["s0"].data_ptr(),
+        p["dy"].data_ptr(), None, *(t.data_ptr() for t in out[1:]), ds0.data_ptr(), T + more, H, Hk, d, d,
+        _abi.GDN_BF16 if dtype == "bf16" else _abi.GDN_FP32, 1.0, ws.data_ptr(), ws.numel() * 4,
+        torch.cuda.current_stream().cuda_stream)
+    torch.cuda.synchronize()
+    assert rc == 0 and api.gdn_read_device_status() == 0
+    for a, b in zip(out, want):
+        assert bool((a[T:] == 7.0).all())
+        # the cuts may fall elsewhere: two results, each off by two bf16 roundings (2^-8.7 in the root mean square, most of
+        # it alike), or by 2^-20
+        rel = float((a[:T].double() - b.double()).norm() / b.double().norm())
+        assert rel <= (2.0 ** -8 if dtype == "bf16" else 2.0 ** -19), rel
+    assert bool(torch.isfinite(ds0).all())
