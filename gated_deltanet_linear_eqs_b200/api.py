@@ -1001,7 +1001,7 @@ def _like(t, name, x, make):
 def gdn_add_rmsnorm(x, residual, w, eps=1e-6, o=None, h=None, stream=None):
     """h = x + residual, o = (1 + w) h / sqrt(mean(h^2) + eps) over the last axis: x, residual
     [..., C] (bf16 or fp32; residual None: h = x and is not written), w [C] fp32.  h may be x or
-    residual, o may be x.  Returns (o, h)."""
+    residual, o may be x.  Returns (o, h), and h = None where o is x and nothing else holds h."""
     if stream is not None:
         return _on(stream, gdn_add_rmsnorm, locals())
     dt, dev, shape, C, rows = _rows(x, w, "x")
@@ -1015,7 +1015,9 @@ def gdn_add_rmsnorm(x, residual, w, eps=1e-6, o=None, h=None, stream=None):
     rc = f(*a) if dev == _current_device() else _launch(dev, f, a)
     if rc:
         _check(rc, "gdn_add_rmsnorm")
-    return o, x if h is None else h
+    if h is None and o.data_ptr() != x.data_ptr():
+        h = x
+    return o, h
 
 
 def gdn_add_rmsnorm_fp8(x, residual, w, eps=1e-6, group=0, o=None, scales=None, h=None,

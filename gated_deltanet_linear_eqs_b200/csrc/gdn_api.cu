@@ -682,6 +682,7 @@ int gdn_add_rmsnorm(const void* x, const void* residual, const float* w, void* o
     if (int rc = check_add_norm(w, rows, C, dtype, eps)) return rc;
     const auto ok = [rows](const void* p) { return rows == 0 ? aligned16(p) : ok_ptr(p); };
     if (!ok(x) || !ok(o) || !ok_opt_ptr(residual) || !ok_opt_ptr(h)) return GDN_ERR_INVALID_ARG;
+    if (o != nullptr && o == h) return GDN_ERR_INVALID_ARG;  // one buffer for two outputs
     DeviceInfo dev;
     if (int rc = current_device_info(&dev)) return rc;
     gdn::AddNormArgs a{};
@@ -697,6 +698,9 @@ int gdn_add_rmsnorm_fp8(const void* x, const void* residual, const float* w, voi
     const auto ok = [rows](const void* p) { return rows == 0 ? aligned16(p) : ok_ptr(p); };
     if (!ok(x) || !ok(o8) || !ok(scales) || !ok_opt_ptr(residual) || !ok_opt_ptr(h)) return GDN_ERR_INVALID_ARG;
     if (rows == 0) return GDN_OK;
+    // rows of o8 and of the scales lie elsewhere than x's, residual's and h's: other rows' blocks may still read those
+    for (const void* p : {x, residual, static_cast<const void*>(h)})
+        if (p == o8 || p == scales || o8 == scales) return GDN_ERR_INVALID_ARG;
     DeviceInfo dev;
     if (int rc = current_device_info(&dev)) return rc;
     gdn::AddNormArgs a{};

@@ -495,12 +495,13 @@ int gdn_rotary_inv_freq(int rotary_dim, double base, int scaling, double factor,
  * over rows of C values (zero-centred gain, as in gdn_gated_rmsnorm).  The sum is taken in fp32 and
  * the norm is of that sum; h, in dtype, is its rounding.
  *   x, residual, o, h [rows, C] in dtype (bf16 or fp32); w [C] fp32; residual NULL: h = x; h NULL: not
- *   written.  h may be x or residual (in place); o may be x.  C a multiple of 8 in 8..16384.
+ *   written.  h may be x or residual (in place); o may be x, but not h.  C a multiple of 8 in 8..16384.
  *   0 <= rows < 2^31.
  * gdn_add_rmsnorm_fp8 -- the same with an 8-bit o8 [rows, C] (e4m3) for an 8-bit product, and
  *   scales [rows, C / group] fp32: scale = max |o| / 448 over each group of columns and
  *   o8 = e4m3(o / scale), from the fp32 o; group = C (one scale a row) or 128 (C a multiple of 128).
- *   A group of zeros has scale 0; a NaN makes its group's scale and values NaN.
+ *   A group of zeros has scale 0; a NaN makes its group's scale and values NaN.  o8 and scales may be
+ *   none of the other tensors.
  * gdn_add_rmsnorm_backward -- from the stored h: dx = dL/dh [rows, C] in dtype, the gradient of
  *   both x and residual, given d_o and d_h (the gradient that reaches h itself; NULL = 0), and dw
  *   [C] fp32, summed over the rows in a fixed order.  ws/ws_bytes:

@@ -166,3 +166,20 @@ def test_no_rows_and_graph():
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(got["dx"], want["dx"]) and torch.equal(got["dw"], want["dw"])
+
+
+def test_in_place_without_a_residual_keeps_no_h():
+    """h = x is overwritten by o: the caller is not given o for it."""
+    x = make(5, 256, "bf16", seed=2)["x"].cuda()
+    w = torch.randn(256, device="cuda")
+    want, h = api.gdn_add_rmsnorm(x, None, w)
+    assert h is x
+    kept = torch.empty_like(x)
+    xx = x.clone()
+    o, h = api.gdn_add_rmsnorm(xx, None, w, o=xx)
+    assert o is xx and h is None and torch.equal(o, want)
+    xx = x.clone()
+    o, h = api.gdn_add_rmsnorm(xx, None, w, o=xx, h=kept)
+    assert o is xx and h is kept and torch.equal(h, x) and torch.equal(o, want)
+    with pytest.raises(api.GdnError):
+        api.gdn_add_rmsnorm(x, x, w, o=x, h=x)

@@ -250,3 +250,15 @@ def test_decay_factors_that_take_turns():
         drift = max(drift, 2048 * abs(np.log(np.float64(hi)) - 64.0 * np.float64(x)))
     assert worst <= 2.0 ** -23 * 1.01, worst
     assert drift >= 2.0 ** -15, drift
+
+
+def test_add_norm_outputs_that_share_memory_are_refused(lib):
+    """o and h in one buffer: one of them would be lost.  8-bit rows and scales lie elsewhere than the rows that other
+    blocks still read."""
+    fwd = lambda **kw: lib.gdn_add_rmsnorm(*{**dict(x=A, r=2 * A, w=3 * A, o=4 * A, h=5 * A, rows=10, C=256, dt=0, eps=1e-6),
+                                             **kw}.values(), None)
+    q = lambda **kw: lib.gdn_add_rmsnorm_fp8(*{**dict(x=A, r=2 * A, w=3 * A, o=4 * A, s=6 * A, h=5 * A, rows=10, C=256, g=128,
+                                                      dt=0, eps=1e-6), **kw}.values(), None)
+    assert fwd(o=A, h=A) == BAD and fwd(o=5 * A) == BAD and fwd(x=0, r=0, o=0, h=0, rows=0) not in (BAD, SHAPE)
+    for same in (dict(o=A), dict(o=2 * A), dict(o=5 * A), dict(s=A), dict(s=2 * A), dict(s=5 * A), dict(s=4 * A)):
+        assert q(**same) == BAD
