@@ -653,14 +653,13 @@ int gdn_rotary_inv_freq(int rotary_dim, double base, int scaling, double factor,
         hi = ceil(pair_of(beta_slow));
         lo = lo < 0.0 ? 0.0 : lo;
         hi = hi > rotary_dim - 1.0 ? rotary_dim - 1.0 : hi;
-        if (hi <= lo) hi = lo + 0.001;
     }
     for (int i = 0; i < half; ++i) {
         double f = pow(base, -2.0 * i / rotary_dim);
         if (scaling == GDN_ROTARY_LINEAR) f /= factor;
         if (scaling == GDN_ROTARY_YARN) {
-            double slow = (i - lo) / (hi - lo);
-            slow = slow < 0.0 ? 0.0 : slow > 1.0 ? 1.0 : slow;
+            // (hi <= lo: every pair is slow, with hi at 0 or below, or none is, with lo past the last)
+            const double slow = i >= hi ? 1.0 : i <= lo ? 0.0 : (i - lo) / (hi - lo);
             f = f / factor * slow + f * (1.0 - slow);
         }
         inv_freq[i] = (float)f;

@@ -471,7 +471,8 @@ int gdn_linear_attn_backward_varlen(const void* q, const void* k, const void* v,
  *   base * factor^(rotary_dim / (rotary_dim - 2)) for GDN_ROTARY_NTK; and for GDN_ROTARY_YARN divided by
  *   factor for pairs that make fewer than beta_slow turns within original_context positions, kept
  *   for those that make more than beta_fast, with a linear ramp over the pair index between
- *   (whole pair indices).  *scale receives 0.1 ln(factor) + 1 for YARN and 1 otherwise: gdn_rotary's scale.
+ *   (whole pair indices, between 0 and rotary_dim - 1).  *scale receives 0.1 ln(factor) + 1 for YARN and
+ *   1 otherwise: gdn_rotary's scale.
  */
 typedef enum {
     GDN_ROTARY_PLAIN = 0,

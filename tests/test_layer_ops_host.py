@@ -262,3 +262,14 @@ def test_add_norm_outputs_that_share_memory_are_refused(lib):
     assert fwd(o=A, h=A) == BAD and fwd(o=5 * A) == BAD and fwd(x=0, r=0, o=0, h=0, rows=0) not in (BAD, SHAPE)
     for same in (dict(o=A), dict(o=2 * A), dict(o=5 * A), dict(s=A), dict(s=2 * A), dict(s=5 * A), dict(s=4 * A)):
         assert q(**same) == BAD
+
+
+def test_yarn_where_all_pairs_are_slow_or_fast(lib):
+    """A context in which no pair makes beta_slow turns: all are divided by the factor, the first one,
+    too; one in which all make more than beta_fast: none is."""
+    plain = api.gdn_rotary_inv_freq(64, base=1e4)[0].double().numpy()
+    for kw in (dict(original_context=4), dict(original_context=100, beta_fast=64.0, beta_slow=16.0)):
+        y, _ = api.gdn_rotary_inv_freq(64, base=1e4, scaling="yarn", factor=8, **kw)
+        np.testing.assert_allclose(y.double().numpy(), plain / 8, rtol=2.0 ** -23)
+    y, _ = api.gdn_rotary_inv_freq(64, base=1e4, scaling="yarn", factor=8, original_context=10 ** 9)
+    np.testing.assert_allclose(y.double().numpy(), plain, rtol=2.0 ** -23)
