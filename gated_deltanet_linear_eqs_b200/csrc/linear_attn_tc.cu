@@ -131,26 +131,6 @@ __device__ __forceinline__ float decay_of(float2 d, int left) {
                           __float2int_rn((float)(left - 1) * d.y));
 }
 
-// A wait of a whole warp for a phase, bounded: one that gives up leaves the barrier's number + 1 in *abort, which
-// ends the others' waits, too.  All lanes poll together and vote: a lane that polled alone would split the warp
-// while it is held, and the warp-collective instructions behind the wait (ldmatrix, whose lanes give each
-// other's addresses) would then fault.
-__device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, volatile int* abort, int id) {
-    constexpr uint32_t ALL = 0xffffffffu;
-    if (__all_sync(ALL, mbar_try_wait(bar, parity))) return true;
-    const long long c0 = clock64();
-    for (;;) {
-#pragma unroll 1
-        for (int i = 0; i < 64; ++i)
-            if (__all_sync(ALL, mbar_try_wait(bar, parity))) return true;
-        if (__any_sync(ALL, *abort != 0)) return false;
-        if (__any_sync(ALL, clock64() - c0 > 4000000000ll)) {  // two seconds
-            *abort = id + 1;
-            return false;
-        }
-    }
-}
-
 // MODE: what a pass writes
 enum { M_OUT = 0, M_STATE = 1, M_OUT_F32 = 2 };
 

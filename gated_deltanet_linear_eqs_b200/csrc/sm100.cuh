@@ -125,6 +125,27 @@ __device__ __forceinline__ bool mbar_spin_warp(uint64_t* bar, uint32_t parity,
     return __all_sync(0xffffffffu, ok);
 }
 
+// A wait of a whole warp for a phase, bounded (two seconds at 2 GHz): one that gives up leaves id + 1 in *abort,
+// which ends the others' waits, too (a later one after its first poll).  All lanes poll together and vote: a lane that
+// polled alone would split the warp while it is held, and the warp-collective instructions behind the wait (ldmatrix,
+// whose lanes give each other's addresses) would then fault.
+__device__ __forceinline__ bool wait_all(uint64_t* bar, uint32_t parity, volatile int* abort, int id,
+                                         long long limit_cycles = 4000000000ll) {
+    constexpr uint32_t ALL = 0xffffffffu;
+    if (__all_sync(ALL, mbar_try_wait(bar, parity))) return true;
+    const long long c0 = clock64();
+    for (;;) {
+        if (__any_sync(ALL, *abort != 0)) return false;
+#pragma unroll 1
+        for (int i = 0; i < 64; ++i)
+            if (__all_sync(ALL, mbar_try_wait(bar, parity))) return true;
+        if (__any_sync(ALL, clock64() - c0 > limit_cycles)) {
+            *abort = id + 1;
+            return false;
+        }
+    }
+}
+
 // ------------------------------------------------------------------------------ fences
 __device__ __forceinline__ void fence_proxy_async_smem() {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");

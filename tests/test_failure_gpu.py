@@ -34,3 +34,17 @@ def test_bounded_wait_reports_timeout_and_device_stays_usable():
     yr, sr = oracle.forward(inp["q"], inp["k"], inp["v"], inp["alpha"], inp["beta"], inp["s0"])
     assert max_rel(y, yr) <= Y_TOL and frob_rel(sf, sr) <= S_TOL
     assert api.gdn_read_device_status(reset=False) == 0
+
+
+def test_waits_of_whole_warps_end_together():
+    """One warp's wait runs out after 1 ms; two others, whose own limit is two seconds, end with it, a hundred waits in a
+    row, and meet at a named barrier (the status is recorded only then)."""
+    api.gdn_read_device_status(reset=True)
+    for _ in range(3):
+        t0 = time.perf_counter()
+        api.gdn_selftest_wait_timeout(1_000_000)
+        torch.cuda.synchronize()
+        elapsed = time.perf_counter() - t0
+        assert api.gdn_read_device_status(reset=True) == GDN_ERR_TIMEOUT
+    print(f"{elapsed * 1e3:.2f} ms")
+    assert elapsed < 1.0
