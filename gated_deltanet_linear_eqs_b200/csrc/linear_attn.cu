@@ -14,7 +14,8 @@ namespace {
 // of computing the scores in each.
 //
 // A product of fp32 values x y is taken as xh yh + xh yl + xl yh, x = xh + xl with xh = x rounded to tf32's 11
-// bits: what is left out is 2^-22 of |x y|, against 2^-24 for a fused multiply-add, and the sums stay fp32.
+// bits (Markidis et al. 2018, Ootomo and Yokota 2022): what is left out is 2^-22 of |x y|, against 2^-24 for a fused
+// multiply-add, and the sums stay fp32.
 // Tiles of a chunk (Q, K, V rows with padded strides, so that fragments are read without bank conflicts) come
 // by asynchronous copies into two buffers, the next chunk's while this one is computed; the state is kept in
 // fragments (registers) and copied to shared memory as the operand of Q S.
@@ -34,7 +35,8 @@ struct LaTf {
 };
 
 __device__ __forceinline__ void tf_split(float x, uint32_t& hi, uint32_t& lo) {
-    hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;  // to nearest, ties away (a NaN stays one in lo)
+    // to nearest, ties away (a NaN stays one in lo; within 2^-12 of the largest float hi is infinite)
+    hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
     lo = __float_as_uint(x - __uint_as_float(hi));
 }
 __device__ __forceinline__ void tf_mma(float* c, const uint32_t* a, const uint32_t* b) {

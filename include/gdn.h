@@ -398,7 +398,9 @@ int gdn_qsa_indexer(const void* q, const void* k, const float* g, const int32_t*
  *   s0, s_final, ds_final, ds0: [B or num_seqs, H, dk, dv] fp32, with H states (the heads' decays
  *   differ even where k and v are shared).  s0 / ds_final NULL = 0; s_final / ds0 NULL = not written.
  *   Inputs must be finite: a value that is not makes its whole 64-token chunk, and what follows in
- *   its document and head, non-finite.  Other documents and heads are not touched by it.
+ *   its document and head, non-finite.  Other documents and heads are not touched by it.  fp32 inputs
+ *   must be below 2^127 in magnitude (the prompt calls: a high part may round up to infinity within 2^-12 of
+ *   the largest float), as must the products of k and v that a state holds.
  *
  * gdn_linear_attn -- B dense sequences of T tokens.  gdn_linear_attn_varlen -- one packed stream
  * ([T, H, dk] tensors) of num_seqs documents; cu_seqlens as in gdn_prefill_varlen (empty documents
@@ -407,9 +409,12 @@ int gdn_qsa_indexer(const void* q, const void* k, const float* g, const int32_t*
  * cut into pieces that run side by side, each from a start state that a first pass prepares in the
  * workspace.  Equal calls give equal bits.  Where the cuts fall depends on all lengths of a call, and
  * with them a document's last bits; uncut bf16 documents do not depend on the others in any bit.
- * For bf16 the scores and the chunk-start states are rounded to bf16 as operands of the tensor cores;
- * sums and states are fp32 (s_final and ds0 are exact to fp32 rounding), fp32 inputs are computed in
- * fp32 throughout.
+ * Precision: sums, states and decays are fp32.  bf16: the scores and the chunk-start states are
+ * rounded to bf16 once, as operands of the tensor cores (y, dq, dk and dv are off by 2.4e-3 of their
+ * 2-norm, 1.7e-3 of it their own rounding); what enters the states is not, and s_final and ds0 are off
+ * by 2e-7 to 4e-7.  fp32: a product of two values is three of their tf32 parts (the high one to 11 bits,
+ * the low one the rest); the low parts' product is left out, 2^-22 of a product at most, and all outputs
+ * and states are off by 2e-7 to 4e-7.  The single-token call is fp32 throughout.
  * gdn_linear_attn_decode_step -- one token for each of N sequences: q, y [N, H, dk], k, v
  * [N, Hk, dk]; state [N, H, dk, dv] fp32 is read once and updated in place.
  * gdn_linear_attn_backward, _varlen -- gradients of L(y, s_final) given dy and ds_final: dq like q,
@@ -494,7 +499,8 @@ int gdn_rotary_inv_freq(int rotary_dim, double base, int scaling, double factor,
  *     h = x + residual          o = (1 + w) * h / sqrt(mean(h^2) + eps)
  *
  * over rows of C values (zero-centred gain, as in gdn_gated_rmsnorm).  The sum is taken in fp32 and
- * the norm is of that sum; h, in dtype, is its rounding.
+ * the norm is of that sum; h, in dtype, is its rounding.  The sum of squares is fp32, too: a row that
+ * passes its range (values around 1e19) has the norm infinity.
  *   x, residual, o, h [rows, C] in dtype (bf16 or fp32); w [C] fp32; residual NULL: h = x; h NULL: not
  *   written.  h may be x or residual (in place); o may be x, but not h.  C a multiple of 8 in 8..16384.
  *   0 <= rows < 2^31.

@@ -487,3 +487,19 @@ def test_rows_outside_the_documents_are_left(lens, H, Hk, dtype):
         rel = float((a[:T].double() - b.double()).norm() / b.double().norm())
         assert rel <= (2.0 ** -8 if dtype == "bf16" else 2.0 ** -19), rel
     assert bool(torch.isfinite(ds0).all())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_scaled_inputs_give_the_same_bits(dtype):
+    """Powers of two are exact in every product, part and sum: k times 2^-100 with v times 2^100 is the same call."""
+    x = make([200, 65], 2, 1, 128, dtype, seed=12, decay="slow")
+    c = cuda(x)
+    z = {**c, "k": c["k"] * 2.0 ** -100, "v": c["v"] * 2.0 ** 100}
+    f = lambda a: api.gdn_linear_attn_varlen(a["q"], a["k"], a["v"], a["log_decay"], a["cu_seqlens"], s0=a["s0"], scale=0.1)
+    g = lambda a: api.gdn_linear_attn_backward_varlen(a["q"], a["k"], a["v"], a["log_decay"], a["cu_seqlens"], a["dy"],
+                                                      s0=a["s0"], scale=0.1)
+    for a, b in zip(f(c), f(z)):
+        assert torch.equal(a, b)
+    a, b = g(c), g(z)
+    assert torch.equal(a["dq"], b["dq"]) and torch.equal(a["ds0"], b["ds0"])
+    assert torch.equal(a["dk"] * 2.0 ** 100, b["dk"]) and torch.equal(a["dv"] * 2.0 ** -100, b["dv"])
