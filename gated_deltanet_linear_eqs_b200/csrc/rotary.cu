@@ -7,7 +7,8 @@
 //
 // Angles: f_i / (2 pi) is taken to 64 bits after the point of a turn, so that p f_i / (2 pi) modulo one
 // turn is the low word of an integer product: no error grows with the position beyond the 2^-53 of the
-// frequency itself, and no 64-bit float is touched per token.
+// frequency itself, and up to r = 128 no 64-bit float is touched per token (a lane keeps two frequencies; those
+// of wider heads are converted at every token).
 //
 // A warp serves a token at a time.  Its lanes compute the r / 2 (cos, sin) into shared memory (each lane
 // keeps its frequencies), then turn all heads of q and k with them, 16 bytes of both halves of the pairs a
