@@ -620,6 +620,8 @@ int gdn_rotary(const void* q, const void* k, void* q_out, void* k_out, const int
         return T == 0 ? aligned16(x) && aligned16(y) : ok_ptr(x) && ok_ptr(y);
     };
     if (!ok(q, q_out, Hq, ld_q, ld_q_out) || !ok(k, k_out, Hk, ld_k, ld_k_out)) return GDN_ERR_INVALID_ARG;
+    // one tensor's output in the other's place: either may be read or written first
+    if (Hk > 0 && q_out != nullptr && (q_out == k_out || q_out == k || k_out == q)) return GDN_ERR_INVALID_ARG;
     if (!ok_ptr(inv_freq) || (T > 0 && !ok_int_ptr(positions))) return GDN_ERR_INVALID_ARG;
     DeviceInfo dev;
     if (int rc = current_device_info(&dev)) return rc;

@@ -465,7 +465,7 @@ int gdn_linear_attn_backward_varlen(const void* q, const void* k, const void* v,
  *   q [T, Hq, d], k [T, Hk, d] in dtype; a token's heads are contiguous and tokens are ld_* elements
  *   apart (ld >= heads * d and a multiple of 8; heads * d < 2^31), so that q and k may be parts of
  *   one projection's output.  q_out / k_out likewise; each may be its input (same pointer, same ld: in place), and
- *   must not overlap it otherwise.
+ *   must not overlap it otherwise, nor the other's input or output.
  *   positions [T] int32 and inv_freq [rotary_dim / 2] fp32 on the device.  Hk = 0: k and k_out
  *   may be NULL.  T >= 0.
  * Errors: GDN_ERR_INVALID_ARG (null or misaligned pointer, bad size or ld), GDN_ERR_UNSUPPORTED_SHAPE

@@ -273,3 +273,54 @@ def test_yarn_where_all_pairs_are_slow_or_fast(lib):
         np.testing.assert_allclose(y.double().numpy(), plain / 8, rtol=2.0 ** -23)
     y, _ = api.gdn_rotary_inv_freq(64, base=1e4, scaling="yarn", factor=8, original_context=10 ** 9)
     np.testing.assert_allclose(y.double().numpy(), plain, rtol=2.0 ** -23)
+
+
+def test_rotary_outputs_in_the_others_place_are_refused(lib):
+    def call(q=A, k=2 * A, qo=3 * A, ko=4 * A, Hk=2, T=10):
+        return lib.gdn_rotary(q, k, qo, ko, A, A, T, 2, Hk, 64, 32, 128, 128, 128, 128, 0, 0, 1.0, 0, None)
+    assert call(qo=4 * A) == BAD and call(qo=2 * A) == BAD and call(ko=A) == BAD and call(k=A, qo=A, ko=A) == BAD
+    assert call(T=0) not in (BAD, SHAPE) and call(k=0, qo=A, ko=A, Hk=0, T=0) != BAD  # (no tokens: nothing is launched)
+    assert call(q=0, k=0, qo=0, ko=0, T=0) != BAD and call(qo=4 * A, T=0) == BAD
+
+
+def test_refusals_with_tensors_apart(lib):
+    """Every refusal on its own, with a buffer for each tensor.  The calls that are not refused have no rows or tokens, so
+    that none launches anything."""
+    no = (BAD, SHAPE, WS)
+
+    def rotary(**kw):
+        a = dict(q=A, k=2 * A, qo=3 * A, ko=4 * A, p=5 * A, f=6 * A, T=10, Hq=4, Hk=2, d=64, r=32, lq=256, lk=128, lqo=256,
+                 lko=128, il=0, inv=0, scale=1.0, dt=0)
+        a.update(kw)
+        return lib.gdn_rotary(*a.values(), None)
+    assert rotary(T=0) not in no and rotary(qo=A, ko=2 * A, T=0) not in no and rotary(k=A, T=0) not in no
+    for kw in (dict(q=0), dict(qo=3 * A + 8), dict(k=0), dict(ko=0), dict(p=0), dict(p=A + 2), dict(f=0), dict(T=-1), dict(Hq=0),
+               dict(Hk=-1), dict(dt=3), dict(lq=248), dict(lk=132), dict(qo=A, lqo=264)):
+        assert rotary(**kw) == BAD, kw
+
+    def fwd(**kw):
+        a = dict(x=A, r=2 * A, w=3 * A, o=4 * A, h=5 * A, rows=10, C=256, dt=0, eps=1e-6)
+        a.update(kw)
+        return lib.gdn_add_rmsnorm(*a.values(), None)
+
+    def fp8(**kw):
+        a = dict(x=A, r=2 * A, w=3 * A, o=4 * A, s=6 * A, h=5 * A, rows=10, C=256, g=128, dt=0, eps=1e-6)
+        a.update(kw)
+        return lib.gdn_add_rmsnorm_fp8(*a.values(), None)
+
+    def back(**kw):
+        a = dict(h=A, w=2 * A, do=3 * A, dh=0, dx=4 * A, dw=5 * A, rows=10, C=256, dt=0, eps=1e-6, ws=6 * A, wsb=1 << 30)
+        a.update(kw)
+        return lib.gdn_add_rmsnorm_backward(*a.values(), None)
+    for kw in ({}, dict(o=A), dict(h=A), dict(h=2 * A), dict(r=0, h=0)):
+        assert fwd(rows=0, **kw) not in no
+    assert fp8(rows=0) == 0 and back(ws=0) == WS and back(ws=0, dx=3 * A) == WS
+    for f in (fwd, fp8, back):
+        for kw in (dict(w=0), dict(rows=-1), dict(rows=1 << 31), dict(eps=-1.0), dict(eps=float("nan")), dict(dt=4)):
+            assert f(**kw) == BAD, kw
+        for C in (4, 252, 16392):
+            assert f(C=C) == SHAPE
+    for f in (fwd, fp8):
+        for kw in (dict(x=0), dict(o=4 * A + 8), dict(r=A + 2), dict(h=A + 8)):
+            assert f(**kw) == BAD, kw
+    assert fp8(s=0) == BAD and fp8(g=64) == BAD and fp8(C=264) == SHAPE
