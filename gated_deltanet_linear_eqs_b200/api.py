@@ -1015,7 +1015,7 @@ def gdn_add_rmsnorm(x, residual, w, eps=1e-6, o=None, h=None, stream=None):
     rc = f(*a) if dev == _current_device() else _launch(dev, f, a)
     if rc:
         _check(rc, "gdn_add_rmsnorm")
-    if h is None and o.data_ptr() != x.data_ptr():
+    if h is None and (o.data_ptr() != x.data_ptr() or rows == 0):
         h = x
     return o, h
 

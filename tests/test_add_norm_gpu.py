@@ -183,3 +183,5 @@ def test_in_place_without_a_residual_keeps_no_h():
     assert o is xx and h is kept and torch.equal(h, x) and torch.equal(o, want)
     with pytest.raises(api.GdnError):
         api.gdn_add_rmsnorm(x, x, w, o=x, h=x)
+    e = torch.empty(0, 256, device="cuda")
+    assert api.gdn_add_rmsnorm(e, None, w)[1] is e
