@@ -113,3 +113,24 @@ def test_a_foreign_stream_object():
     got = CALLS["packed"](x, stream=Raw())
     torch.cuda.synchronize()
     assert same(got, want)
+
+
+@pytest.mark.parametrize("call", ["packed", "packed gradients", "norm gradients", "rotary"])
+def test_captured_on_a_forked_stream(call):
+    """A graph whose capture forks to the given stream: workspace and outputs come from the graph's own memory."""
+    f, x = CALLS[call], inputs(4)
+    want = f(x)
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        side.wait_stream(torch.cuda.current_stream())
+        out = f(x, stream=side)
+        torch.cuda.current_stream().wait_stream(side)
+    mine = [torch.full((1 << n,), 7, dtype=torch.uint8, device="cuda") for n in range(16, 26)]
+    for _ in range(2):
+        for t in tensors(out):
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert same(out, want)
+    assert all(bool((t == 7).all()) for t in mine)
