@@ -11,8 +11,8 @@
 // thread and vector, at most kVec vectors a thread), so everything is read once; several rows' blocks
 // share an SM, and their loads hide each other's row sums.  Products and sums are packed, two 32-bit values an
 // instruction: with single ones the SMs issue for half the time and more, and the passes take a fifth longer.
-// Measured, 16 bits: 32768 rows of 2048 with a residual 83 us (6.5 TB/s); 8191 rows of 5120 to 8 bits 50 us
-// (5.9 TB/s); 16384 rows of 4096 in the reverse mode 97 us (5.5 TB/s).
+// Measured, 16 bits: 32768 rows of 2048 with a residual 83 us (6.5 TB/s); 8191 rows of 5120 to 8 bits 53 us
+// (5.5 TB/s); 16384 rows of 4096 in the reverse mode 102 us (5.3 TB/s); 50 and 97 us in short runs.
 #include <cuda_fp8.h>
 #include <float.h>
 

@@ -27,12 +27,12 @@
 // runs beside its predecessor's back; warp 16 loads by TMA through a ring of stages, warps 17 to 19 issue the
 // products.  Full chunks' outputs leave by TMA.  Every wait is bounded; one that gives up records
 // GDN_ERR_TIMEOUT.
-// Measured, d = 128: 148 chains of 64 chunks 123 us, 1.9 us a chunk and SM, 5.0 TB/s of the 6.45 that a copy
+// Measured, d = 128: 148 chains of 64 chunks 124 us, 1.9 us a chunk and SM, 5.0 TB/s of the 6.45 that a copy
 // reaches.  No one unit bounds it: leaving out the outputs, V~'s arithmetic, P's decay, two of LOC's three
 // products or the trips to HBM shortens it by 11, 9, 5, 9 and 14%.  (The SMs' clock falls from 1.9 to 1.5 GHz
-// under a second of it.)  8 sequences of 4096 tokens, 32 heads: 230 us (256 chains on 148 SMs), their gradients
-// 691 us in three passes; 32768 tokens in 4 documents, 16 heads, cut: 175 us, of it 60 the first pass, 8 the
-// states between and 105 the second.
+// under a second of it.)  8 sequences of 4096 tokens, 32 heads: 227 us (256 chains on 148 SMs), their gradients
+// 700 us in three passes; 32768 tokens in 4 documents, 16 heads, cut: 177 us, of it 60 the first pass, 8 the
+// states between and 107 the second.  (Short runs; a second and more of load: 205 us for the last, 830 us the gradients.)
 #include <mutex>
 #include <type_traits>
 

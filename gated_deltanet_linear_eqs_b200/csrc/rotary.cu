@@ -166,8 +166,8 @@ cudaError_t launch(const RotaryArgs& a, bool keep, cudaStream_t st) {
     const int turned = INTER && VEC > 1 ? a.r / VEC : a.r / 2 / VEC;
     const int units = turned + (keep ? (a.d - a.r) / VEC : 0);
     const int heads = a.a[0].heads + a.a[1].heads;
-    // three times the blocks that fit the SMs at once walk over the tokens (32768 tokens of 18 heads of 128: 54.1 us;
-    // once 55.3 us, six times 55.2 us, a warp a token 56 us); few tokens: the heads go over several blocks, each of
+    // three times the blocks that fit the SMs at once walk over the tokens (32768 tokens of 18 heads of 128: 54 to 55 us;
+    // once 2% more, six times as much, a warp a token 4%); few tokens: the heads go over several blocks, each of
     // which computes the angles again
     const int blocks = a.T / kRotWarps + (a.T % kRotWarps != 0), fit = 148 * kRotBlocks;
     const int hpw = units < 32 ? 32 / units : 1;
