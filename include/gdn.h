@@ -500,7 +500,7 @@ int gdn_rotary_inv_freq(int rotary_dim, double base, int scaling, double factor,
  *
  * over rows of C values (zero-centred gain, as in gdn_gated_rmsnorm).  The sum is taken in fp32 and
  * the norm is of that sum; h, in dtype, is its rounding.  The sum of squares is fp32, too: a row that
- * passes its range (values around 1e19) has the norm infinity.
+ * passes its range (values around 1e19) gives zeros.
  *   x, residual, o, h [rows, C] in dtype (bf16 or fp32); w [C] fp32; residual NULL: h = x; h NULL: not
  *   written.  h may be x or residual (in place); o may be x, but not h.  C a multiple of 8 in 8..16384.
  *   0 <= rows < 2^31.
